@@ -51,6 +51,25 @@ class DecodeBwdArgs(ctypes.Structure):
 READOUT_BEFORE_WRITE, READOUT_AFTER_WRITE = 0, 1
 
 
+class PoolStruct(ctypes.Structure):
+    _fields_ = [('layers', c_i32), ('slots', c_i32), ('Hv', c_i32), ('Dk', c_i32), ('Dv', c_i32),
+                ('state_fmt', c_i32), ('block_v', c_i32), ('data', c_vp), ('scales', c_vp)]
+
+
+class PoolStepArgs(ctypes.Structure):
+    _fields_ = [('B', c_i32), ('T', c_i32), ('Hqk', c_i32), ('io_dtype', c_i32), ('layer', c_i32),
+                ('readout', c_i32), ('scale', c_f32), ('q_stride', c_i64), ('k_stride', c_i64),
+                ('v_stride', c_i64), ('slots', c_vp), ('slots_out', c_vp), ('lens', c_vp), ('q', c_vp),
+                ('k', c_vp), ('v', c_vp), ('g', c_vp), ('beta', c_vp), ('o', c_vp)]
+
+
+class BeamArgs(ctypes.Structure):
+    _fields_ = [('B', c_i32), ('W', c_i32), ('V', c_i32), ('K', c_i32), ('io_dtype', c_i32),
+                ('pad_token', c_i32), ('row_stride', c_i64), ('logits', c_vp), ('scores', c_vp),
+                ('finished', c_vp), ('out_scores', c_vp), ('parents', c_vp), ('tokens', c_vp),
+                ('workspace', c_vp), ('workspace_bytes', c_sz)]
+
+
 class SavedLayout(ctypes.Structure):
     _fields_ = [('num_slots', c_i64), ('off_state', c_i64), ('off_state_scale', c_i64),
                 ('off_w', c_i64), ('off_w_scale', c_i64), ('off_x', c_i64), ('off_anchor', c_i64),
@@ -86,7 +105,15 @@ def load_library():
                        ('gdn_qdq_state', [c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_i32,
                                           c_i32, c_vp]),
                        ('gdn_decode_fwd', [ctypes.POINTER(DecodeArgs), c_vp]),
-                       ('gdn_decode_bwd', [ctypes.POINTER(DecodeBwdArgs), c_vp])):
+                       ('gdn_decode_bwd', [ctypes.POINTER(DecodeBwdArgs), c_vp]),
+                       ('gdn_pool_write', [ctypes.POINTER(PoolStruct), c_i32, c_vp, c_i32, c_vp, c_vp]),
+                       ('gdn_pool_read', [ctypes.POINTER(PoolStruct), c_i32, c_vp, c_i32, c_vp, c_vp]),
+                       ('gdn_pool_copy', [ctypes.POINTER(PoolStruct), c_vp, c_vp, c_i32, c_vp]),
+                       ('gdn_pool_reorder', [ctypes.POINTER(PoolStruct), c_vp, c_vp, c_i32, c_i32,
+                                             c_vp]),
+                       ('gdn_pool_step', [ctypes.POINTER(PoolStruct), ctypes.POINTER(PoolStepArgs),
+                                          c_vp]),
+                       ('gdn_beam_select', [ctypes.POINTER(BeamArgs), c_vp])):
         f = getattr(lib, name)
         f.argtypes = argt
         f.restype = c_i32
@@ -104,6 +131,8 @@ def load_library():
     lib.gdn_decode_saved_bytes.restype = c_sz
     lib.gdn_decode_bwd_workspace_bytes.argtypes = [ctypes.POINTER(DecodeBwdArgs)]
     lib.gdn_decode_bwd_workspace_bytes.restype = c_sz
+    lib.gdn_beam_workspace_bytes.argtypes = [ctypes.POINTER(BeamArgs)]
+    lib.gdn_beam_workspace_bytes.restype = c_sz
     _LIB = lib
     return lib
 
@@ -120,6 +149,7 @@ def _check(status):
 
 
 DEVERR_LDS_WAIT, DEVERR_FLAG_WAIT, DEVERR_SAVED_STAMP, DEVERR_P_RANGE = 1, 2, 4, 8
+DEVERR_POOL_SLOT = 16
 
 
 def fwd_schedule(args, cus=0):
@@ -480,3 +510,263 @@ def gdn_prefill_decode_bwd(q, k, v, g, beta, saved, do, dht=None, scale=None, h0
     else:
         out['dh0'] = dh_mid
     return out
+
+
+# ----------------------------------------------------------- state pool, beams
+# These calls are made once per layer and token: each checks its tensors'
+# types, shapes and layout (an error raises before anything is launched) and
+# is otherwise one library call.
+def _need(t, name, dtype, shape, dev):
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f'{name}: {str(dtype)[6:]} {list(shape)} on {dev}, contiguous; got '
+                         f'{str(t.dtype)[6:]} {list(t.shape)} on {t.device}'
+                         f'{"" if t.is_contiguous() else ", not contiguous"}')
+
+
+def _launch(fn, dev, *args):
+    """fn(*args, stream) on dev, its current stream and as the current device."""
+    if dev.type != 'cuda':
+        raise ValueError(f'tensors must be on a GPU, not on {dev}')
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        _check(status)
+
+
+def _token_stride(t, name, shape, dtype, dev):
+    """Elements between consecutive tokens of t [B, T, H, D] whose heads are
+    contiguous (a view of a wider projection is fine)."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        raise ValueError(f'{name}: {str(dtype)[6:]} {list(shape)} on {dev}; got '
+                         f'{str(t.dtype)[6:]} {list(t.shape)} on {t.device}')
+    sb, st, sh, sd = t.stride()
+    B, T, H, D = shape
+    ts = st if T > 1 else sb
+    if t.numel() and (sd != 1 or (H > 1 and sh != D) or (T > 1 and B > 1 and sb != T * st) or
+                      (B * T > 1 and ts < H * D)):
+        raise ValueError(f'{name}: heads of a token must be contiguous and all B * T tokens evenly '
+                         f'spaced; got strides {t.stride()} for shape {list(shape)}')
+    return ts if B * T > 1 else 0
+
+
+class StatePool:
+    """Pages of recurrent states: slots of [Hv, Dk, Dv] states for `layers`
+    layers, stored value-major as codes and tile scales (state_fmt QDQ_E4M3 or
+    QDQ_INT8) or as FP32 (QDQ_OFF); see gdn_pool in include/gdn.h. A new pool
+    holds zero states.
+
+    data [layers, slots, Hv, Dv, Dk] (float8_e4m3fn, int8 or float32) and
+    scales [layers, slots, Hv, Dv / block_v] (float32, or None) are ordinary
+    tensors; the pool only refers to them."""
+
+    def __init__(self, layers, slots, Hv, Dk, Dv, state_fmt=QDQ_OFF, block_v=64, device='cuda'):
+        dev = torch.device(device)
+        if state_fmt not in self._DTYPES:
+            raise ValueError(f'state_fmt {state_fmt}: use 0 off, 1 E4M3, 2 INT8')
+        if state_fmt != QDQ_OFF and (block_v < 1 or Dv % block_v):
+            raise ValueError(f'block_v {block_v} does not divide Dv {Dv}')
+        data = torch.zeros(layers, slots, Hv, Dv, Dk, dtype=self._DTYPES[state_fmt], device=dev)
+        scales = None
+        if state_fmt != QDQ_OFF:
+            scales = torch.full((layers, slots, Hv, Dv // block_v), 2.0 ** -126, device=dev)
+        self._bind(data, scales, state_fmt, block_v)
+
+    _DTYPES = {QDQ_OFF: torch.float32, QDQ_E4M3: torch.float8_e4m3fn, QDQ_INT8: torch.int8}
+
+    @classmethod
+    def from_tensors(cls, data, scales, state_fmt=QDQ_OFF, block_v=64):
+        """A pool on existing tensors (shared, not copied)."""
+        pool = cls.__new__(cls)
+        pool._bind(data, scales, state_fmt, block_v)
+        return pool
+
+    def _bind(self, data, scales, state_fmt, block_v):
+        if state_fmt not in self._DTYPES or data.dtype is not self._DTYPES[state_fmt]:
+            raise ValueError(f'pool data of {data.dtype} for state_fmt {state_fmt}')
+        if data.dim() != 5 or not data.is_contiguous():
+            raise ValueError('pool data: [layers, slots, Hv, Dv, Dk], contiguous')
+        L, S, Hv, Dv, Dk = data.shape
+        if state_fmt == QDQ_OFF:
+            if scales is not None:
+                raise ValueError('an FP32 pool has no scales')
+        else:
+            if block_v < 1 or Dv % block_v:
+                raise ValueError(f'block_v {block_v} does not divide Dv {Dv}')
+            if scales is None:
+                raise ValueError('scales is None')
+            _need(scales, 'scales', torch.float32, (L, S, Hv, Dv // block_v), data.device)
+        self.data, self.scales = data, scales
+        self.layers, self.slots, self.Hv, self.Dk, self.Dv = L, S, Hv, Dk, Dv
+        self.state_fmt, self.block_v, self.device = state_fmt, block_v, data.device
+        self._struct = PoolStruct(L, S, Hv, Dk, Dv, state_fmt, block_v, data.data_ptr(),
+                                  None if scales is None else scales.data_ptr())
+        self._ref = ctypes.byref(self._struct)
+
+
+def gdn_pool_write(pool, layer, slots, states):
+    """FP32 states [n, Hv, Dk, Dv] (a prefill's ht) into `slots` (int32 [n])
+    of a layer, through the pool's quantizer (bit-exact to gdn_qdq_state).
+    Slot -1 skips an entry; a slot named twice, or outside the pool, is left
+    as it was and raises DEVERR_POOL_SLOT in device_errors()."""
+    n = slots.shape[0]
+    _need(slots, 'slots', torch.int32, (n,), pool.device)
+    _need(states, 'states', torch.float32, (n, pool.Hv, pool.Dk, pool.Dv), pool.device)
+    _launch(load_library().gdn_pool_write, pool.device, pool._ref, layer, slots.data_ptr(), n,
+            states.data_ptr())
+
+
+def gdn_pool_read(pool, layer, slots, out=None):
+    """FP32 states [n, Hv, Dk, Dv] of `slots` (int32 [n]) of a layer (the h0 of
+    a chunk prefill). Slot -1 gives the zero state, a slot outside the pool
+    NaN (and DEVERR_POOL_SLOT)."""
+    n = slots.shape[0]
+    _need(slots, 'slots', torch.int32, (n,), pool.device)
+    shape = (n, pool.Hv, pool.Dk, pool.Dv)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=pool.device)
+    else:
+        _need(out, 'out', torch.float32, shape, pool.device)
+    _launch(load_library().gdn_pool_read, pool.device, pool._ref, layer, slots.data_ptr(), n,
+            out.data_ptr())
+    return out
+
+
+def gdn_pool_copy(pool, src, dst):
+    """page[dst[m]] <- page[src[m]] in every layer (int32 [n] each): forks,
+    moves, compaction. src -1 clears the page, dst -1 skips the entry. No
+    destination may be named twice or be another entry's source (such pages
+    are left as they were, with DEVERR_POOL_SLOT)."""
+    n = src.shape[0]
+    _need(src, 'src', torch.int32, (n,), pool.device)
+    _need(dst, 'dst', torch.int32, (n,), pool.device)
+    _launch(load_library().gdn_pool_copy, pool.device, pool._ref, src.data_ptr(), dst.data_ptr(), n)
+
+
+def gdn_pool_reorder(pool, slots, parents):
+    """In place and in every layer, page[slots[g, w]] <- the page that
+    slots[g, parents[g, w]] held (int32 [groups, width] each, width up to 32):
+    the beams of each group take their parents' states. Parent -1 leaves a
+    page alone; slot -1 is a beam that is not there."""
+    if slots.dim() != 2:
+        raise ValueError(f'slots: [groups, width]; got {list(slots.shape)}')
+    _need(slots, 'slots', torch.int32, slots.shape, pool.device)
+    _need(parents, 'parents', torch.int32, slots.shape, pool.device)
+    _launch(load_library().gdn_pool_reorder, pool.device, pool._ref, slots.data_ptr(),
+            parents.data_ptr(), slots.shape[0], slots.shape[1])
+
+
+def gdn_pool_step(pool, layer, slots, q, k, v, g, beta, scale=None, slots_out=None, lens=None,
+                  readout=READOUT_BEFORE_WRITE, out=None):
+    """Recurrent steps of B sequences on their pages: tokens 0 .. lens[b] - 1
+    (lens int32 [B], or all T) of q, k [B, T, Hqk, Dk], v [B, T, Hv, Dv] (bf16
+    or FP32; token strides are free) and g, beta [B, T, Hv] FP32, from the
+    states in `slots` (int32 [B], -1: no sequence) to `slots_out` (default:
+    the same; -1: not kept; parents may be shared, a page written may not be
+    named by another sequence). Returns o [B, T, Hv, Dv] in q's type; rows
+    past lens and of absent sequences are not written (zero in a new o)."""
+    dev, shape = pool.device, q.shape
+    if len(shape) != 4:
+        raise ValueError(f'q: [B, T, Hqk, Dk]; got {list(shape)}')
+    B, T, Hqk, _ = shape
+    dt, Hv = q.dtype, pool.Hv
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f'q: bfloat16 or float32, not {dt}')
+    a = PoolStepArgs(B=B, T=T, Hqk=Hqk, io_dtype=GDN_BF16 if dt is torch.bfloat16 else GDN_F32,
+                     layer=layer, readout=readout, scale=pool.Dk ** -0.5 if scale is None else scale)
+    shape_qk, shape_v, shape_g = (B, T, Hqk, pool.Dk), (B, T, Hv, pool.Dv), (B, T, Hv)
+    a.q_stride = _token_stride(q, 'q', shape_qk, dt, dev)
+    a.k_stride = _token_stride(k, 'k', shape_qk, dt, dev)
+    a.v_stride = _token_stride(v, 'v', shape_v, dt, dev)
+    _need(g, 'g', torch.float32, shape_g, dev)
+    _need(beta, 'beta', torch.float32, shape_g, dev)
+    _need(slots, 'slots', torch.int32, (B,), dev)
+    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
+    a.g, a.beta, a.slots = g.data_ptr(), beta.data_ptr(), slots.data_ptr()
+    if slots_out is not None:
+        _need(slots_out, 'slots_out', torch.int32, (B,), dev)
+        a.slots_out = slots_out.data_ptr()
+    if lens is not None:
+        _need(lens, 'lens', torch.int32, (B,), dev)
+        a.lens = lens.data_ptr()
+    if out is None:
+        out = torch.zeros(shape_v, dtype=dt, device=dev)
+    else:
+        _need(out, 'out', dt, shape_v, dev)
+    a.o = out.data_ptr()
+    _launch(load_library().gdn_pool_step, dev, pool._ref, ctypes.byref(a))
+    return out
+
+
+def gdn_pool_prefill(pool, layer, slots, q, k, v, g, beta, scale=None, cu_seqlens=None, w_fmt=QDQ_OFF,
+                     resume=True):
+    """Chunk prefill of the sequences in `slots` (int32 [N]): gdn_chunk_fwd from
+    the states of their pages (resume=False: from zero states, the pages are
+    not read), its final states written to the pages. Arguments as
+    gdn_chunk_fwd; the state site uses the pool's format and tiles. Returns
+    o. The final state passes the quantizer once, as in
+    gdn_prefill_decode_fwd."""
+    h0 = gdn_pool_read(pool, layer, slots) if resume else None
+    o, ht, _ = gdn_chunk_fwd(q, k, v, g, beta, scale, h0, cu_seqlens, pool.state_fmt, w_fmt,
+                             pool.block_v)
+    gdn_pool_write(pool, layer, slots, ht)
+    return o
+
+
+def gdn_beam_select(logits, scores, num_select=None, finished=None, pad_token=0):
+    """The num_select (default W, at most 64) best continuations of each of B
+    requests of W beams (W up to 32): logits [B, W, V] (bf16 or FP32, rows
+    evenly spaced), scores [B, W] FP32 sums of log-probabilities, finished
+    [B, W] bool or uint8 (such a beam offers pad_token at no cost). Returns
+    (scores [B, K] FP32, parents [B, K] int32, tokens [B, K] int32), best
+    first, ties to the lower beam then token; see gdn_beam_select in
+    include/gdn.h for masked, NaN and exhausted rows."""
+    if logits.dim() != 3:
+        raise ValueError(f'logits: [B, W, V]; got {list(logits.shape)}')
+    B, W, V = logits.shape
+    K = W if num_select is None else num_select
+    dev, dt = logits.device, logits.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f'logits: bfloat16 or float32, not {dt}')
+    sb, sw, sv = logits.stride()
+    rs = sw if W > 1 else sb
+    if logits.numel() and ((sv != 1 and V > 1) or (W > 1 and B > 1 and sb != W * sw) or
+                           (B * W > 1 and rs < V)):
+        raise ValueError(f'logits: rows must be contiguous and evenly spaced; got strides '
+                         f'{logits.stride()}')
+    _need(scores, 'scores', torch.float32, (B, W), dev)
+    a = BeamArgs(B=B, W=W, V=V, K=K, io_dtype=GDN_BF16 if dt is torch.bfloat16 else GDN_F32,
+                 pad_token=pad_token, row_stride=rs if B * W > 1 else 0, logits=logits.data_ptr(),
+                 scores=scores.data_ptr())
+    if finished is not None:
+        _need(finished, 'finished', torch.bool if finished.dtype is torch.bool else torch.uint8,
+              (B, W), dev)
+        a.finished = finished.data_ptr()
+    lib = load_library()
+    nbytes = lib.gdn_beam_workspace_bytes(ctypes.byref(a))
+    if nbytes == 0 and B:
+        _check(lib.gdn_beam_select(ctypes.byref(a), None))      # reports the argument error
+    out = torch.empty(B, K, dtype=torch.float32, device=dev)
+    parents = torch.empty(B, K, dtype=torch.int32, device=dev)
+    tokens = torch.empty(B, K, dtype=torch.int32, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    a.out_scores, a.parents, a.tokens = out.data_ptr(), parents.data_ptr(), tokens.data_ptr()
+    a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+    _launch(lib.gdn_beam_select, dev, ctypes.byref(a))
+    return out, parents, tokens
+
+
+def gdn_beam_advance(pool, slots, logits, scores, finished=None, pad_token=0):
+    """One step of beam search over the states of a pool: gdn_beam_select of W
+    continuations of each request, then gdn_pool_reorder of the beams' pages
+    (slots int32 [B, W]) to their parents'. Returns (scores, parents,
+    tokens) as gdn_beam_select does."""
+    if logits.dim() != 3 or tuple(slots.shape) != tuple(logits.shape[:2]):
+        raise ValueError(f'slots: [B, W] of logits [B, W, V]; got {list(slots.shape)} and '
+                         f'{list(logits.shape)}')
+    _need(slots, 'slots', torch.int32, slots.shape, pool.device)
+    out, parents, tokens = gdn_beam_select(logits, scores, None, finished, pad_token)
+    gdn_pool_reorder(pool, slots, parents)
+    return out, parents, tokens

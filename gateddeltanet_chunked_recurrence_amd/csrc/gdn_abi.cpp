@@ -751,6 +751,108 @@ gdn::DecodeConfig decode_config(const gdn_decode_args* a) {
   return c;
 }
 
+// ------------------------------------------------------------- state pool
+gdn_status check_pool(const gdn_pool* p, const char* what) {
+  if (!p) return fail(GDN_E_INVALID, "%s: pool is NULL", what);
+  if (!valid_fmt(p->state_fmt))
+    return fail(GDN_E_UNSUPPORTED, "%s: unknown pool format %d: use 0 off, 1 E4M3, 2 INT8", what, p->state_fmt);
+  if (p->layers < 1 || p->layers > 65535 || p->slots < 1 || p->Hv < 1)
+    return fail(GDN_E_INVALID, "%s: bad pool sizes layers=%d slots=%d Hv=%d", what, p->layers, p->slots, p->Hv);
+  if (p->Hv > 65535) return fail(GDN_E_UNSUPPORTED, "%s: Hv %d exceeds 65535", what, p->Hv);
+  if (p->Dk != 64 && p->Dk != 128) return fail(GDN_E_UNSUPPORTED, "%s: Dk %d: supported 64, 128", what, p->Dk);
+  if (p->Dv != 64 && p->Dv != 128 && p->Dv != 256)
+    return fail(GDN_E_UNSUPPORTED, "%s: Dv %d: supported 64, 128, 256", what, p->Dv);
+  if (p->state_fmt != GDN_QDQ_OFF) {
+    const int32_t bv = p->block_v;
+    if (bv != 16 && bv != 32 && bv != 64 && bv != 128 && bv != 256)
+      return fail(GDN_E_UNSUPPORTED, "%s: block_v %d: supported 16, 32, 64, 128, 256", what, bv);
+    if (p->Dv % bv != 0) return fail(GDN_E_INVALID, "%s: block_v %d does not divide Dv %d", what, bv, p->Dv);
+    if (!p->scales) return fail(GDN_E_INVALID, "%s: pool scales is NULL", what);
+    if (!aligned16(p->scales)) return fail(GDN_E_INVALID, "%s: pool scales is not 16-byte aligned", what);
+  }
+  if (!p->data) return fail(GDN_E_INVALID, "%s: pool data is NULL", what);
+  if (!aligned16(p->data)) return fail(GDN_E_INVALID, "%s: pool data is not 16-byte aligned", what);
+  return GDN_OK;
+}
+
+gdn_status check_entries(const char* what, int32_t n, const void* p, const char* name) {
+  if (n < 0) return fail(GDN_E_INVALID, "%s: %d entries", what, n);
+  if (n > 65535) return fail(GDN_E_UNSUPPORTED, "%s: %d entries: at most 65535", what, n);
+  if (n && !p) return fail(GDN_E_INVALID, "%s: %s is NULL", what, name);
+  if (p && !aligned16(p)) return fail(GDN_E_INVALID, "%s: %s is not 16-byte aligned", what, name);
+  return GDN_OK;
+}
+
+gdn_status check_layer(const char* what, const gdn_pool* p, int32_t layer) {
+  if (layer < 0 || layer >= p->layers)
+    return fail(GDN_E_INVALID, "%s: layer %d of %d", what, layer, p->layers);
+  return GDN_OK;
+}
+
+gdn::PoolRef pool_ref(const gdn_pool* p) {
+  gdn::PoolRef r{};
+  const bool q = p->state_fmt != GDN_QDQ_OFF;
+  r.data = static_cast<uint8_t*>(p->data);
+  r.scales = q ? p->scales : nullptr;
+  r.err = err_word();
+  r.page = (int64_t)p->Hv * p->Dk * p->Dv * (q ? 1 : 4);
+  r.tiles = q ? p->Hv * (p->Dv / p->block_v) : 0;
+  r.layers = p->layers;
+  r.slots = p->slots;
+  r.Hv = p->Hv;
+  r.Dk = p->Dk;
+  r.Dv = p->Dv;
+  r.fmt = p->state_fmt;
+  r.block_v = q ? p->block_v : p->Dv;
+  return r;
+}
+
+gdn_status no_err_word() {
+  return fail(GDN_E_HIP, "device error word unavailable on the current device");
+}
+
+gdn_status check_beam(const gdn_beam_args* a) {
+  if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
+  if (a->B < 0 || a->B > 65535 || a->V < 1)
+    return fail(GDN_E_INVALID, "gdn_beam_select: bad sizes B=%d V=%d", a->B, a->V);
+  if (a->W < 1 || a->W > gdn::kBeamMaxW)
+    return fail(GDN_E_UNSUPPORTED, "gdn_beam_select: %d beams: 1 to %d", a->W, gdn::kBeamMaxW);
+  if (a->K < 1 || a->K > gdn::kBeamMaxK)
+    return fail(GDN_E_UNSUPPORTED, "gdn_beam_select: K %d: 1 to %d", a->K, gdn::kBeamMaxK);
+  if (a->V > (1 << 30)) return fail(GDN_E_UNSUPPORTED, "gdn_beam_select: V %d exceeds 2^30", a->V);
+  if (a->io_dtype != GDN_BF16 && a->io_dtype != GDN_F32)
+    return fail(GDN_E_INVALID, "io_dtype %d: use 0 bf16 or 1 f32", a->io_dtype);
+  if (a->row_stride != 0 && a->row_stride < a->V)
+    return fail(GDN_E_INVALID, "gdn_beam_select: row_stride %lld below V %d", (long long)a->row_stride, a->V);
+  return GDN_OK;
+}
+
+gdn::BeamArgs beam_args(const gdn_beam_args* a) {
+  gdn::BeamArgs k{};
+  k.logits = a->logits;
+  k.scores = a->scores;
+  k.finished = a->finished;
+  k.out_scores = a->out_scores;
+  k.parents = a->parents;
+  k.tokens = a->tokens;
+  k.ws = a->workspace;
+  k.row_stride = a->row_stride ? a->row_stride : a->V;
+  k.B = a->B;
+  k.W = a->W;
+  k.V = a->V;
+  k.K = a->K;
+  k.pad_token = a->pad_token;
+  k.f32 = a->io_dtype == GDN_F32;
+  gdn::beam_plan(k);
+  return k;
+}
+
+gdn_status check_beam_parts(const gdn::BeamArgs& k) {
+  if ((int64_t)k.B * k.W * k.splits > INT32_MAX)
+    return fail(GDN_E_UNSUPPORTED, "gdn_beam_select: B * W * V is too large");
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -989,6 +1091,157 @@ gdn_status gdn_qdq_state(const float* x, float* y, float* scales, uint8_t* codes
   return hip_status(gdn::launch_qdq_state(x, y, scales, codes, n_states, Dk, Dv, block_v, fmt,
                                           static_cast<hipStream_t>(stream)),
                     "gdn_qdq_state launch");
+}
+
+gdn_status gdn_pool_write(const gdn_pool* pool, int32_t layer, const int32_t* slots, int32_t n,
+                          const float* states, void* stream) {
+  const char* what = "gdn_pool_write";
+  gdn_status s = check_pool(pool, what);
+  if (s != GDN_OK || (s = check_layer(what, pool, layer)) != GDN_OK) return s;
+  if ((s = check_entries(what, n, slots, "slots")) != GDN_OK) return s;
+  if ((s = check_entries(what, n, states, "states")) != GDN_OK) return s;
+  if ((int64_t)n * pool->Hv * (pool->Dv / 32) * 2 > INT32_MAX)
+    return fail(GDN_E_UNSUPPORTED, "%s: n * Hv * Dv exceeds 2^35", what);
+  if (n == 0) return GDN_OK;
+  const gdn::PoolRef r = pool_ref(pool);
+  if (!r.err) return no_err_word();
+  return hip_status(gdn::launch_pool_write(r, layer, slots, n, states, static_cast<hipStream_t>(stream)),
+                    "gdn_pool_write launch");
+}
+
+gdn_status gdn_pool_read(const gdn_pool* pool, int32_t layer, const int32_t* slots, int32_t n,
+                         float* states, void* stream) {
+  const char* what = "gdn_pool_read";
+  gdn_status s = check_pool(pool, what);
+  if (s != GDN_OK || (s = check_layer(what, pool, layer)) != GDN_OK) return s;
+  if ((s = check_entries(what, n, slots, "slots")) != GDN_OK) return s;
+  if ((s = check_entries(what, n, states, "states")) != GDN_OK) return s;
+  if ((int64_t)n * pool->Hv * (pool->Dv / 32) * 2 > INT32_MAX)
+    return fail(GDN_E_UNSUPPORTED, "%s: n * Hv * Dv exceeds 2^35", what);
+  if (n == 0) return GDN_OK;
+  const gdn::PoolRef r = pool_ref(pool);
+  if (!r.err) return no_err_word();
+  return hip_status(gdn::launch_pool_read(r, layer, slots, n, states, static_cast<hipStream_t>(stream)),
+                    "gdn_pool_read launch");
+}
+
+gdn_status gdn_pool_copy(const gdn_pool* pool, const int32_t* src, const int32_t* dst, int32_t n,
+                         void* stream) {
+  const char* what = "gdn_pool_copy";
+  gdn_status s = check_pool(pool, what);
+  if (s != GDN_OK || (s = check_entries(what, n, src, "src")) != GDN_OK) return s;
+  if ((s = check_entries(what, n, dst, "dst")) != GDN_OK) return s;
+  if (n == 0) return GDN_OK;
+  const gdn::PoolRef r = pool_ref(pool);
+  if (!r.err) return no_err_word();
+  return hip_status(gdn::launch_pool_copy(r, src, dst, n, static_cast<hipStream_t>(stream)),
+                    "gdn_pool_copy launch");
+}
+
+gdn_status gdn_pool_reorder(const gdn_pool* pool, const int32_t* slots, const int32_t* parents,
+                            int32_t groups, int32_t width, void* stream) {
+  const char* what = "gdn_pool_reorder";
+  gdn_status s = check_pool(pool, what);
+  if (s != GDN_OK) return s;
+  if (width < 1 || width > gdn::kBeamMaxW)
+    return fail(GDN_E_UNSUPPORTED, "%s: width %d: 1 to %d", what, width, gdn::kBeamMaxW);
+  if (groups < 0) return fail(GDN_E_INVALID, "%s: %d groups", what, groups);
+  if ((int64_t)groups * width > 65535)
+    return fail(GDN_E_UNSUPPORTED, "%s: groups * width = %lld: at most 65535", what, (long long)groups * width);
+  if ((s = check_entries(what, groups * width, slots, "slots")) != GDN_OK) return s;
+  if ((s = check_entries(what, groups * width, parents, "parents")) != GDN_OK) return s;
+  if (groups == 0) return GDN_OK;
+  const gdn::PoolRef r = pool_ref(pool);
+  if (!r.err) return no_err_word();
+  return hip_status(gdn::launch_pool_reorder(r, slots, parents, groups, width, static_cast<hipStream_t>(stream)),
+                    "gdn_pool_reorder launch");
+}
+
+gdn_status gdn_pool_step(const gdn_pool* pool, const gdn_pool_step_args* a, void* stream) {
+  const char* what = "gdn_pool_step";
+  gdn_status s = check_pool(pool, what);
+  if (s != GDN_OK) return s;
+  if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
+  if ((s = check_layer(what, pool, a->layer)) != GDN_OK) return s;
+  if (a->T < 0 || a->Hqk <= 0) return fail(GDN_E_INVALID, "%s: bad sizes T=%d Hqk=%d", what, a->T, a->Hqk);
+  if (pool->Hv % a->Hqk != 0)
+    return fail(GDN_E_INVALID, "%s: Hv (%d) must be a multiple of Hqk (%d)", what, pool->Hv, a->Hqk);
+  if (a->io_dtype != GDN_BF16 && a->io_dtype != GDN_F32)
+    return fail(GDN_E_INVALID, "io_dtype %d: use 0 bf16 or 1 f32", a->io_dtype);
+  if (a->readout != GDN_READOUT_BEFORE_WRITE && a->readout != GDN_READOUT_AFTER_WRITE)
+    return fail(GDN_E_INVALID, "%s: readout %d: use 0 before or 1 after the write", what, a->readout);
+  if (!std::isfinite(a->scale)) return fail(GDN_E_INVALID, "scale is not finite");
+  if ((s = check_entries(what, a->B, a->slots, "slots")) != GDN_OK) return s;
+  const bool any = a->B > 0 && a->T > 0;
+  const struct { const void* p; const char* name; bool required; } ptrs[] = {
+      {a->q, "q", any}, {a->k, "k", any}, {a->v, "v", any}, {a->g, "g", any}, {a->beta, "beta", any},
+      {a->o, "o", any}, {a->slots_out, "slots_out", false}, {a->lens, "lens", false}};
+  for (const auto& e : ptrs) {
+    if (e.required && !e.p) return fail(GDN_E_INVALID, "%s: %s is NULL", what, e.name);
+    if (e.p && !aligned16(e.p)) return fail(GDN_E_INVALID, "%s: %s is not 16-byte aligned", what, e.name);
+  }
+  const int64_t es = a->io_dtype == GDN_F32 ? 4 : 2;
+  const int64_t row_qk = (int64_t)a->Hqk * pool->Dk, row_v = (int64_t)pool->Hv * pool->Dv;
+  const struct { int64_t stride, row; const char* name; } strides[] = {
+      {a->q_stride, row_qk, "q"}, {a->k_stride, row_qk, "k"}, {a->v_stride, row_v, "v"}};
+  for (const auto& e : strides)
+    if (e.stride != 0 && (e.stride < e.row || e.stride * es % 16 != 0))
+      return fail(GDN_E_INVALID, "%s: %s_stride %lld: at least %lld and a multiple of 16 bytes", what, e.name,
+                  (long long)e.stride, (long long)e.row);
+  if ((int64_t)a->B * pool->Hv * (pool->Dv / 16) > INT32_MAX - 64)
+    return fail(GDN_E_UNSUPPORTED, "%s: B * Hv * Dv exceeds 2^35", what);
+  if (a->B == 0) return GDN_OK;
+  gdn::PoolStepArgs k{};
+  k.pool = pool_ref(pool);
+  if (!k.pool.err) return no_err_word();
+  k.slots = a->slots;
+  k.slots_out = a->slots_out;
+  k.lens = a->lens;
+  k.q = a->q;
+  k.k = a->k;
+  k.v = a->v;
+  k.g = a->g;
+  k.beta = a->beta;
+  k.o = a->o;
+  k.qs = a->q_stride ? a->q_stride : row_qk;
+  k.ks = a->k_stride ? a->k_stride : row_qk;
+  k.vs = a->v_stride ? a->v_stride : row_v;
+  k.layer_page = (int64_t)a->layer * pool->slots;
+  k.B = a->B;
+  k.T = a->T;
+  k.Hqk = a->Hqk;
+  k.readout = a->readout;
+  k.f32_io = a->io_dtype == GDN_F32;
+  k.scale = a->scale;
+  return hip_status(gdn::launch_pool_step(k, static_cast<hipStream_t>(stream)), "gdn_pool_step launch");
+}
+
+size_t gdn_beam_workspace_bytes(const gdn_beam_args* a) {
+  if (check_beam(a) != GDN_OK) return 0;
+  const gdn::BeamArgs k = beam_args(a);
+  if (check_beam_parts(k) != GDN_OK) return 0;
+  return (size_t)gdn::beam_workspace_bytes(k);
+}
+
+gdn_status gdn_beam_select(const gdn_beam_args* a, void* stream) {
+  gdn_status s = check_beam(a);
+  if (s != GDN_OK) return s;
+  const bool any = a->B > 0;
+  const struct { const void* p; const char* name; bool required; } ptrs[] = {
+      {a->logits, "logits", any},         {a->scores, "scores", any},   {a->finished, "finished", false},
+      {a->out_scores, "out_scores", any}, {a->parents, "parents", any}, {a->tokens, "tokens", any},
+      {a->workspace, "workspace", false}};
+  for (const auto& e : ptrs) {
+    if (e.required && !e.p) return fail(GDN_E_INVALID, "gdn_beam_select: %s is NULL", e.name);
+    if (e.p && !aligned16(e.p)) return fail(GDN_E_INVALID, "gdn_beam_select: %s is not 16-byte aligned", e.name);
+  }
+  if (!any) return GDN_OK;
+  const gdn::BeamArgs k = beam_args(a);
+  if ((s = check_beam_parts(k)) != GDN_OK) return s;
+  const size_t need = (size_t)gdn::beam_workspace_bytes(k);
+  if (!a->workspace || a->workspace_bytes < need)
+    return fail(GDN_E_WORKSPACE, "workspace of %zu bytes given, %zu needed", a->workspace_bytes, need);
+  return hip_status(gdn::launch_beam_select(k, static_cast<hipStream_t>(stream)), "gdn_beam_select launch");
 }
 
 }  // extern "C"

@@ -98,6 +98,7 @@ constexpr uint32_t kErrLdsWait = 1u;      // a bounded LDS-counter wait gave up
 constexpr uint32_t kErrFlagWait = 2u;     // a bounded wait on another workgroup gave up
 constexpr uint32_t kErrSavedStamp = 4u;   // saved buffer written under another policy or shape
 constexpr uint32_t kErrPRange = 8u;       // a masked Q K^T entry beyond the fp16 range
+constexpr uint32_t kErrPoolSlot = 16u;    // a pool slot out of range, or written while named twice
 
 // The policy and shape a forward wrote its saved buffer under; the backward
 // compares it with its own arguments on the device.
@@ -262,6 +263,64 @@ struct DecodeConfig {
 inline int decode_slabs_per_group(int state_fmt, int block_v) {
   return state_fmt != 0 && block_v > 64 ? block_v / 64 : 1;
 }
+
+// State pool (gdn_pool.hip, gdn_pool_step.hip): pages [layers, slots] of Hv
+// value-major states, codes [Hv, Dv, Dk] with one FP32 scale per block_v
+// value rows, or FP32 states [Hv, Dv, Dk].
+struct PoolRef {
+  uint8_t* data;
+  float* scales;              // NULL with the format off
+  uint32_t* err;              // sticky device error flags
+  int64_t page;               // bytes of one page's data
+  int32_t tiles;              // scales of one page (0 with the format off)
+  int32_t layers, slots, Hv, Dk, Dv, fmt, block_v;
+};
+hipError_t launch_pool_write(const PoolRef& p, int layer, const int32_t* slots, int n,
+                             const float* states, hipStream_t s);
+hipError_t launch_pool_read(const PoolRef& p, int layer, const int32_t* slots, int n, float* states,
+                            hipStream_t s);
+hipError_t launch_pool_copy(const PoolRef& p, const int32_t* src, const int32_t* dst, int n,
+                            hipStream_t s);
+hipError_t launch_pool_reorder(const PoolRef& p, const int32_t* slots, const int32_t* parents,
+                               int groups, int width, hipStream_t s);
+
+struct PoolStepArgs {
+  PoolRef pool;
+  const int32_t* slots;
+  const int32_t* slots_out;   // nullable (in place)
+  const int32_t* lens;        // nullable (T tokens each)
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  void* o;
+  int64_t qs, ks, vs;         // elements between tokens of q, k, v
+  int64_t layer_page;         // first page of the layer
+  int32_t B, T, Hqk, readout, f32_io;
+  float scale;
+};
+hipError_t launch_pool_step(const PoolStepArgs& a, hipStream_t s);
+
+// Beam selection (gdn_beam.hip).
+constexpr int kBeamMaxW = 32, kBeamMaxK = 64;
+struct BeamArgs {
+  const void* logits;
+  const float* scores;
+  const uint8_t* finished;    // nullable
+  float* out_scores;
+  int32_t* parents;
+  int32_t* tokens;
+  void* ws;
+  int64_t row_stride;
+  int32_t B, W, V, K, pad_token, f32;
+  int32_t vecs;               // 16-byte vectors per thread of a split (1, 2, 4 or 8)
+  int32_t splits;             // workgroups per row
+};
+// Sets vecs and splits, by the sizes alone.
+void beam_plan(BeamArgs& a);
+int64_t beam_workspace_bytes(const BeamArgs& a);
+hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
 
 hipError_t launch_decode_fwd(const DecodeConfig& c, const DecodeKernelArgs& a, hipStream_t s);
 hipError_t launch_decode_bwd(const DecodeConfig& c, const DecodeKernelArgs& a, hipStream_t s);

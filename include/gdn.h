@@ -384,6 +384,124 @@ typedef struct {
 size_t gdn_decode_bwd_workspace_bytes(const gdn_decode_bwd_args* a);
 gdn_status gdn_decode_bwd(const gdn_decode_bwd_args* a, void* stream);
 
+/* ------------------------------------------------------------------------
+ * State pool: the recurrent states of many sequences in slots of one cache,
+ * as a server keeps them, with the codes and tile scales of the state
+ * quantizer really stored in one byte (E4M3FN bit patterns or int8), or FP32
+ * states with the format off. A page is one slot of one layer: Hv states,
+ * VALUE-major, data [layers, slots, Hv, Dv, Dk] (Dk contiguous: a scale tile
+ * of block_v values and Dk keys is one contiguous block, and the step's sums
+ * over keys run along rows), scales [layers, slots, Hv, Dv / block_v] FP32 (NULL
+ * with the format off). The caller allocates both. A page of zero bytes with
+ * scales 2^-126 is the zero state.
+ *
+ * Slots are device arrays of int32 (16-byte aligned like every pointer). In
+ * all calls slot -1 means "no sequence here": nothing is read or written for
+ * it, so batches of a fixed size may be padded (and captured into a graph). A
+ * slot outside [-1, slots), or one that a call would write while another
+ * entry of the same call reads or writes it, is refused on the device: the
+ * pages stay as they were, outputs of the refused entries are NaN, and
+ * GDN_DEVERR_POOL_SLOT is set. States must be finite.
+ *
+ * Sizes: Dk in {64, 128}; Dv in {64, 128, 256}; block_v 16, 32, 64, 128 or
+ * 256 dividing Dv (ignored when OFF); at most 65535 entries, layers and groups per
+ * call. The calls allocate nothing, need no workspace and may be captured
+ * into HIP graphs. Calls that touch the same pages must be ordered by the
+ * caller (one stream, or events). */
+typedef struct {
+  int32_t layers, slots, Hv, Dk, Dv;
+  int32_t state_fmt;           /* gdn_qdq_fmt                                 */
+  int32_t block_v;
+  void* data;
+  float* scales;
+} gdn_pool;
+
+/* states [n, Hv, Dk, Dv] FP32 (the layout of h0 and ht) -> pages of `layer`:
+ * the state as written, QDQ codes and scales bit-exact to gdn_qdq_state. */
+gdn_status gdn_pool_write(const gdn_pool* pool, int32_t layer, const int32_t* slots, int32_t n,
+                          const float* states, void* stream);
+
+/* Pages of `layer` -> states [n, Hv, Dk, Dv] FP32, code times scale. Slot -1
+ * gives the zero state; a slot may be named any number of times. */
+gdn_status gdn_pool_read(const gdn_pool* pool, int32_t layer, const int32_t* slots, int32_t n,
+                         float* states, void* stream);
+
+/* page[dst[m]] <- page[src[m]] in every layer: forks (one src many times),
+ * moves, compaction. src -1 clears the page (zero states); dst -1 skips the
+ * entry, src == dst does nothing. Destinations must be distinct and none may
+ * be a source of another entry. */
+gdn_status gdn_pool_copy(const gdn_pool* pool, const int32_t* src, const int32_t* dst, int32_t n,
+                         void* stream);
+
+/* Reordering of beams, in place and in every layer: within each of `groups`
+ * groups of `width` (1 to 32) beams, page[slots[g, w]] <- the page that
+ * slots[g, parents[g, w]] held before the call, for all w at once. Parent -1
+ * leaves the beam's page as it is, slot -1 is a beam that is not there (it
+ * may not be a parent). */
+gdn_status gdn_pool_reorder(const gdn_pool* pool, const int32_t* slots, const int32_t* parents,
+                            int32_t groups, int32_t width, void* stream);
+
+/* Recurrent step: tokens 0 .. lens[b] - 1 of each of B sequences from the
+ * states in `slots`, as gdn_decode_fwd computes them (the state is a written
+ * one already: there is no first write), the last written state to
+ * `slots_out`. FP32 arithmetic. */
+typedef struct {
+  int32_t B, T, Hqk;           /* T tokens per row of the batch               */
+  int32_t io_dtype;            /* gdn_dtype of q, k, v and o                  */
+  int32_t layer;
+  int32_t readout;             /* gdn_readout                                 */
+  float scale;
+  int64_t q_stride, k_stride, v_stride; /* elements between consecutive tokens
+                                  of q, k, v (of all B * T, batch-major); 0:
+                                  contiguous. Rows start 16-byte aligned, so
+                                  views into one projection's output can be
+                                  passed as they are                          */
+  const int32_t* slots;        /* [B] state read                              */
+  const int32_t* slots_out;    /* [B] state written, or NULL (= slots); -1: the
+                                  state is not kept. With slots_out a parent
+                                  may be read by several sequences            */
+  const int32_t* lens;         /* [B] tokens of each sequence (clamped to
+                                  [0, T]), or NULL (= T). With 0 the state is
+                                  only copied to slots_out                    */
+  const void* q;               /* [B, T, Hqk, Dk]                             */
+  const void* k;               /* [B, T, Hqk, Dk]                             */
+  const void* v;               /* [B, T, Hv, Dv]                              */
+  const float* g;              /* [B, T, Hv] log-gate                         */
+  const float* beta;           /* [B, T, Hv]                                  */
+  void* o;                     /* out [B, T, Hv, Dv]; rows past lens, and of
+                                  slot -1, are left as they were              */
+} gdn_pool_step_args;
+gdn_status gdn_pool_step(const gdn_pool* pool, const gdn_pool_step_args* a, void* stream);
+
+/* Beam search's selection over beams and vocabulary, for B requests of W
+ * beams: with logp[b, w, t] = x - log sum exp x over the vocabulary and total =
+ * scores[b, w] + logp, the K best (w, t) of each request, best first; equal
+ * totals go to the lower beam, then the lower token. Totals are compared in
+ * 64 bits (two beams' totals seldom differ by much) and returned in FP32. A
+ * finished beam offers one candidate, pad_token with logp 0. Logits of -inf
+ * are masked and NaN counts as masked; +inf counts as the largest finite
+ * value. Candidates with total -inf are never chosen: where fewer than K
+ * are left, the rest of the row is score -inf, parent -1, token -1 (a parent
+ * that gdn_pool_reorder leaves alone). scores must not be NaN or +inf. */
+typedef struct {
+  int32_t B, W, V, K;          /* W in [1, 32], K in [1, 64], V >= 1          */
+  int32_t io_dtype;            /* gdn_dtype of the logits                     */
+  int32_t pad_token;
+  int64_t row_stride;          /* elements between rows of logits; 0: V       */
+  const void* logits;          /* [B, W, V] (rows row_stride apart)           */
+  const float* scores;         /* [B, W]                                      */
+  const uint8_t* finished;     /* [B, W] nonzero: finished; or NULL           */
+  float* out_scores;           /* out [B, K]                                  */
+  int32_t* parents;            /* out [B, K] beam of each choice              */
+  int32_t* tokens;             /* out [B, K]                                  */
+  void* workspace;             /* gdn_beam_workspace_bytes() bytes, device;
+                                  contents undefined before and after; calls
+                                  that may overlap need one each              */
+  size_t workspace_bytes;
+} gdn_beam_args;
+size_t gdn_beam_workspace_bytes(const gdn_beam_args* a);   /* 0 on error */
+gdn_status gdn_beam_select(const gdn_beam_args* a, void* stream);
+
 const char* gdn_last_error(void);
 int32_t gdn_abi_version(void);
 
@@ -402,13 +520,18 @@ int32_t gdn_abi_version(void);
  *                           significand, range +-65504). Precondition:
  *                           |q_i . k_j| < 65504, which L2-normalised q and k
  *                           (GatedDeltaNet's) always meet. An entry beyond
- *                           it sets this flag (o and ht are then invalid).
+ *                           it sets this flag (o and ht are then invalid);
+ *   GDN_DEVERR_POOL_SLOT    a state pool call named a slot outside the pool,
+ *                           or one that it would write twice, or write while
+ *                           another of its entries reads it (that page is
+ *                           left as it was).
  * Diagnostic query: unlike every other entry point it synchronizes the
  * device, then writes the flags to *flags and clears them. */
 #define GDN_DEVERR_LDS_WAIT 1u
 #define GDN_DEVERR_FLAG_WAIT 2u
 #define GDN_DEVERR_SAVED_STAMP 4u
 #define GDN_DEVERR_P_RANGE 8u
+#define GDN_DEVERR_POOL_SLOT 16u
 gdn_status gdn_device_errors(uint32_t* flags);
 
 #ifdef __cplusplus
