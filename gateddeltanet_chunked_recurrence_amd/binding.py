@@ -49,11 +49,13 @@ class DecodeBwdArgs(ctypes.Structure):
 
 
 READOUT_BEFORE_WRITE, READOUT_AFTER_WRITE = 0, 1
+SCALE_DIVIDE, SCALE_RECIPROCAL = 0, 1
 
 
 class PoolStruct(ctypes.Structure):
     _fields_ = [('layers', c_i32), ('slots', c_i32), ('Hv', c_i32), ('Dk', c_i32), ('Dv', c_i32),
-                ('state_fmt', c_i32), ('block_v', c_i32), ('data', c_vp), ('scales', c_vp)]
+                ('state_fmt', c_i32), ('block_v', c_i32), ('scale_rule', c_i32), ('data', c_vp),
+                ('scales', c_vp)]
 
 
 class PoolStepArgs(ctypes.Structure):
@@ -560,9 +562,12 @@ class StatePool:
 
     data [layers, slots, Hv, Dv, Dk] (float8_e4m3fn, int8 or float32) and
     scales [layers, slots, Hv, Dv / block_v] (float32, or None) are ordinary
-    tensors; the pool only refers to them."""
+    tensors; the pool only refers to them. scale_rule: SCALE_DIVIDE writes the
+    bits of gdn_qdq_state, SCALE_RECIPROCAL those of a state quantized in
+    PyTorch (x.abs().amax() / 448 on a GPU; see gdn_scale_rule)."""
 
-    def __init__(self, layers, slots, Hv, Dk, Dv, state_fmt=QDQ_OFF, block_v=64, device='cuda'):
+    def __init__(self, layers, slots, Hv, Dk, Dv, state_fmt=QDQ_OFF, block_v=64, device='cuda',
+                 scale_rule=SCALE_DIVIDE):
         dev = torch.device(device)
         if state_fmt not in self._DTYPES:
             raise ValueError(f'state_fmt {state_fmt}: use 0 off, 1 E4M3, 2 INT8')
@@ -572,18 +577,18 @@ class StatePool:
         scales = None
         if state_fmt != QDQ_OFF:
             scales = torch.full((layers, slots, Hv, Dv // block_v), 2.0 ** -126, device=dev)
-        self._bind(data, scales, state_fmt, block_v)
+        self._bind(data, scales, state_fmt, block_v, scale_rule)
 
     _DTYPES = {QDQ_OFF: torch.float32, QDQ_E4M3: torch.float8_e4m3fn, QDQ_INT8: torch.int8}
 
     @classmethod
-    def from_tensors(cls, data, scales, state_fmt=QDQ_OFF, block_v=64):
+    def from_tensors(cls, data, scales, state_fmt=QDQ_OFF, block_v=64, scale_rule=SCALE_DIVIDE):
         """A pool on existing tensors (shared, not copied)."""
         pool = cls.__new__(cls)
-        pool._bind(data, scales, state_fmt, block_v)
+        pool._bind(data, scales, state_fmt, block_v, scale_rule)
         return pool
 
-    def _bind(self, data, scales, state_fmt, block_v):
+    def _bind(self, data, scales, state_fmt, block_v, scale_rule):
         if state_fmt not in self._DTYPES or data.dtype is not self._DTYPES[state_fmt]:
             raise ValueError(f'pool data of {data.dtype} for state_fmt {state_fmt}')
         if data.dim() != 5 or not data.is_contiguous():
@@ -601,7 +606,8 @@ class StatePool:
         self.data, self.scales = data, scales
         self.layers, self.slots, self.Hv, self.Dk, self.Dv = L, S, Hv, Dk, Dv
         self.state_fmt, self.block_v, self.device = state_fmt, block_v, data.device
-        self._struct = PoolStruct(L, S, Hv, Dk, Dv, state_fmt, block_v, data.data_ptr(),
+        self.scale_rule = scale_rule
+        self._struct = PoolStruct(L, S, Hv, Dk, Dv, state_fmt, block_v, scale_rule, data.data_ptr(),
                                   None if scales is None else scales.data_ptr())
         self._ref = ctypes.byref(self._struct)
 

@@ -767,6 +767,8 @@ gdn_status check_pool(const gdn_pool* p, const char* what) {
     if (bv != 16 && bv != 32 && bv != 64 && bv != 128 && bv != 256)
       return fail(GDN_E_UNSUPPORTED, "%s: block_v %d: supported 16, 32, 64, 128, 256", what, bv);
     if (p->Dv % bv != 0) return fail(GDN_E_INVALID, "%s: block_v %d does not divide Dv %d", what, bv, p->Dv);
+    if (p->scale_rule != GDN_SCALE_DIVIDE && p->scale_rule != GDN_SCALE_RECIPROCAL)
+      return fail(GDN_E_INVALID, "%s: scale_rule %d: use 0 divide or 1 reciprocal", what, p->scale_rule);
     if (!p->scales) return fail(GDN_E_INVALID, "%s: pool scales is NULL", what);
     if (!aligned16(p->scales)) return fail(GDN_E_INVALID, "%s: pool scales is not 16-byte aligned", what);
   }
@@ -804,6 +806,7 @@ gdn::PoolRef pool_ref(const gdn_pool* p) {
   r.Dv = p->Dv;
   r.fmt = p->state_fmt;
   r.block_v = q ? p->block_v : p->Dv;
+  r.recip = p->scale_rule == GDN_SCALE_RECIPROCAL;
   return r;
 }
 

@@ -12,15 +12,15 @@
 // one workgroup per request, joins the parts: log-sums per beam, totals of
 // the candidates, the K best. Bound: reading the logits once from HBM.
 //
-// The K largest of a part: the K-th largest of a wave's 64 lane maxima is a
-// bound that at least K elements reach, found by bisection over the upper 16
-// bits of an order-preserving integer (16 ballots; a bound too low by less
-// than one such step only lets a few more elements through). The largest of
-// the four waves' bounds holds for the part; elements that reach it (about 2 K)
-// go to a list in LDS, where each finds its rank by counting. Only a list that
-// overflows (many equal logits) takes the slow way, K passes that each find
-// the next element in order. Elements are distinct by (value, token), so the
-// result does not depend on the order in which the list was filled.
+// The K largest of a part: the K-th largest of the workgroup's 256 lane maxima
+// is a bound that at least K elements reach, found by bisection over the upper
+// 16 bits of an order-preserving integer (16 rounds of four ballots; a bound too
+// low by less than one such step only lets a few more elements through).
+// Elements that reach it (little more than K) go to a list in LDS, where each
+// finds its rank by counting. Only a list that overflows (many equal logits)
+// takes the slow way, K passes that each find the next element in order.
+// Elements are distinct by (value, token), so the result does not depend on
+// the order in which the list was filled.
 //
 // Sums: FP32 within a part (at most 64 terms per lane, then a tree), FP64
 // across parts and for the totals. An exponent is exp2((x - m) log2(e)) with
@@ -51,25 +51,36 @@ __device__ __forceinline__ uint64_t pick_key(float x, int token) {
   return (uint64_t)ord32(x) << 32 | (uint32_t)~token;
 }
 
-// The largest t of `bits` upper bits such that at least `want` lanes have
-// key >= t << (32 - bits) (key: ord32 of each lane's value).
-template <int BITS>
-__device__ __forceinline__ uint32_t kth_bound(uint32_t key, int want) {
+// The largest t of BITS upper bits such that at least `want` of the N keys per
+// lane are >= t << (32 - BITS) (keys: ord32 of values).
+template <int BITS, int N>
+__device__ __forceinline__ uint32_t kth_bound(const uint32_t (&key)[N], int want) {
   uint32_t t = 0;
 #pragma unroll
   for (int b = 31; b >= 32 - BITS; --b) {
     const uint32_t c = t | (1u << b);
-    if (__builtin_popcountll(__ballot(key >= c)) >= want) t = c;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __builtin_popcountll(__ballot(key[i] >= c));
+    if (n >= want) t = c;
   }
   return t;
 }
 
-// Workspace of one call: per (row, split) the maximum and the sum, the count
-// and the K best as keys.
+// The sum over the 64 lanes, in every lane: DPP within rows of 16, then the
+// four row sums through scalar registers.
+__device__ __forceinline__ float wave_total(float x) {
+  x += dpp_f<0xB1>(x);
+  x += dpp_f<0x4E>(x);
+  x += dpp_f<0x141>(x);
+  x += dpp_f<0x140>(x);
+  return (read_lane(x, 0) + read_lane(x, 16)) + (read_lane(x, 32) + read_lane(x, 48));
+}
+
+// Workspace of one call: per (row, split) the maximum and the sum, and the K
+// best as keys (0 where there are fewer).
 struct Ws {
-  float* m;
-  float* s;
-  int32_t* cnt;
+  float2* ms;
   uint64_t* key;
 };
 __host__ __device__ inline int64_t up16(int64_t x) { return (x + 15) & ~int64_t(15); }
@@ -77,10 +88,8 @@ __host__ __device__ inline Ws ws_of(const BeamArgs& a) {
   const int64_t parts = (int64_t)a.B * a.W * a.splits;
   char* p = static_cast<char*>(a.ws);
   Ws w;
-  w.m = reinterpret_cast<float*>(p);
-  w.s = reinterpret_cast<float*>(p + up16(parts * 4));
-  w.cnt = reinterpret_cast<int32_t*>(p + 2 * up16(parts * 4));
-  w.key = reinterpret_cast<uint64_t*>(p + 3 * up16(parts * 4));
+  w.ms = reinterpret_cast<float2*>(p);
+  w.key = reinterpret_cast<uint64_t*>(p + up16(parts * 8));
   return w;
 }
 
@@ -94,7 +103,7 @@ template <bool F32, int E>
 __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
   constexpr int ES = F32 ? 4 : 2, VE = 16 / ES;
   __shared__ float sm[kWaves], ss[kWaves];
-  __shared__ uint32_t sb[kWaves];
+  __shared__ __attribute__((aligned(16))) uint32_t tops[kThreads];
   __shared__ uint64_t list[kList], best;
   __shared__ int count;
   const int row = blockIdx.x / a.splits, split = blockIdx.x - row * a.splits, tid = threadIdx.x;
@@ -106,29 +115,34 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
   const char* vec0 = base - (int64_t)off * ES;
   const int first = split * (E * kThreads) + tid;
   if (tid == 0) count = 0;
-
-  u32x4 raw[E];
-  const uint32_t ninf = F32 ? 0xFF800000u : 0xFF80FF80u;
-#pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int lo = (first + j * kThreads) * VE - off;      // token of the vector's first element
-    raw[j] = u32x4{ninf, ninf, ninf, ninf};
+  auto token0 = [&](int j) { return (first + j * kThreads) * VE - off; };   // of vector j's first element
+  auto load = [&](int j) {
+    const uint32_t ninf = F32 ? 0xFF800000u : 0xFF80FF80u;
+    const int lo = token0(j);
+    u32x4 raw{ninf, ninf, ninf, ninf};
     if (lo >= 0 && lo + VE <= a.V) {
-      raw[j] = *reinterpret_cast<const u32x4*>(vec0 + (int64_t)(first + j * kThreads) * 16);
+      raw = *reinterpret_cast<const u32x4*>(vec0 + (int64_t)(first + j * kThreads) * 16);
     } else if (lo + VE > 0 && lo < a.V) {
       // the row's ends: single elements
 #pragma unroll
       for (int e = 0; e < VE; ++e)
         if (lo + e >= 0 && lo + e < a.V) {
           if constexpr (F32) {
-            raw[j][e] = reinterpret_cast<const uint32_t*>(base)[lo + e];
+            raw[e] = reinterpret_cast<const uint32_t*>(base)[lo + e];
           } else {
             const uint32_t h = reinterpret_cast<const uint16_t*>(base)[lo + e];
-            raw[j][e / 2] = e & 1 ? (raw[j][e / 2] & 0xFFFFu) | h << 16 : (raw[j][e / 2] & 0xFFFF0000u) | h;
+            raw[e / 2] = e & 1 ? (raw[e / 2] & 0xFFFFu) | h << 16 : (raw[e / 2] & 0xFFFF0000u) | h;
           }
         }
     }
-  }
+    return raw;
+  };
+  // NaN counts as masked, +inf as the largest finite value
+  auto plain = [](float v) { return v != v ? -kInf : fminf(v, kMaxF); };
+
+  u32x4 raw[E];
+#pragma unroll
+  for (int j = 0; j < E; ++j) raw[j] = load(j);
   float x[E * VE], top = -kInf, vtop[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) {
@@ -145,8 +159,7 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
   float m = fmaxf(wave_max(top), -kMaxF), s = 0.f;
 #pragma unroll
   for (int i = 0; i < E * VE; ++i) s += fexp2((x[i] - m) * kLog2e);
-  // A NaN, or +inf (whose difference with itself is NaN), shows in the sum:
-  // count NaN as masked, +inf as the largest finite value, and sum again.
+  // A NaN, or +inf (whose difference with itself is NaN), shows in the sum
   if (__ballot(!(s <= kMaxF)) != 0) {
     top = -kInf;
 #pragma unroll
@@ -154,9 +167,8 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
       vtop[j] = -kInf;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        float& v = x[j * VE + e];
-        v = v != v ? -kInf : fminf(v, kMaxF);
-        vtop[j] = fmaxf(vtop[j], v);
+        x[j * VE + e] = plain(x[j * VE + e]);
+        vtop[j] = fmaxf(vtop[j], x[j * VE + e]);
       }
       top = fmaxf(top, vtop[j]);
     }
@@ -165,17 +177,16 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
 #pragma unroll
     for (int i = 0; i < E * VE; ++i) s += fexp2((x[i] - m) * kLog2e);
   }
-  s = wave_sum(s);
-  const uint32_t bound_w = kth_bound<16>(ord32(top), min(a.K, WAVE));
+  tops[tid] = ord32(top);
+  s = wave_total(s);
   if (lane == 0) {
     sm[wave] = m;
     ss[wave] = s;
-    sb[wave] = bound_w;
   }
   __syncthreads();
-  uint32_t bound = sb[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) bound = max(bound, sb[w]);
+  const u32x4 t4 = *reinterpret_cast<const u32x4*>(tops + 4 * lane);
+  const uint32_t tk[4] = {t4[0], t4[1], t4[2], t4[3]};
+  const uint32_t bound = kth_bound<16>(tk, a.K);
   // at least the smallest value above -inf (its upper 16 bits alone would let -inf through)
   const float reach = fmaxf(unord32(max(bound, ord32(-kInf))), -kMaxF);
   const int64_t part = (int64_t)row * a.splits + split;
@@ -187,18 +198,19 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
     float S = 0.f;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) S += ss[i] * fexp2((sm[i] - M) * kLog2e);
-    w.m[part] = M;
-    w.s[part] = S;
+    w.ms[part] = make_float2(M, S);
   }
+  if (__ballot(top >= reach) != 0) {
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    if (__ballot(vtop[j] >= reach) == 0) continue;
+    for (int j = 0; j < E; ++j) {
+      if (__ballot(vtop[j] >= reach) == 0) continue;
 #pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (x[j * VE + e] >= reach) {
-        const int p = atomicAdd(&count, 1);
-        if (p < kList) list[p] = pick_key(x[j * VE + e], (first + j * kThreads) * VE - off + e);
-      }
+      for (int e = 0; e < VE; ++e)
+        if (x[j * VE + e] >= reach) {
+          const int p = atomicAdd(&count, 1);
+          if (p < kList) list[p] = pick_key(x[j * VE + e], token0(j) + e);
+        }
+    }
   }
   __syncthreads();
   const int n = count;
@@ -210,18 +222,24 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
       for (int j = 0; j < n; ++j) rank += list[j] > mine;
       if (rank < a.K) out[rank] = mine;
     }
-    if (tid == 0) w.cnt[part] = min(n, a.K);
+    for (int i = n + tid; i < a.K; i += kThreads) out[i] = 0;
     return;
   }
-  // more ties than the list holds: the next element in order, K times
+  // more ties than the list holds: the next element in order, K times, read
+  // again (the registers of the elements are given up by now)
   uint64_t prev = ~0ull;
-  int found = 0;
-  for (; found < a.K; ++found) {
+  for (int found = 0; found < a.K; ++found) {
     uint64_t mine = 0;
+#pragma unroll 1
+    for (int j = 0; j < E; ++j) {
+      asm volatile("" ::: "memory");             // not hoisted out of the passes, which would take the registers
+      const u32x4 v = load(j);
 #pragma unroll
-    for (int i = 0; i < E * VE; ++i) {
-      const uint64_t k = pick_key(x[i], (first + (i / VE) * kThreads) * VE - off + i % VE);
-      if (x[i] >= reach && k < prev && k > mine) mine = k;
+      for (int e = 0; e < VE; ++e) {
+        const float y = plain(elem<F32>(v, e));
+        const uint64_t k = pick_key(y, token0(j) + e);
+        if (y >= reach && k < prev && k > mine) mine = k;
+      }
     }
     __syncthreads();
     if (tid == 0) best = 0;
@@ -229,10 +247,9 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
     if (mine) atomicMax(reinterpret_cast<unsigned long long*>(&best), (unsigned long long)mine);
     __syncthreads();
     prev = best;
-    if (prev == 0) break;
     if (tid == 0) out[found] = prev;
+    if (prev == 0) prev = 1;                     // none left: the rest is 0 too
   }
-  if (tid == 0) w.cnt[part] = found;
 }
 
 // One candidate of the join: order by total, then beam, then token.
@@ -245,18 +262,26 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
   return a.beam != b.beam ? a.beam < b.beam : a.token < b.token;
 }
 
+// ONE: all candidates of a request fit kHeld per thread, and stay in registers.
+constexpr int kHeld = 12;
+template <bool ONE>
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
+  constexpr float kLog2e = 1.4426950408889634f;
   // total = (x - top) + shift, with the beam's largest logit and score - log
   // sum exp(x - top); shift -inf: no candidates
   __shared__ double topx[kBeamMaxW], shift[kBeamMaxW];
-  __shared__ double ctot[kList];
-  __shared__ int cbeam[kList], ctok[kList];
-  __shared__ uint32_t sb[kWaves];
-  __shared__ Cand best[kWaves];
+  __shared__ Cand list[kList], best[kWaves];
+  __shared__ __attribute__((aligned(16))) uint32_t tops[kThreads];
   __shared__ int count;
   const int b = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const Ws w = ws_of(a);
   const int per = a.splits * a.K, cand = a.W * per;
+  const uint64_t* keys = w.key + (int64_t)b * cand;
+  uint64_t held[ONE ? kHeld : 1];
+  if constexpr (ONE) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) held[u] = tid + u * kThreads < cand ? keys[tid + u * kThreads] : 0;
+  }
   if (tid == 0) count = 0;
   for (int beam = wave; beam < a.W; beam += kWaves) {
     const int row = b * a.W + beam;
@@ -265,14 +290,16 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
     if (a.finished && a.finished[row]) {
       sh = score;
     } else {
+      const float2* ms = w.ms + (int64_t)row * a.splits;
       float M = -kMaxF;
-      for (int i = lane; i < a.splits; i += WAVE) M = fmaxf(M, w.m[(int64_t)row * a.splits + i]);
-      M = wave_max(M);
-      double S = 0.0;
-      for (int i = lane; i < a.splits; i += WAVE) {
-        const int64_t p = (int64_t)row * a.splits + i;
-        S += (double)w.s[p] * exp((double)w.m[p] - (double)M);
-      }
+      float2 f{-kMaxF, 0.f};
+      if (lane < a.splits) f = ms[lane];
+      for (int i = lane + WAVE; i < a.splits; i += WAVE) M = fmaxf(M, ms[i].x);
+      M = wave_max(fmaxf(M, f.x));
+      // each part's share relative to the largest: its FP32 error is that of
+      // an exponential of a difference, as within a part
+      double S = (double)(f.y * fexp2((f.x - M) * kLog2e));
+      for (int i = lane + WAVE; i < a.splits; i += WAVE) S += (double)(ms[i].y * fexp2((ms[i].x - M) * kLog2e));
 #pragma unroll
       for (int o = 32; o >= 1; o >>= 1) S += __shfl_xor(S, o, WAVE);
       tx = M;
@@ -289,45 +316,54 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
     a.tokens[(int64_t)b * a.K + i] = -1;
   }
   __syncthreads();
-  auto get = [&](int i, Cand& c) -> bool {
+  auto get = [&](int i, uint64_t key, Cand& c) -> bool {
     c.beam = i / per;
-    const int r = i - c.beam * per, split = r / a.K, k = r - split * a.K, row = b * a.W + c.beam;
     const double sh = shift[c.beam];
     if (!(sh > -(double)kInf)) return false;
-    if (a.finished && a.finished[row]) {
+    if (a.finished && a.finished[b * a.W + c.beam]) {
       c.total = sh;
       c.token = a.pad_token;
-      return r == 0;
+      return i == c.beam * per;
     }
-    const int64_t part = (int64_t)row * a.splits + split;
-    if (k >= w.cnt[part]) return false;
-    const uint64_t key = w.key[part * a.K + k];
+    if (key == 0) return false;
     c.total = ((double)unord32((uint32_t)(key >> 32)) - topx[c.beam]) + sh;
     c.token = ~(uint32_t)key;
     return true;
   };
-  // a bound that at least K candidates reach (all of them where a wave has fewer)
-  uint32_t top = 0;
-  for (int i = tid; i < cand; i += kThreads) {
-    Cand c;
-    if (get(i, c)) top = max(top, ord32((float)c.total));
-  }
-  const uint32_t bw = kth_bound<20>(top, min(a.K, WAVE));
-  if (lane == 0) sb[wave] = bw;
-  __syncthreads();
-  uint32_t bound = sb[0];
+  // a bound that at least K candidates reach (all of them where there are fewer)
+  uint32_t top = 0, ck[ONE ? kHeld : 1];
+  if constexpr (ONE) {
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) bound = max(bound, sb[i]);
-  for (int i = tid; i < cand; i += kThreads) {
-    Cand c;
-    if (get(i, c) && ord32((float)c.total) >= bound) {
-      const int p = atomicAdd(&count, 1);
-      if (p < kList) {
-        ctot[p] = c.total;
-        cbeam[p] = c.beam;
-        ctok[p] = c.token;
-      }
+    for (int u = 0; u < kHeld; ++u) {
+      Cand c;
+      ck[u] = 0;
+      if (tid + u * kThreads < cand && get(tid + u * kThreads, held[u], c)) ck[u] = ord32((float)c.total);
+      top = max(top, ck[u]);
     }
+  } else {
+    for (int i = tid; i < cand; i += kThreads) {
+      Cand c;
+      if (get(i, keys[i], c)) top = max(top, ord32((float)c.total));
+    }
+  }
+  tops[tid] = top;
+  __syncthreads();
+  const u32x4 t4 = *reinterpret_cast<const u32x4*>(tops + 4 * lane);
+  const uint32_t tk[4] = {t4[0], t4[1], t4[2], t4[3]};
+  const uint32_t bound = max(kth_bound<20>(tk, a.K), 1u);
+  auto keep = [&](int i, uint64_t key) {
+    Cand c;
+    if (get(i, key, c) && ord32((float)c.total) >= bound) {
+      const int p = atomicAdd(&count, 1);
+      if (p < kList) list[p] = c;
+    }
+  };
+  if constexpr (ONE) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (ck[u] >= bound) keep(tid + u * kThreads, held[u]);
+  } else {
+    for (int i = tid; i < cand; i += kThreads) keep(i, keys[i]);
   }
   __syncthreads();
   const int n = count;
@@ -338,9 +374,9 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
   };
   if (n <= kList) {
     for (int i = tid; i < n; i += kThreads) {
-      const Cand mine{ctot[i], cbeam[i], ctok[i]};
+      const Cand mine = list[i];
       int rank = 0;
-      for (int j = 0; j < n; ++j) rank += before(Cand{ctot[j], cbeam[j], ctok[j]}, mine);
+      for (int j = 0; j < n; ++j) rank += before(list[j], mine);
       if (rank < a.K) put(rank, mine);
     }
     return;
@@ -351,7 +387,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
     Cand mine{-(double)kInf, 0, 0};
     for (int i = tid; i < cand; i += kThreads) {
       Cand c;
-      if (get(i, c) && before(prev, c) && before(c, mine)) mine = c;
+      if (get(i, keys[i], c) && before(prev, c) && before(c, mine)) mine = c;
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
@@ -386,7 +422,7 @@ void beam_plan(BeamArgs& a) {
 
 int64_t beam_workspace_bytes(const BeamArgs& a) {
   const int64_t parts = (int64_t)a.B * a.W * a.splits;
-  return 3 * up16(parts * 4) + parts * a.K * 8;
+  return up16(parts * 8) + parts * a.K * 8;
 }
 
 namespace {
@@ -407,7 +443,9 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
   else launch_parts<false>(a, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  beam_join_kernel<<<dim3((unsigned)a.B), kThreads, 0, s>>>(a);
+  const dim3 grid((unsigned)a.B);
+  if ((int64_t)a.W * a.splits * a.K <= kHeld * kThreads) beam_join_kernel<true><<<grid, kThreads, 0, s>>>(a);
+  else beam_join_kernel<false><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -274,6 +274,7 @@ struct PoolRef {
   int64_t page;               // bytes of one page's data
   int32_t tiles;              // scales of one page (0 with the format off)
   int32_t layers, slots, Hv, Dk, Dv, fmt, block_v;
+  int32_t recip;              // gdn_scale_rule
 };
 hipError_t launch_pool_write(const PoolRef& p, int layer, const int32_t* slots, int n,
                              const float* states, hipStream_t s);

@@ -14,26 +14,46 @@ __device__ __forceinline__ void pool_error(const PoolRef& p) {
 // (out[j]). Every wave that writes a part of the page asks this, with the
 // same answer in each, so an index given twice leaves the page as it was
 // instead of a mixture of two results. All 64 lanes call it together; each
-// takes four entries per step (the arrays are 16-byte aligned).
+// takes four entries per load (the arrays are 16-byte aligned), and four
+// loads are in flight at once: 1,024 entries cost one round trip to L2. The
+// last vector is read again by lanes past it (asking twice changes nothing).
+// Several waves may ask for a part of the entries each and join the answers.
 __device__ __forceinline__ bool pool_claimed(const int32_t* in, const int32_t* out, int count, int n,
-                                             int dst, int lo) {
+                                             int dst, int lo, int part = 0, int parts = 1) {
   typedef int i32x4 __attribute__((ext_vector_type(4)));
+  const int lane = __lane_id(), nv = count >> 2;
   bool hit = false;
-  for (int j0 = 4 * (int)__lane_id(); j0 < count; j0 += 4 * WAVE) {
-    if (j0 + 4 <= count) {
-      const i32x4 a = *reinterpret_cast<const i32x4*>(in + j0);
-      const i32x4 b = in == out ? a : *reinterpret_cast<const i32x4*>(out + j0);
+  auto test = [&](int j, int a, int b) {
+    hit |= (j != n) & (a >= lo) & (b >= 0) & ((a == dst) | (b == dst));
+  };
+  for (int v0 = 4 * WAVE * part; v0 < nv; v0 += 4 * WAVE * parts) {
+    i32x4 a[4], b[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        hit |= j0 + e != n && a[e] >= lo && b[e] >= 0 && (a[e] == dst || b[e] == dst);
-    } else {
-      for (int j = j0; j < count; ++j) {
-        const int a = in[j], b = out[j];
-        hit |= j != n && a >= lo && b >= 0 && (a == dst || b == dst);
-      }
+    for (int u = 0; u < 4; ++u)
+      if (v0 + u * WAVE < nv) a[u] = reinterpret_cast<const i32x4*>(in)[min(v0 + u * WAVE + lane, nv - 1)];
+    if (in != out) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (v0 + u * WAVE < nv) b[u] = reinterpret_cast<const i32x4*>(out)[min(v0 + u * WAVE + lane, nv - 1)];
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (v0 + u * WAVE < nv)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          test(4 * min(v0 + u * WAVE + lane, nv - 1) + e, a[u][e], in != out ? b[u][e] : a[u][e]);
   }
+  const int j = 4 * nv + lane;
+  if (part == 0 && j < count) test(j, in[j], out[j]);
   return __ballot(hit) != 0;
+}
+
+// The tile scale under the pool's rule: amax / q_max as gdn_qdq_state, or amax
+// times the FP32-rounded 1 / q_max as PyTorch divides a tensor by a number.
+template <int FMT>
+__device__ __forceinline__ float pool_scale(const PoolRef& p, float amax) {
+  constexpr float kRecip = 1.0f / QdqFmt<FMT>::qmax;
+  return p.recip ? fmaxf(amax * kRecip, 1.17549435e-38f) : qdq_scale<FMT>(amax);
 }
 
 // Four codes of one word as floats (unscaled).
@@ -54,19 +74,41 @@ __device__ __forceinline__ void codes4(uint32_t w, float (&x)[4]) {
   }
 }
 
-// Four values of a tile to codes c = RNE(fl(x r)) and their word, r = fl(1/d)
+// Eight codes (two words) as the bf16 values they are (exact: E4M3 has four
+// significant bits, the integers at most seven).
+template <int FMT>
+__device__ __forceinline__ bf16x8 codes8_bf16(uint32_t w0, uint32_t w1) {
+  bf16x8 b;
+  if constexpr (FMT == 1) {
+    typedef bf16 bf16x2v __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int w = static_cast<int>(h < 2 ? w0 : w1);
+      const bf16x2v x = (h & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
+                                : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+      b[2 * h] = x[0];
+      b[2 * h + 1] = x[1];
+    }
+  } else {
+    float x[8];
+    codes4<FMT>(w0, *reinterpret_cast<float(*)[4]>(&x[0]));
+    codes4<FMT>(w1, *reinterpret_cast<float(*)[4]>(&x[4]));
+#pragma unroll
+    for (int c = 0; c < 8; ++c) b[c] = to_bf16(x[c]);
+  }
+  return b;
+}
+
+// Four values of a tile to the word of their codes c = RNE(fl(x r)), r = fl(1/d)
 // from the tile's own amax, so no clamp is needed (see quant4 in
 // gdn_device.h). The integer format rounds by adding 1.5 * 2^23: the sum's
-// low byte is the integer in two's complement and the difference the value
-// (|x r| <= 127 (1 + 2^-21) < 2^22), one add each instead of a rounding, a
-// conversion and a mask.
+// low byte is the integer in two's complement (|x r| <= 127 (1 + 2^-21) < 2^22),
+// one add instead of a rounding, a conversion and a mask.
 template <int FMT>
-__device__ __forceinline__ uint32_t quant_word(float (&x)[4], float r) {
+__device__ __forceinline__ uint32_t quant_word(const float (&x)[4], float r) {
   if constexpr (FMT == 1) {
     const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * r, x[1] * r, 0, false);
-    const uint32_t w = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * r, x[3] * r, lo, true));
-    codes4<1>(w, x);
-    return w;
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * r, x[3] * r, lo, true));
   } else {
     // the product rounds before the sum (no fused multiply-add)
 #pragma clang fp contract(off)
@@ -77,7 +119,6 @@ __device__ __forceinline__ uint32_t quant_word(float (&x)[4], float r) {
       const float p = x[e] * r;
       const float y = p + kMagic;
       b[e] = __builtin_bit_cast(uint32_t, y);
-      x[e] = y - kMagic;
     }
     // bytes (b0, b1) and (b2, b3) into halves, then into one word
     const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(512) pool_write_kernel(PoolRef P, int64_t laye
   float amax = 0.f;
   for (int i = 0; i < KW * nb; ++i)
     for (int q = 0; q < nq; ++q) amax = fmaxf(amax, xm[w0 + i][q0 + q]);
-  const float d = qdq_scale<FMT>(amax), r = 1.0f / d;
+  const float d = pool_scale<FMT>(P, amax), r = 1.0f / d;
   uint8_t* dst = P.data + (layer_page + slot) * P.page + (int64_t)w.h * P.Dv * DK;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {

@@ -10,20 +10,31 @@
 // and the last S goes to slot slots_out[n] (or back). As executed, with
 // a = alpha d:  p = c^T k, w = c^T q;  u = beta (v - a p);
 //   o_before = scale (a w + (k . q) u);  S' = a c + k u^T
-// so the state is decoded once, both products read the codes as they are
-// (exact in FP32) and the output needs no pass over S'. All arithmetic is FP32.
+// so both products read the codes as they are and the output needs no pass
+// over S'.
 //
 // Bound: a token moves Dk Dv bytes in and out per head for 6 Dk Dv FLOP, so
 // at many sequences this is a copy (bound by HBM). The page is value-major
-// ([Dv, Dk], Dk contiguous): a scale tile is one contiguous block, and the
-// sums over Dk run along a row, mostly inside a lane: 8 lanes (Dk 128; 4 at
-// Dk 64) hold a row as 16 codes each, so a sum is 16 FMAs and 3 (2) DPP adds.
-// With key-major pages every row sum would instead cross 16 lanes for each of
-// 16 columns. One wave holds RPW consecutive rows of one tile (16-byte loads,
-// NLD per lane, all issued at once); a tile of several waves exchanges its
-// amax through LDS. The vector ALUs do the products: at most 7 instructions
-// per element, and matrix cores would need the codes converted to bf16 and
-// leave 14 of 16 columns empty.
+// ([Dv, Dk], Dk contiguous), so a scale tile is one contiguous block and the
+// sums over Dk run along a row.
+//
+// Pages of codes: the products on the matrix cores, as an integer or E4M3 code
+// is exact in bf16. With 16 state rows as the columns of B (32 keys deep),
+// v_mfma_f32_16x16x32_bf16 forms
+//   - p and w: A has k and q as rows, repeated every four rows, so that each
+//     lane finds both sums of its own state row in its accumulator;
+//   - S' in units of a, c + k (u / a): A picks 16 of the 32 keys (a permuted
+//     identity), then adds k times u / a, both as sums of bf16 parts (three parts are
+//     exact for 24 bits). The keys of a 16x16 result tile are those of one dword
+//     of codes per lane, so its four values are quantized into that dword.
+// The vector ALUs keep half an instruction per element to decode, two to
+// quantize and half for the amax. With S' and the sums on them (FP32 FMAs)
+// they took 6.9 instructions per element and, at 1,024 sequences of 32 heads
+// (Dv 256, 1.8 GB in and out), bound the step: 460 us.
+// Pages of FP32 states move four times the bytes; their sums stay on the
+// vector ALUs.
+#include <algorithm>
+
 #include "gdn_device.h"
 #include "gdn_launch.h"
 #include "gdn_pool.h"
@@ -32,12 +43,11 @@ namespace gdn {
 
 namespace {
 
-// The sum over the LPR lanes that hold one row (4 or 8 neighbours).
-template <int LPR>
+// The sum over the eight neighbouring lanes that hold one row.
 __device__ __forceinline__ float sum_row(float x) {
   x += dpp_f<0xB1>(x);
   x += dpp_f<0x4E>(x);
-  if constexpr (LPR == 8) x += dpp_f<0x141>(x);
+  x += dpp_f<0x141>(x);
   return x;
 }
 
@@ -101,215 +111,675 @@ __device__ __forceinline__ void st_run(void* p, const float (&x)[N]) {
   }
 }
 
-// How a wave covers its rows. With codes a lane holds 16 consecutive keys of
-// a row; FP32 states are read as four keys every 32, so that the eight lanes
-// of a row together touch whole 128-byte lines in each load.
-template <int DK, int FMT>
-struct StepMap {
-  static constexpr int LPR = FMT != 0 ? DK / 16 : 8;    // lanes per row
-  static constexpr int EPL = DK / LPR;                  // keys per lane
-  static constexpr int GR = WAVE / LPR;                 // rows side by side
+// What every wave of a call does first: its sequence, head and rows, whether
+// it may run, and where its state goes.
+struct StepUnit {
+  int n, h, row;              // sequence, value head, first row of the wave
+  int T, slot, to;
+  bool idle;                  // no sequence, or nothing to do
+};
+__device__ __forceinline__ StepUnit step_unit(const PoolStepArgs& a, int unit, int rpw) {
+  const int per = a.pool.Dv / rpw, ph = per * a.pool.Hv;
+  StepUnit w;
+  w.n = unit / ph;
+  const int rem = unit - w.n * ph;
+  w.h = rem / per;
+  w.row = (rem - w.h * per) * rpw;
+  w.T = a.lens ? min(max(a.lens[w.n], 0), a.T) : a.T;
+  w.slot = a.slots[w.n];
+  w.to = a.slots_out ? a.slots_out[w.n] : w.slot;
+  w.idle = w.slot == -1 || (w.T == 0 && w.to == w.slot);
+  return w;
+}
+__device__ __forceinline__ bool step_in_ok(const PoolStepArgs& a, const StepUnit& w) {
+  return w.slot >= 0 && w.slot < a.pool.slots;
+}
+__device__ __forceinline__ bool step_refused(const PoolStepArgs& a, const StepUnit& w) {
+  if (!step_in_ok(a, w) || w.to < -1 || w.to >= a.pool.slots) return true;
+  return w.to >= 0 && pool_claimed(a.slots, a.slots_out ? a.slots_out : a.slots, a.B, w.n, w.to, 0);
+}
+
+// ------------------------------------------------------------ pages of codes
+// Part m of a float: three bf16 values whose sum is the float (to 2^-24), then 0.
+__device__ __forceinline__ bf16 split_part(float x, int m) {
+  const bf16 h = to_bf16(x);
+  const float r1 = x - from_bf16(h);
+  const bf16 mid = to_bf16(r1);
+  const bf16 low = to_bf16(r1 - from_bf16(mid));
+  return m == 0 ? h : m == 1 ? mid : m == 2 ? low : to_bf16(0.f);
+}
+
+// A wave's LDS: k and q as they come, zeros, and k laid out for the update:
+// for result tile x = 4 s + c and row m, the A row of key 64 s + 16 (m >> 2) + 4 c
+// + (m & 3): bf16 (k, k, k, 0...), FP32 the parts (k1, k1, k1, k2, k2, k3, 0, 0).
+template <int DK, bool F32>
+struct HeadLds {
+  static constexpr int ES = F32 ? 4 : 2, HB = 2 * DK * ES, LB = HB / WAVE;
+  static constexpr int ZERO = HB, ROWS = HB + DK * ES, BYTES = ROWS + 16 * DK;
 };
 
-// NW waves per workgroup. A tile of WPT waves (block_v / RPW) is one
-// workgroup (NW = WPT); with WPT = 1 the waves are independent.
-template <int DK, int FMT, bool F32, int NLD, int NW>
-__global__ void __launch_bounds__(NW * WAVE) pool_step_kernel(PoolStepArgs a, int wpt, int waves) {
-  using M = StepMap<DK, FMT>;
-  constexpr int LPR = M::LPR, EPL = M::EPL, RPW = M::GR * NLD, ES = F32 ? 4 : 2;
+// Writes a head's LDS from the lanes' shares of k and q (LB bytes each).
+template <int DK, bool F32>
+__device__ __forceinline__ void head_to_lds(char* hb, const uint32_t* share) {
+  using H = HeadLds<DK, F32>;
+  const int lane = __lane_id();
+  if constexpr (H::LB == 16) *reinterpret_cast<u32x4*>(hb + lane * 16) = u32x4{share[0], share[1], share[2], share[3]};
+  else if constexpr (H::LB == 8) *reinterpret_cast<uint2*>(hb + lane * 8) = make_uint2(share[0], share[1]);
+  else *reinterpret_cast<uint32_t*>(hb + lane * 4) = share[0];
+  // a lane below 32 holds DK / 32 keys of k
+  if (lane < 32) {
+#pragma unroll
+    for (int i = 0; i < DK / 32; ++i) {
+      const int key = lane * (DK / 32) + i, s = key >> 6, y = key & 63;
+      const int x = 4 * s + ((y >> 2) & 3), m = 4 * (y >> 4) + (y & 3);
+      bf16x8 row{};
+      if constexpr (F32) {
+        const float k = __builtin_bit_cast(float, share[i]);
+        const bf16 k1 = split_part(k, 0), k2 = split_part(k, 1);
+        row[0] = row[1] = row[2] = k1;
+        row[3] = row[4] = k2;
+        row[5] = split_part(k, 2);
+      } else {
+        const uint32_t w = share[i / 2];
+        const bf16 k = __builtin_bit_cast(bf16, static_cast<uint16_t>(i & 1 ? w >> 16 : w & 0xFFFFu));
+        row[0] = row[1] = row[2] = k;
+      }
+      *reinterpret_cast<bf16x8*>(hb + H::ROWS + (16 * x + m) * 16) = row;
+    }
+  }
+  // the wave's own buffer: LDS operations of a wave stay in order
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+template <int DK, bool F32>
+__device__ __forceinline__ void head_zeros(char* hb) {
+  using H = HeadLds<DK, F32>;
+  for (int i = 4 * __lane_id(); i < DK * H::ES; i += 4 * WAVE) *reinterpret_cast<uint32_t*>(hb + H::ZERO + i) = 0;
+}
+
+// The lane's row of A for the row sums over keys 64 s + 16 g + 8 i .. + 7. bf16
+// inputs: k (r % 4 == 0), q (1) or zeros. FP32: part r % 4 of k (which = 0) or q (1).
+template <int DK, bool F32>
+__device__ __forceinline__ bf16x8 sum_row_of(const char* hb, int r, int g, int s, int i, int which) {
+  using H = HeadLds<DK, F32>;
+  if constexpr (F32) {
+    const float* p = reinterpret_cast<const float*>(hb + which * (H::HB / 2)) + 64 * s + 16 * g + 8 * i;
+    bf16x8 x;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = split_part(p[c], r & 3);
+    return x;
+  } else {
+    const char* p = hb + ((r & 2) ? H::ZERO : (r & 1) * (H::HB / 2));
+    return *reinterpret_cast<const bf16x8*>(p + (64 * s + 16 * g + 8 * i) * 2);
+  }
+}
+
+// k . q, in every lane.
+template <int DK, bool F32>
+__device__ __forceinline__ float head_kq(const char* hb, int r, int g) {
+  using H = HeadLds<DK, F32>;
+  if constexpr (F32) {
+    float kq = 0.f;
+    const float *k = reinterpret_cast<const float*>(hb), *q = reinterpret_cast<const float*>(hb + H::HB / 2);
+#pragma unroll
+    for (int i = 0; i < DK / WAVE; ++i) kq = fmaf(k[WAVE * i + 16 * g + r], q[WAVE * i + 16 * g + r], kq);
+    return wave_sum(kq);
+  } else {
+    f32x4 acc = zero4();
+#pragma unroll
+    for (int s = 0; s < DK / 64; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        acc = mfma(sum_row_of<DK, F32>(hb, r, g, s, i, 0),
+                   *reinterpret_cast<const bf16x8*>(hb + (64 * s + 16 * g + 8 * i) * 2), acc);
+    return acc[1];
+  }
+}
+
+// One token on the rows of a wave: 16 NT rows of one scale tile, lane (r = lane
+// & 15, g = lane >> 4) holding, of each 16-row tile, row r and the keys 64 s + 16 g
+// .. + 15 (one 16-byte piece per s). In: codes `raw`, a = exp(g) d. Out: the new
+// codes in `raw`, the tile's scale d and the outputs o. `join` makes the
+// tile's amax of a wave's; `decoded` is called when the codes are in bf16.
+template <int DK, int FMT, bool F32, int NT, typename Decoded, typename Join>
+__device__ __forceinline__ void step_tile(const PoolRef& P, const char* hb, u32x4 (&raw)[NT][DK / 64],
+                                          float alpha, float beta, float kq, float scale,
+                                          const float (&v)[NT], float (&o)[NT], float& d, bool after,
+                                          Decoded decoded, Join join) {
+  using H = HeadLds<DK, F32>;
+  constexpr int NS = DK / 64;
+  const int lane = __lane_id(), r = lane & 15, g = lane >> 4;
+  // the codes as B operands
+  bf16x8 b[NT][NS][2];
+  auto decode = [&]() {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) b[j][s][i] = codes8_bf16<FMT>(raw[j][s][2 * i], raw[j][s][2 * i + 1]);
+  };
+  float p[NT], q[NT];
+  auto row_sums = [&]() {
+    f32x4 ak[NT], aq[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) ak[j] = aq[j] = zero4();
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bf16x8 rk = sum_row_of<DK, F32>(hb, r, g, s, i, 0);
+        bf16x8 rq = rk;
+        if constexpr (F32) rq = sum_row_of<DK, F32>(hb, r, g, s, i, 1);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          ak[j] = mfma(rk, b[j][s][i], ak[j]);
+          if constexpr (F32) aq[j] = mfma(rq, b[j][s][i], aq[j]);
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      p[j] = F32 ? ak[j][0] + (ak[j][1] + ak[j][2]) : ak[j][0];
+      q[j] = F32 ? aq[j][0] + (aq[j][1] + aq[j][2]) : ak[j][1];
+    }
+  };
+  decode();
+  decoded();
+  row_sums();
+  // The update in units of a, or of 2^-64 where a is smaller (a state forgotten
+  // within a token, or the zero page with its scale 2^-126), so that u / unit
+  // cannot overflow for |u| < 2^63; the codes then count a / unit < 1 each,
+  // rounded to bf16: that rounds values below 2^-55 only.
+  const float unit = fmaxf(alpha, 0x1p-64f), ru = 1.0f / unit;
+  const uint32_t one = alpha >= 0x1p-64f ? 0x3F803F80u : [&]() {
+    const uint32_t h = __builtin_bit_cast(uint16_t, to_bf16(alpha * ru));
+    return h | h << 16;
+  }();
+  // A of tiles with even and odd c: row m picks, for lanes g == m >> 2, element 4 (c & 1) + (m & 3)
+  bf16x8 pick[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    u32x4 w{0, 0, 0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[2 * c + h] = (g == r >> 2 && (r & 2) == 2 * h) ? one & (r & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+    pick[c] = __builtin_bit_cast(bf16x8, w);
+  }
+  const char* krow = hb + (g == 0 ? H::ROWS + 16 * r : (int)H::ZERO);
+  f32x4 S[NT][4 * NS];
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const float u = beta * fmaf(-alpha, p[j], v[j]);
+    o[j] = scale * fmaf(kq, u, alpha * q[j]);
+    const float uu = u * ru;
+    bf16x8 ub{};
+    const bf16 u1 = to_bf16(uu);
+    const float r1 = uu - from_bf16(u1);
+    const bf16 u2 = to_bf16(r1), u3 = to_bf16(r1 - from_bf16(u2));
+    ub[0] = u1;
+    ub[1] = u2;
+    ub[2] = u3;
+    if constexpr (F32) {
+      ub[3] = u1;
+      ub[4] = u2;
+      ub[5] = u1;
+    }
+#pragma unroll
+    for (int x = 0; x < 4 * NS; ++x) {
+      const bf16x8 kr = *reinterpret_cast<const bf16x8*>(krow + (g == 0 ? 256 * x : 0));
+      f32x4 acc = mfma(pick[x & 1], b[j][x >> 2][(x >> 1) & 1], zero4());
+      acc = mfma(kr, ub, acc);
+      S[j][x] = acc;
+      m = fmaxf(fmaxf(m, fabsf(acc[0])), fabsf(acc[1]));
+      m = fmaxf(fmaxf(m, fabsf(acc[2])), fabsf(acc[3]));
+    }
+  }
+  d = pool_scale<FMT>(P, join(wave_max(m)) * unit);
+  const float rd = (1.0f / d) * unit;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int x = 0; x < 4 * NS; ++x) {
+      const float y[4] = {S[j][x][0], S[j][x][1], S[j][x][2], S[j][x][3]};
+      raw[j][x >> 2][x & 3] = quant_word<FMT>(y, rd);
+    }
+  if (after) {
+    decode();
+    row_sums();
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j] = scale * (d * q[j]);
+  }
+}
+
+// A lane's share of k and q of one token and head (LB bytes of [k | q]).
+template <int DK, bool F32>
+__device__ __forceinline__ void load_share(const PoolStepArgs& a, int64_t token, int hk, uint32_t* share) {
+  using H = HeadLds<DK, F32>;
+  const int at = __lane_id() * H::LB, off = at % (H::HB / 2);
+  const char* kp = static_cast<const char*>(a.k) + (token * a.ks + hk * DK) * H::ES;
+  const char* qp = static_cast<const char*>(a.q) + (token * a.qs + hk * DK) * H::ES;
+  const char* p = (at < H::HB / 2 ? kp : qp) + off;
+  if constexpr (H::LB == 16) {
+    const u32x4 y = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) share[i] = y[i];
+  } else if constexpr (H::LB == 8) {
+    const uint2 y = *reinterpret_cast<const uint2*>(p);
+    share[0] = y.x;
+    share[1] = y.y;
+  } else {
+    share[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// Several tokens, or lengths: one wave per 16 NT rows, the state stays in
+// registers as codes between tokens.
+template <int DK, int FMT, bool F32, int NT, int WPT>
+__global__ void __launch_bounds__((WPT == 1 ? 4 : WPT) * WAVE)
+pool_step_many_kernel(PoolStepArgs a, int waves) {
+  using H = HeadLds<DK, F32>;
+  constexpr int NW = WPT == 1 ? 4 : WPT, NS = DK / 64, ES = H::ES, RPW = 16 * NT;
+  __shared__ __attribute__((aligned(16))) char hbuf[NW][H::BYTES];
   __shared__ float xm[2][NW];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = __lane_id();
-  const int gw = blockIdx.x * NW + wave;
-  if (gw >= waves) return;                      // only where the waves are independent
+  const int wunit = blockIdx.x * NW + wave;
+  if (wunit >= waves) return;                   // only where the waves are independent
   const PoolRef& P = a.pool;
-  const int Hv = P.Hv, Dv = P.Dv, per = Dv / RPW;
-  const int n = gw / (per * Hv), rem = gw - n * per * Hv, h = rem / per, row_w = (rem - h * per) * RPW;
-  const int grp = lane / LPR, c = lane % LPR, row0 = row_w + grp * NLD;   // the lane's first row
-  int T = a.T;
-  if (a.lens) T = min(max(a.lens[n], 0), T);
-  const int slot = a.slots[n];
-  if (slot == -1) return;                       // no sequence here (uniform over a tile)
-  const int32_t* outs = a.slots_out ? a.slots_out : a.slots;
-  const int to = outs[n];
-  const bool in_ok = slot >= 0 && slot < P.slots, out_ok = to >= -1 && to < P.slots;
-
-  u32x4 raw[NLD * (FMT != 0 ? 1 : EPL / 4)];
-  const int64_t head = (int64_t)h * Dv * DK * (FMT != 0 ? 1 : 4);
-  // byte offset of the lane's piece j within a page
-  auto piece = [&](int j) -> int64_t {
-    if constexpr (FMT != 0) return head + (int64_t)(row0 + j) * DK + 16 * c;
-    else return head + ((int64_t)(row0 + j / (EPL / 4)) * DK + 32 * (j % (EPL / 4)) + 4 * c) * 4;
-  };
-  if (in_ok) {
-    const uint8_t* src = P.data + (a.layer_page + slot) * P.page;
-#pragma unroll
-    for (int j = 0; j < (int)(sizeof(raw) / sizeof(raw[0])); ++j)
-      raw[j] = *reinterpret_cast<const u32x4*>(src + piece(j));
-  }
-  const int tile = FMT != 0 ? h * (Dv / P.block_v) + row_w / P.block_v : 0;
+  const int r = lane & 15, g = lane >> 4;
+  const StepUnit w = step_unit(a, wunit, RPW);
+  if (w.idle) return;                           // uniform over a tile's waves
+  const int Hv = P.Hv, Dv = P.Dv, hk = w.h / (Hv / a.Hqk);
+  const int64_t tok0 = (int64_t)w.n * a.T, o_tok = (int64_t)Hv * Dv;
+  u32x4 raw[NT][NS];
+  const int64_t head = (int64_t)w.h * Dv * DK + (int64_t)(w.row + r) * DK + 16 * g;
+  const int tile = w.h * (Dv / P.block_v) + w.row / P.block_v;
   float d = 1.f;
-  if (FMT != 0 && in_ok) d = P.scales[(a.layer_page + slot) * P.tiles + tile];
-  const bool claimed = to >= 0 && pool_claimed(a.slots, outs, a.B, n, to, 0);
-  const int hk = h / (Hv / a.Hqk);
-  const int64_t o_tok = (int64_t)Hv * Dv;
-  const int64_t o_off = (int64_t)n * a.T * o_tok + (int64_t)h * Dv + row0;
-  if (!in_ok || !out_ok || claimed) {
-    // refused: the outputs say so, the pages stay as they are
-    if (lane == 0) pool_error(P);
-    float nan[NLD];
+  if (step_in_ok(a, w)) {
+    const uint8_t* src = P.data + (a.layer_page + w.slot) * P.page + head;
 #pragma unroll
-    for (int j = 0; j < NLD; ++j) nan[j] = __builtin_nanf("");
-    if (c == 0)
-      for (int t = 0; t < T; ++t)
-        st_run<NLD, F32>(static_cast<char*>(a.o) + (o_off + t * o_tok) * ES, nan);
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) raw[j][s] = *reinterpret_cast<const u32x4*>(src + 16 * j * DK + 64 * s);
+    d = P.scales[(a.layer_page + w.slot) * P.tiles + tile];
+  }
+  uint32_t share[H::LB / 4];
+  float v[NT], o[NT], gate = 0.f, beta = 0.f;
+  auto load_token = [&](int t) {
+    load_share<DK, F32>(a, tok0 + t, hk, share);
+    const char* vp = static_cast<const char*>(a.v) + ((tok0 + t) * a.vs + (int64_t)w.h * Dv + w.row + r) * ES;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      v[j] = F32 ? reinterpret_cast<const float*>(vp)[16 * j] : from_bf16(reinterpret_cast<const bf16*>(vp)[16 * j]);
+    gate = a.g[(tok0 + t) * Hv + w.h];
+    beta = a.beta[(tok0 + t) * Hv + w.h];
+  };
+  if (w.T > 0) load_token(0);
+  char* op = static_cast<char*>(a.o) + (tok0 * o_tok + (int64_t)w.h * Dv + w.row + r) * ES;
+  auto put_o = [&](int t) {
+    if (g == 0) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (F32) reinterpret_cast<float*>(op + t * o_tok * ES)[16 * j] = o[j];
+        else reinterpret_cast<bf16*>(op + t * o_tok * ES)[16 * j] = to_bf16(o[j]);
+      }
+    }
+  };
+  if (step_refused(a, w)) {
+    // the outputs say so, the pages stay as they are
+    if (lane == 0) pool_error(P);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j] = __builtin_nanf("");
+    for (int t = 0; t < w.T; ++t) put_o(t);
     return;
   }
-  if (T == 0 && to == slot) return;
+  char* hb = hbuf[wave];
+  head_zeros<DK, F32>(hb);
+  for (int t = 0; t < w.T; ++t) {
+    head_to_lds<DK, F32>(hb, share);
+    const float kq = head_kq<DK, F32>(hb, r, g), alpha = expf(gate) * d, bt = beta;
+    float vt[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) vt[j] = v[j];
+    step_tile<DK, FMT, F32, NT>(
+        P, hb, raw, alpha, bt, kq, a.scale, vt, o, d, a.readout != 0,
+        [&]() {
+          if (t + 1 < w.T) load_token(t + 1);
+        },
+        [&](float m) {
+          if constexpr (WPT > 1) {
+            // the buffers alternate, so one barrier per token is enough: a wave
+            // that writes xm[t & 1] again has passed the barrier of token t + 1,
+            // which every wave reaches after reading xm[t & 1]
+            if (lane == 0) xm[t & 1][wave] = m;
+            lds_barrier();
+#pragma unroll
+            for (int i = 0; i < NW; ++i) m = fmaxf(m, xm[t & 1][i]);
+          }
+          return m;
+        });
+    put_o(t);
+  }
+  if (w.to < 0) return;                         // the state is not kept
+  uint8_t* dst = P.data + (a.layer_page + w.to) * P.page + head;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) *reinterpret_cast<u32x4*>(dst + 16 * j * DK + 64 * s) = raw[j][s];
+  if (lane == 0 && w.row % P.block_v == 0) P.scales[(a.layer_page + w.to) * P.tiles + tile] = d;
+}
 
-  float S[NLD][EPL];
-#pragma unroll
-  for (int j = 0; j < NLD; ++j) {
-    if constexpr (FMT != 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) codes4<FMT>(raw[j][i], *reinterpret_cast<float(*)[4]>(&S[j][4 * i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL / 4; ++i) {
-        const f32x4 x = __builtin_bit_cast(f32x4, raw[j * (EPL / 4) + i]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[j][4 * i + e] = x[e];
-      }
-    }
-  }
-  const char* qp = static_cast<const char*>(a.q) + ((int64_t)n * a.T * a.qs + (int64_t)hk * DK) * ES;
-  const char* kp = static_cast<const char*>(a.k) + ((int64_t)n * a.T * a.ks + (int64_t)hk * DK) * ES;
-  const char* vp = static_cast<const char*>(a.v) + ((int64_t)n * a.T * a.vs + (int64_t)h * Dv + row0) * ES;
-  auto ld_keys = [&](const char* p, float (&x)[EPL]) {
-    if constexpr (FMT != 0) {
-      ld_run<EPL, F32>(p + 16 * c * ES, x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL / 4; ++i)
-        ld_run<4, F32>(p + (32 * i + 4 * c) * ES, *reinterpret_cast<float(*)[4]>(&x[4 * i]));
-    }
+// One token per sequence, the usual call: persistent groups of waves, WPT
+// waves to a scale tile, that run over their elements (sequence, head, `span`
+// tiles of it) and load the next tile's codes and the next head's inputs
+// before they compute the current ones. A wave that is launched per tile
+// waits for its slot, then for its codes, with nothing else in flight.
+template <int DK, int FMT, bool F32, int NT, int WPT, bool AFTER>
+__global__ void __launch_bounds__((WPT == 1 ? 4 : WPT) * WAVE, 3)
+pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk) {
+  using H = HeadLds<DK, F32>;
+  constexpr int NW = WPT == 1 ? 4 : WPT, NS = DK / 64, ES = H::ES, RPW = 16 * NT, BV = WPT * RPW;
+  __shared__ __attribute__((aligned(16))) char hbuf[NW][H::BYTES];
+  __shared__ float xm[2][NW];
+  const PoolRef& P = a.pool;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = __lane_id();
+  const int sub = wave % WPT, r = lane & 15, g = lane >> 4;
+  const int Hv = P.Hv, hp = Hv << lparts, span = 1 << lspan;
+  const int tph = 1 << (lspan + lparts);               // tiles per head
+  int e = (blockIdx.x * (NW / WPT) + wave / WPT) * chunk;
+  const int end = min(e + chunk, elems);
+  if (e >= end) return;
+  char* hb = hbuf[wave];
+  head_zeros<DK, F32>(hb);
+  const int row_in = sub * RPW + r, loff = row_in * DK + 16 * g;
+  // an element's place: first tile, inputs, page read (uniform)
+  struct Place {
+    const uint8_t* src;
+    const float* scale;
+    const char* v;
+    int n, h, tile, slot, to;
   };
-  for (int t = 0; t < T; ++t) {
-    float k[EPL], q[EPL], v[NLD], o[NLD];
-    ld_keys(kp + (int64_t)t * a.ks * ES, k);
-    ld_keys(qp + (int64_t)t * a.qs * ES, q);
-    ld_run<NLD, F32>(vp + (int64_t)t * a.vs * ES, v);
-    const int64_t gi = ((int64_t)n * a.T + t) * Hv + h;
-    const float alpha = expf(a.g[gi]) * d, beta = a.beta[gi];
-    float kq = 0.f;
+  int seq, ph;
+  auto place = [&](int slot, int to) {
+    Place x;
+    x.n = seq;
+    x.h = ph >> lparts;
+    x.tile = (ph & ((1 << lparts) - 1)) << lspan;
+    x.slot = slot;
+    x.to = to;
+    const int64_t page = a.layer_page + slot, tile = x.h * tph + x.tile;
+    x.src = P.data + page * P.page + tile * (BV * DK);
+    x.scale = P.scales + page * P.tiles + tile;
+    x.v = static_cast<const char*>(a.v) + ((int64_t)seq * a.vs + tile * BV) * ES;
+    return x;
+  };
+  uint32_t share[H::LB / 4];
+  float gn = 0.f, bn = 0.f;
+  auto load_head = [&](const Place& x) {
+    load_share<DK, F32>(a, x.n, x.h / (Hv / a.Hqk), share);
+    gn = a.g[(int64_t)x.n * Hv + x.h];
+    bn = a.beta[(int64_t)x.n * Hv + x.h];
+  };
+  u32x4 rawn[NT][NS];
+  float dn = 1.f;
+  uint32_t vn[NT];
+  auto load_tile = [&](const Place& x, int t) {
+    const uint8_t* src = x.src + t * (BV * DK);
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) kq = fmaf(k[e], q[e], kq);
-    kq = sum_row<LPR>(kq);
-    float m = 0.f;
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < NLD; ++j) {
-      float p = 0.f, w = 0.f;
+      for (int s = 0; s < NS; ++s)
+        rawn[j][s] = *reinterpret_cast<const u32x4*>(src + (loff + 16 * j * DK + 64 * s));
+    dn = x.scale[t];
+    const char* vp = x.v + t * (BV * ES);
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        p = fmaf(S[j][e], k[e], p);
-        w = fmaf(S[j][e], q[e], w);
-      }
-      p = sum_row<LPR>(p);
-      w = sum_row<LPR>(w);
-      const float u = beta * fmaf(-alpha, p, v[j]);
-      o[j] = a.scale * fmaf(kq, u, alpha * w);
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        S[j][e] = fmaf(k[e], u, alpha * S[j][e]);
-        m = fmaxf(m, fabsf(S[j][e]));
-      }
-    }
-    if constexpr (FMT != 0) {
-      m = wave_max(m);
-      if (wpt > 1) {
-        // the buffers alternate, so one barrier per token is enough: a wave
-        // that writes xm[t & 1] again has passed the barrier of token t + 1,
-        // which every wave reaches after reading xm[t & 1]
-        if (lane == 0) xm[t & 1][wave] = m;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NW; ++i) m = fmaxf(m, xm[t & 1][i]);
-      }
-      d = qdq_scale<FMT>(m);
-      const float r = 1.0f / d;
-#pragma unroll
-      for (int j = 0; j < NLD; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          raw[j][i] = quant_word<FMT>(*reinterpret_cast<float(*)[4]>(&S[j][4 * i]), r);
-    }
-    if (a.readout != 0) {
-#pragma unroll
-      for (int j = 0; j < NLD; ++j) {
-        float w = 0.f;
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) w = fmaf(S[j][e], q[e], w);
-        o[j] = a.scale * (d * sum_row<LPR>(w));
-      }
-    }
-    if (c == 0) st_run<NLD, F32>(static_cast<char*>(a.o) + (o_off + t * o_tok) * ES, o);
+    for (int j = 0; j < NT; ++j)
+      vn[j] = F32 ? reinterpret_cast<const uint32_t*>(vp)[row_in + 16 * j]
+                  : reinterpret_cast<const uint16_t*>(vp)[row_in + 16 * j];
+  };
+  seq = __builtin_amdgcn_readfirstlane(e / hp);
+  ph = e - seq * hp;
+  const int slot0 = a.slots[seq];
+  Place nxt = place(slot0, a.slots_out ? a.slots_out[seq] : slot0);
+  if (nxt.slot >= 0 && nxt.slot < P.slots) {
+    load_head(nxt);
+    load_tile(nxt, 0);
   }
-  if (to < 0) return;                           // the state is not kept
-  uint8_t* dst = P.data + (a.layer_page + to) * P.page;
-  if constexpr (FMT == 0) {
+  int checked = -1, turn = 0;
+  bool refused = false;
+  for (; e < end; ++e) {
+    const Place cur = nxt;
+    // the element after this one
+    const bool more = e + 1 < end;
+    if (more) {
+      int slot = cur.slot, to = cur.to;
+      if (++ph == hp) {
+        ph = 0;
+        ++seq;
+        slot = a.slots[seq];
+        to = a.slots_out ? a.slots_out[seq] : slot;
+      }
+      nxt = place(slot, to);
+    }
+    const bool fetch = more && nxt.slot >= 0 && nxt.slot < P.slots;
+    if (checked != cur.n) {
+      checked = cur.n;
+      refused = cur.slot < 0 || cur.slot >= P.slots || cur.to < -1 || cur.to >= P.slots ||
+                (cur.to >= 0 &&
+                 pool_claimed(a.slots, a.slots_out ? a.slots_out : a.slots, a.B, cur.n, cur.to, 0));
+      if (refused && cur.slot != -1 && lane == 0) pool_error(P);
+    }
+    char* op = static_cast<char*>(a.o) + ((int64_t)cur.n * Hv * tph + cur.h * tph + cur.tile) * (BV * ES);
+    auto put_o = [&](int t, const float (&o)[NT]) {
+      if (g == 0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if constexpr (F32) reinterpret_cast<float*>(op + t * (BV * ES))[row_in + 16 * j] = o[j];
+          else reinterpret_cast<bf16*>(op + t * (BV * ES))[row_in + 16 * j] = to_bf16(o[j]);
+        }
+      }
+    };
+    if (refused) {                                     // or no sequence here
+      if (cur.slot != -1) {
+        float nan[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) nan[j] = __builtin_nanf("");
+        for (int t = 0; t < span; ++t) put_o(t, nan);
+      }
+      if (fetch) {
+        load_head(nxt);
+        load_tile(nxt, 0);
+      }
+      continue;
+    }
+    head_to_lds<DK, F32>(hb, share);
+    const float decay = expf(gn), beta = bn, kq = AFTER ? 0.f : head_kq<DK, F32>(hb, r, g);
+    if (fetch) load_head(nxt);
+    const int64_t topage = a.layer_page + cur.to, ctile = cur.h * tph + cur.tile;
+    uint8_t* dst = P.data + topage * P.page + ctile * (BV * DK);
+    float* dscale = P.scales + topage * P.tiles + ctile;
+    for (int t = 0; t < span; ++t) {
+      u32x4 raw[NT][NS];
+      float v[NT], o[NT], d;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        v[j] = __builtin_bit_cast(float, F32 ? vn[j] : vn[j] << 16);   // not at the load: that would wait for it
+#pragma unroll
+        for (int s = 0; s < NS; ++s) raw[j][s] = rawn[j][s];
+      }
+      const float alpha = decay * dn;
+      step_tile<DK, FMT, F32, NT>(
+          P, hb, raw, alpha, beta, kq, a.scale, v, o, d, AFTER,
+          [&]() {
+            if (t + 1 < span) load_tile(cur, t + 1);
+            else if (fetch) load_tile(nxt, 0);
+          },
+          [&](float m) {
+            if constexpr (WPT > 1) {
+              // the buffers alternate, so one barrier per tile is enough
+              if (lane == 0) xm[turn][wave] = m;
+              lds_barrier();
+#pragma unroll
+              for (int i = 0; i < NW; ++i) m = fmaxf(m, xm[turn][i]);
+              turn ^= 1;
+            }
+            return m;
+          });
+      // the next tile's loads, and the last tile's stores, before this tile's
+      // stores: a later wait for the loads would wait for these stores too
+      vm_drain();
+      put_o(t, o);
+      if (cur.to >= 0) {
+        uint8_t* dt = dst + t * (BV * DK);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+            *reinterpret_cast<u32x4*>(dt + (loff + 16 * j * DK + 64 * s)) = raw[j][s];
+        if (lane == 0 && sub == 0) dscale[t] = d;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------ pages of FP32 states
+// Eight lanes per row, four keys of every 32 each, so that they touch whole
+// 128-byte lines in each load; a row sum is DK / 8 FMAs and three DPP adds. One
+// wave holds 8 NLD rows; waves are independent.
+template <int DK, bool F32, int NLD>
+__global__ void __launch_bounds__(4 * WAVE) pool_step_f32_kernel(PoolStepArgs a, int waves) {
+  constexpr int NV = DK / 32, EPL = 4 * NV, ES = F32 ? 4 : 2;
+  const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit >= waves) return;
+  const PoolRef& P = a.pool;
+  const int lane = __lane_id(), c = lane & 7;
+  const StepUnit w = step_unit(a, unit, 8 * NLD);
+  if (w.idle) return;
+  const int Hv = P.Hv, Dv = P.Dv, hk = w.h / (Hv / a.Hqk), row0 = w.row + (lane >> 3) * NLD;
+  const int64_t tok0 = (int64_t)w.n * a.T, o_tok = (int64_t)Hv * Dv;
+  const int64_t head = ((int64_t)w.h * Dv + row0) * DK + 4 * c;
+  f32x4 S[NLD][NV];
+  if (step_in_ok(a, w)) {
+    const float* src = reinterpret_cast<const float*>(P.data + (a.layer_page + w.slot) * P.page) + head;
 #pragma unroll
     for (int j = 0; j < NLD; ++j)
 #pragma unroll
-      for (int i = 0; i < EPL / 4; ++i)
-        raw[j * (EPL / 4) + i] = __builtin_bit_cast(
-            u32x4, f32x4{S[j][4 * i], S[j][4 * i + 1], S[j][4 * i + 2], S[j][4 * i + 3]});
+      for (int i = 0; i < NV; ++i) S[j][i] = *reinterpret_cast<const f32x4*>(src + j * DK + 32 * i);
   }
+  float k[EPL], q[EPL], v[NLD], o[NLD];
+  auto load_token = [&](int t) {
+    const char* kp = static_cast<const char*>(a.k) + ((tok0 + t) * a.ks + (int64_t)hk * DK + 4 * c) * ES;
+    const char* qp = static_cast<const char*>(a.q) + ((tok0 + t) * a.qs + (int64_t)hk * DK + 4 * c) * ES;
 #pragma unroll
-  for (int j = 0; j < (int)(sizeof(raw) / sizeof(raw[0])); ++j)
-    *reinterpret_cast<u32x4*>(dst + piece(j)) = raw[j];
-  if (FMT != 0 && lane == 0 && row_w % P.block_v == 0)
-    P.scales[(a.layer_page + to) * P.tiles + tile] = d;
+    for (int i = 0; i < NV; ++i) {
+      ld_run<4, F32>(kp + 32 * i * ES, *reinterpret_cast<float(*)[4]>(&k[4 * i]));
+      ld_run<4, F32>(qp + 32 * i * ES, *reinterpret_cast<float(*)[4]>(&q[4 * i]));
+    }
+    ld_run<NLD, F32>(static_cast<const char*>(a.v) + ((tok0 + t) * a.vs + (int64_t)w.h * Dv + row0) * ES, v);
+  };
+  if (w.T > 0) load_token(0);
+  char* op = static_cast<char*>(a.o) + (tok0 * o_tok + (int64_t)w.h * Dv + row0) * ES;
+  if (step_refused(a, w)) {
+    if (lane == 0) pool_error(P);
+#pragma unroll
+    for (int j = 0; j < NLD; ++j) o[j] = __builtin_nanf("");
+    if (c == 0)
+      for (int t = 0; t < w.T; ++t) st_run<NLD, F32>(op + t * o_tok * ES, o);
+    return;
+  }
+  for (int t = 0; t < w.T; ++t) {
+    if (t > 0) load_token(t);
+    const int64_t gi = (tok0 + t) * Hv + w.h;
+    const float alpha = expf(a.g[gi]), beta = a.beta[gi];
+    float kq = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) kq = fmaf(k[e], q[e], kq);
+    kq = sum_row(kq);
+#pragma unroll
+    for (int j = 0; j < NLD; ++j) {
+      float p = 0.f, x = 0.f;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        p = fmaf(S[j][e / 4][e % 4], k[e], p);
+        x = fmaf(S[j][e / 4][e % 4], q[e], x);
+      }
+      p = sum_row(p);
+      x = sum_row(x);
+      const float u = beta * fmaf(-alpha, p, v[j]);
+      o[j] = a.scale * fmaf(kq, u, alpha * x);       // both readouts: nothing is rounded on the way
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) S[j][e / 4][e % 4] = fmaf(k[e], u, alpha * S[j][e / 4][e % 4]);
+    }
+    if (c == 0) st_run<NLD, F32>(op + t * o_tok * ES, o);
+  }
+  if (w.to < 0) return;
+  float* dst = reinterpret_cast<float*>(P.data + (a.layer_page + w.to) * P.page) + head;
+#pragma unroll
+  for (int j = 0; j < NLD; ++j)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + j * DK + 32 * i) = S[j][i];
 }
 
-template <int DK, int FMT, bool F32, int RPW>
-hipError_t launch_rows(const PoolStepArgs& a, hipStream_t s) {
-  constexpr int NLD = RPW / StepMap<DK, FMT>::GR;
-  const int wpt = FMT != 0 ? a.pool.block_v / RPW : 1;
-  const int64_t waves = (int64_t)a.B * a.pool.Hv * (a.pool.Dv / RPW);
-  if (wpt <= 4) {
-    // tiles of one, two or four waves: workgroups of four, or of the tile
-    if (wpt == 2)
-      pool_step_kernel<DK, FMT, F32, NLD, 2><<<dim3((unsigned)(waves / 2)), 2 * WAVE, 0, s>>>(a, wpt, (int)waves);
-    else
-      pool_step_kernel<DK, FMT, F32, NLD, 4><<<dim3((unsigned)((waves + 3) / 4)), 4 * WAVE, 0, s>>>(a, wpt, (int)waves);
-  } else if (wpt == 8) {
-    pool_step_kernel<DK, FMT, F32, NLD, 8><<<dim3((unsigned)(waves / 8)), 8 * WAVE, 0, s>>>(a, wpt, (int)waves);
-  } else {
-    pool_step_kernel<DK, FMT, F32, NLD, 16><<<dim3((unsigned)(waves / 16)), 16 * WAVE, 0, s>>>(a, wpt, (int)waves);
+inline int ilog2(int x) {
+  int l = 0;
+  while (x > 1) {
+    x >>= 1;
+    ++l;
   }
-  return hipGetLastError();
+  return l;
+}
+
+template <int DK, int FMT, bool F32, int NT, int WPT>
+void launch_codes_wpt(const PoolStepArgs& a, hipStream_t s) {
+  constexpr int NW = WPT == 1 ? 4 : WPT;
+  if (a.T == 1 && !a.lens) {
+    // Groups that fit the device at three waves per SIMD. With at least as many
+    // heads, an element is a whole head, and at most two per group: one
+    // group for its share of all elements was slower at 1,024 sequences of 32
+    // heads (467 us against 439 with two and 442 with one).
+    const int tph = a.pool.Dv / a.pool.block_v, gpb = NW / WPT, heads = a.B * a.pool.Hv;
+    const int room = device_cus() * (12 / NW) * gpb, span = heads >= room ? tph : 1;
+    const int elems = heads * (tph / span), chunk = std::min(2, (elems + room - 1) / room);
+    const int blocks = ((elems + chunk - 1) / chunk + gpb - 1) / gpb;
+    if (a.readout)
+      pool_step_one_kernel<DK, FMT, F32, NT, WPT, true><<<dim3(blocks), NW * WAVE, 0, s>>>(
+          a, ilog2(span), ilog2(tph / span), elems, chunk);
+    else
+      pool_step_one_kernel<DK, FMT, F32, NT, WPT, false><<<dim3(blocks), NW * WAVE, 0, s>>>(
+          a, ilog2(span), ilog2(tph / span), elems, chunk);
+  } else {
+    const int waves = a.B * a.pool.Hv * (a.pool.Dv / (16 * NT));
+    pool_step_many_kernel<DK, FMT, F32, NT, WPT><<<dim3((waves + NW - 1) / NW), NW * WAVE, 0, s>>>(a, waves);
+  }
 }
 
 template <int DK, int FMT, bool F32>
-hipError_t launch_dk(const PoolStepArgs& a, hipStream_t s) {
-  if (FMT != 0 && a.pool.block_v == 16) return launch_rows<DK, FMT, F32, 16>(a, s);
-  return launch_rows<DK, FMT, F32, 32>(a, s);
+void launch_codes(const PoolStepArgs& a, hipStream_t s) {
+  switch (a.pool.block_v) {
+    case 16: return launch_codes_wpt<DK, FMT, F32, 1, 1>(a, s);
+    case 32: return launch_codes_wpt<DK, FMT, F32, 2, 1>(a, s);
+    case 64: return launch_codes_wpt<DK, FMT, F32, 2, 2>(a, s);
+    case 128: return launch_codes_wpt<DK, FMT, F32, 2, 4>(a, s);
+    default: return launch_codes_wpt<DK, FMT, F32, 2, 8>(a, s);
+  }
 }
 
-template <int DK, int FMT>
-hipError_t launch_fmt(const PoolStepArgs& a, hipStream_t s) {
-  return a.f32_io ? launch_dk<DK, FMT, true>(a, s) : launch_dk<DK, FMT, false>(a, s);
-}
-
-template <int DK>
-hipError_t launch_pool_step_dk(const PoolStepArgs& a, hipStream_t s) {
-  if (a.pool.fmt == 0) return launch_fmt<DK, 0>(a, s);
-  return a.pool.fmt == 1 ? launch_fmt<DK, 1>(a, s) : launch_fmt<DK, 2>(a, s);
+template <int DK, bool F32>
+void launch_dk(const PoolStepArgs& a, hipStream_t s) {
+  if (a.pool.fmt == 1) return launch_codes<DK, 1, F32>(a, s);
+  if (a.pool.fmt == 2) return launch_codes<DK, 2, F32>(a, s);
+  constexpr int NLD = 4;
+  const int waves = a.B * a.pool.Hv * (a.pool.Dv / (8 * NLD));
+  pool_step_f32_kernel<DK, F32, NLD><<<dim3((unsigned)((waves + 3) / 4)), 4 * WAVE, 0, s>>>(a, waves);
 }
 
 }  // namespace
 
 hipError_t launch_pool_step(const PoolStepArgs& a, hipStream_t s) {
-  return a.pool.Dk == 128 ? launch_pool_step_dk<128>(a, s) : launch_pool_step_dk<64>(a, s);
+  if (a.pool.Dk == 128) a.f32_io ? launch_dk<128, true>(a, s) : launch_dk<128, false>(a, s);
+  else a.f32_io ? launch_dk<64, true>(a, s) : launch_dk<64, false>(a, s);
+  return hipGetLastError();
 }
 
 }  // namespace gdn

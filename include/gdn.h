@@ -408,16 +408,26 @@ gdn_status gdn_decode_bwd(const gdn_decode_bwd_args* a, void* stream);
  * call. The calls allocate nothing, need no workspace and may be captured
  * into HIP graphs. Calls that touch the same pages must be ordered by the
  * caller (one stream, or events). */
+/* How a write evaluates a tile's scale d from its amax: amax / q_max rounded
+ * once, as everywhere else in this library, or amax times the FP32-rounded 1 /
+ * q_max, which is how PyTorch divides a GPU tensor by a number ("[2/4] GDN/KDA
+ * decode QAT with INT8 recurrent state", "Testing": rounded reciprocal
+ * multiplication as Torch scalar division). The two differ by one unit in the last place
+ * in some tiles; the second gives the bits of states quantized in PyTorch. */
+typedef enum { GDN_SCALE_DIVIDE = 0, GDN_SCALE_RECIPROCAL = 1 } gdn_scale_rule;
+
 typedef struct {
   int32_t layers, slots, Hv, Dk, Dv;
   int32_t state_fmt;           /* gdn_qdq_fmt                                 */
   int32_t block_v;
+  int32_t scale_rule;          /* gdn_scale_rule (ignored when OFF)           */
   void* data;
   float* scales;
 } gdn_pool;
 
 /* states [n, Hv, Dk, Dv] FP32 (the layout of h0 and ht) -> pages of `layer`:
- * the state as written, QDQ codes and scales bit-exact to gdn_qdq_state. */
+ * the state as written, codes and scales bit-exact to gdn_qdq_state (with
+ * GDN_SCALE_DIVIDE). */
 gdn_status gdn_pool_write(const gdn_pool* pool, int32_t layer, const int32_t* slots, int32_t n,
                           const float* states, void* stream);
 

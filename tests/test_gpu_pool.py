@@ -131,6 +131,32 @@ def test_write_equals_the_standalone_quantizer():
     assert torch.equal(B.gdn_pool_read(pool, 0, _ints([0, 1, 2, 3, 4])), y.view(5, 4, 128, 128))
 
 
+@pytest.mark.parametrize("fmt,qmax", [(E4M3, 448.0), (INT8, 127.0)])
+def test_reciprocal_scales_are_those_of_pytorch(fmt, qmax):
+    """SCALE_RECIPROCAL: the bits of a state quantized in PyTorch on the GPU,
+    whose division of a tensor by a number is a product with its reciprocal."""
+    x = torch.randn(40, 3, 64, 128, device='cuda') * torch.rand(40, 3, 1, 1, device='cuda')
+    pool = B.StatePool(1, 40, 3, 64, 128, fmt, 16, scale_rule=B.SCALE_RECIPROCAL)
+    B.gdn_pool_write(pool, 0, _ints(list(range(40))), x)
+    t = x.mT.reshape(40, 3, 8, 16 * 64)
+    amax = t.abs().amax(-1)
+    d = amax * torch.tensor(1.0 / qmax, device='cuda')
+    assert torch.equal(pool.scales[0], d) and torch.equal(d, amax / qmax)
+    y = t * (1.0 / d).unsqueeze(-1)
+    c = y.clamp(-448, 448).to(torch.float8_e4m3fn) if fmt == E4M3 else y.round().clamp(-127, 127).to(torch.int8)
+    assert _same(pool.data[0], c.view(40, 3, 128, 64))
+    other = B.StatePool(1, 40, 3, 64, 128, fmt, 16)
+    B.gdn_pool_write(other, 0, _ints(list(range(40))), x)
+    assert float(((other.scales - pool.scales).abs() / other.scales).max()) <= 2.0 ** -22
+    # the step writes by the same rule: scales of the two pools differ by at most the rounding
+    z = _draw(40, 1, 1, 3, 64, 128, torch.bfloat16, seed=40)
+    again = B.StatePool.from_tensors(pool.data.clone(), pool.scales.clone(), fmt, 16)
+    B.gdn_pool_step(pool, 0, _ints(list(range(40))), **z)
+    B.gdn_pool_step(again, 0, _ints(list(range(40))), **z)
+    off = (again.scales - pool.scales).abs() / again.scales
+    assert 0 < float(off.max()) <= 2.0 ** -22
+
+
 @pytest.mark.parametrize("fmt", [E4M3, OFF])
 def test_write_refuses_bad_slots(fmt):
     pool = _random_pool(fmt, 1, 6, 2, 64, 64, 64)

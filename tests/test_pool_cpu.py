@@ -13,7 +13,7 @@ FAKE = 0x10000                                   # aligned, never dereferenced o
 
 
 def _pool(**kw):
-    p = B.PoolStruct(2, 5, 4, 128, 128, B.QDQ_E4M3, 64, FAKE, FAKE)
+    p = B.PoolStruct(2, 5, 4, 128, 128, B.QDQ_E4M3, 64, B.SCALE_DIVIDE, FAKE, FAKE)
     for k, v in kw.items():
         setattr(p, k, v)
     return p
@@ -34,6 +34,7 @@ BAD_POOL = [
     (dict(Dv=512), B.GDN_E_UNSUPPORTED, 'Dv'),
     (dict(block_v=48), B.GDN_E_UNSUPPORTED, 'block_v'),
     (dict(block_v=256), B.GDN_E_INVALID, 'divide'),
+    (dict(scale_rule=2), B.GDN_E_INVALID, 'scale_rule'),
     (dict(scales=None), B.GDN_E_INVALID, 'scales is NULL'),
     (dict(scales=FAKE + 4), B.GDN_E_INVALID, 'scales is not'),
     (dict(data=None), B.GDN_E_INVALID, 'data is NULL'),
@@ -152,7 +153,7 @@ def test_beam_select_checks_its_arguments(kw, status, msg):
 
 
 def test_beam_workspace_covers_every_part():
-    """12 bytes and K keys of 8 bytes per (row, split), rounded up; 0 for
+    """8 bytes and K keys of 8 bytes per (row, split), rounded up; 0 for
     arguments that the call refuses."""
     lib = B.load_library()
     a = _beam(B=1, W=4, V=131072, K=8)
