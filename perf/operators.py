@@ -146,8 +146,9 @@ def _bytes(t):
 def _handle(s, fmt, bv):
     """The pool handle that a serving program keeps."""
     if own:
-        from gateddeltanet_chunked_recurrence_amd import StatePool
-        s["pool"] = StatePool.from_tensors(s["data"], s["scales"], state_fmt=fmt, block_v=bv)
+        from gateddeltanet_chunked_recurrence_amd import SCALE_RECIPROCAL, StatePool
+        # _quantize divides the amax by a number, which PyTorch does on the GPU as a product with its reciprocal
+        s["pool"] = StatePool.from_tensors(s["data"], s["scales"], state_fmt=fmt, block_v=bv, scale_rule=SCALE_RECIPROCAL)
     return s
 
 
