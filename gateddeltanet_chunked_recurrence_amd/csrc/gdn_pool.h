@@ -9,24 +9,25 @@ __device__ __forceinline__ void pool_error(const PoolRef& p) {
   __hip_atomic_fetch_or(p.err, kErrPoolSlot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Whether entry `n` may write slot `dst`: no other entry j that does
-// something (in[j] >= lo and out[j] >= 0) may read it (in[j]) or write it
-// (out[j]). Every wave that writes a part of the page asks this, with the
+// Whether another entry than `n` reads (in[j]) or writes (out[j]) slot `dst`,
+// so that entry `n` may not write it. COPY: entries do something where out[j]
+// >= 0 (in -1 clears the page); otherwise where in[j] >= 0, and an entry with out
+// -1 still reads. Every wave that writes a part of the page asks this, with the
 // same answer in each, so an index given twice leaves the page as it was
 // instead of a mixture of two results. All 64 lanes call it together; each
 // takes four entries per load (the arrays are 16-byte aligned), and four
 // loads are in flight at once: 1,024 entries cost one round trip to L2. The
 // last vector is read again by lanes past it (asking twice changes nothing).
-// Several waves may ask for a part of the entries each and join the answers.
+template <bool COPY>
 __device__ __forceinline__ bool pool_claimed(const int32_t* in, const int32_t* out, int count, int n,
-                                             int dst, int lo, int part = 0, int parts = 1) {
+                                             int dst) {
   typedef int i32x4 __attribute__((ext_vector_type(4)));
   const int lane = __lane_id(), nv = count >> 2;
   bool hit = false;
   auto test = [&](int j, int a, int b) {
-    hit |= (j != n) & (a >= lo) & (b >= 0) & ((a == dst) | (b == dst));
+    hit |= (j != n) & (COPY ? (a >= -1) & (b >= 0) : a >= 0) & ((a == dst) | (b == dst));
   };
-  for (int v0 = 4 * WAVE * part; v0 < nv; v0 += 4 * WAVE * parts) {
+  for (int v0 = 0; v0 < nv; v0 += 4 * WAVE) {
     i32x4 a[4], b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -44,7 +45,7 @@ __device__ __forceinline__ bool pool_claimed(const int32_t* in, const int32_t* o
           test(4 * min(v0 + u * WAVE + lane, nv - 1) + e, a[u][e], in != out ? b[u][e] : a[u][e]);
   }
   const int j = 4 * nv + lane;
-  if (part == 0 && j < count) test(j, in[j], out[j]);
+  if (j < count) test(j, in[j], out[j]);
   return __ballot(hit) != 0;
 }
 

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(512) pool_write_kernel(PoolRef P, int64_t laye
   f32x4 x[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = *reinterpret_cast<const f32x4*>(src + (int64_t)(key + i) * P.Dv);
-  if (slot < 0 || slot >= P.slots || pool_claimed(slots, slots, count, w.n, slot, 0)) {
+  if (slot < 0 || slot >= P.slots || pool_claimed<false>(slots, slots, count, w.n, slot)) {
     if (lane == 0) pool_error(P);
     return;
   }
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(256) pool_f32_kernel(PoolRef P, int64_t layer_
   const int slot = slots[n];
   if (WRITE && slot == -1) return;
   bool ok = slot >= 0 && slot < P.slots;
-  if (WRITE && ok) ok = !pool_claimed(slots, slots, count, n, slot, 0);
+  if (WRITE && ok) ok = !pool_claimed<false>(slots, slots, count, n, slot);
   if (!ok && slot != -1 && lane == 0) pool_error(P);
   if (WRITE && !ok) return;
   const int64_t page_off = ok ? (layer_page + slot) * P.page : 0;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kMoveThreads) pool_copy_kernel(PoolRef P, cons
   const int from = src[m], to = dst[m];
   if (to == -1 || from == to) return;
   if (from < -1 || from >= P.slots || to < 0 || to >= P.slots ||
-      pool_claimed(src, dst, count, m, to, -1)) {
+      pool_claimed<true>(src, dst, count, m, to)) {
     if (lane == 0) pool_error(P);
     return;
   }
@@ -250,7 +250,7 @@ pool_reorder_kernel(PoolRef P, const int32_t* slots, const int32_t* parents, int
   for (int w = 0; w < width; ++w) {
     if (!__builtin_amdgcn_readlane((int)(wants && !bad), w)) continue;
     const int s = __builtin_amdgcn_readlane(my_slot, w);
-    if (pool_claimed(slots, slots, total, grp * width + w, s, 0) && lane == w) bad = true;
+    if (pool_claimed<false>(slots, slots, total, grp * width + w, s) && lane == w) bad = true;
   }
   if (bad) pool_error(P);
   const bool moves = wants && !bad;

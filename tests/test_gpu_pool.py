@@ -371,6 +371,23 @@ def test_step_refuses_bad_slots(fmt, bv):
     assert _pool_same(big, snap, [1, 299]) and not _pool_same(big, snap, [0])
 
 
+@pytest.mark.parametrize("fmt,bv,lens", [(E4M3, 64, False), (INT8, 128, True), (OFF, 64, False)])
+def test_step_refuses_to_write_a_page_that_another_only_reads(fmt, bv, lens):
+    """slots_out -1 keeps no state, but its page is read all the same."""
+    Hv, D = 2, 128
+    pool, want = (_random_pool(fmt, 1, 8, Hv, D, D, bv, seed=14) for _ in range(2))
+    snap = _snapshot(pool)
+    x = _draw(5, 1, 1, Hv, D, D, torch.bfloat16, seed=15)
+    n = dict(lens=_ints([1] * 5)) if lens else {}
+    # 1 is read by entry 1 and would be written by entry 0; 3 is read by entries 2 and 4, not written
+    o = B.gdn_pool_step(pool, 0, _ints([0, 1, 3, 5, 3]), slots_out=_ints([1, -1, -1, 5, -1]), **n, **x)
+    assert B.device_errors() == B.DEVERR_POOL_SLOT
+    o2 = B.gdn_pool_step(want, 0, _ints([-1, 1, 3, 5, 3]), slots_out=_ints([-1, -1, -1, 5, -1]), **n, **x)
+    assert B.device_errors() == 0
+    assert bool(o[0].isnan().all()) and torch.equal(o[1:], o2[1:])
+    assert _pool_same(pool, _snapshot(want)) and _pool_same(pool, snap, [0, 1, 2, 3, 4, 6, 7])
+
+
 # ------------------------------------------------------------- page moves
 MOVES = [(E4M3, 3, 4, 128, 128, 64), (INT8, 2, 3, 64, 64, 16), (OFF, 1, 1, 64, 64, 64), (E4M3, 1, 5, 128, 256, 256),
          (OFF, 2, 2, 128, 64, 64), (E4M3, 1, 1, 64, 64, 64)]
