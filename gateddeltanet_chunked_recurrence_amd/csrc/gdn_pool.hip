@@ -21,7 +21,9 @@ constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126, the scale of a zero t
 // kg = lane >> 4) holds columns 4 cq .. + 3 of keys 16 kg .. + 15: 16-byte FP32
 // accesses, 256 contiguous bytes per key, and 16-byte code accesses, 64
 // contiguous bytes per value row; the transposition between the key-major
-// states and the value-major pages is then only the choice of registers.
+// states and the value-major pages is then only the choice of registers. 64
+// sequences of 16 heads of 128 x 128 (67 MB of FP32, 17 MB of codes): 16.7 us to
+// pages, 14.5 from them, 5.0 and 5.8 TB/s.
 template <int DK>
 struct XchgPos {
   int n, h, col, key;
@@ -181,7 +183,13 @@ __global__ void __launch_bounds__(256) pool_f32_kernel(PoolRef P, int64_t layer_
 
 // ------------------------------------------------------------ page copies
 // One workgroup per (part of a page, move, layer); 16 bytes per lane and
-// access, U accesses in flight. The last part is the page's scales.
+// access, U accesses each. The last part is the page's scales. The loads go
+// out before the slots are checked for being named twice, the stores after.
+// Stores are non-temporal, loads are not: 60 forks of 12 layers (208 MB read
+// once and written, pages of 256 KB) take 39 us so (5.3 TB/s; a large linear
+// copy reaches 5.6 to 6.6 on this card), 45 with plain stores, 58 with
+// non-temporal loads too (a parent is read several times) or with the check
+// before the loads; 49 with one access per lane, 39.5 with eight.
 constexpr int kMoveThreads = 256;
 
 template <int U>
@@ -191,32 +199,34 @@ __global__ void __launch_bounds__(kMoveThreads) pool_copy_kernel(PoolRef P, cons
   const int part = blockIdx.x, m = blockIdx.y, layer = blockIdx.z, lane = __lane_id();
   const int from = src[m], to = dst[m];
   if (to == -1 || from == to) return;
-  if (from < -1 || from >= P.slots || to < 0 || to >= P.slots ||
-      pool_claimed<true>(src, dst, count, m, to)) {
+  const int64_t base = (int64_t)layer * P.slots;
+  const bool ok = from >= -1 && from < P.slots && to >= 0 && to < P.slots;
+  u32x4 x[U];
+  const int64_t off = (int64_t)part * (U * kMoveThreads * 16) + threadIdx.x * 16;
+  if (part < parts) {
+    const uint8_t* s = P.data + (base + from) * P.page + off;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      x[i] = u32x4{0, 0, 0, 0};
+      if (ok && from >= 0 && off + (int64_t)i * (kMoveThreads * 16) < P.page)
+        x[i] = *reinterpret_cast<const u32x4*>(s + i * (kMoveThreads * 16));
+    }
+  }
+  if (!ok || pool_claimed<true>(src, dst, count, m, to)) {
     if (lane == 0) pool_error(P);
     return;
   }
-  const int64_t base = (int64_t)layer * P.slots;
   if (part == parts) {
     float* d = P.scales + (base + to) * P.tiles;
     for (int i = threadIdx.x; i < P.tiles; i += kMoveThreads)
       d[i] = from < 0 ? kTinyScale : P.scales[(base + from) * P.tiles + i];
     return;
   }
-  const int64_t off = (int64_t)part * (U * kMoveThreads * 16) + threadIdx.x * 16;
-  const uint8_t* s = P.data + (base + from) * P.page + off;
   uint8_t* d = P.data + (base + to) * P.page + off;
-  u32x4 x[U];
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    x[i] = u32x4{0, 0, 0, 0};
-    if (from >= 0 && off + (int64_t)i * (kMoveThreads * 16) < P.page)
-      x[i] = *reinterpret_cast<const u32x4*>(s + i * (kMoveThreads * 16));
-  }
 #pragma unroll
   for (int i = 0; i < U; ++i)
     if (off + (int64_t)i * (kMoveThreads * 16) < P.page)
-      *reinterpret_cast<u32x4*>(d + i * (kMoveThreads * 16)) = x[i];
+      __builtin_nontemporal_store(x[i], reinterpret_cast<u32x4*>(d + i * (kMoveThreads * 16)));
 }
 
 // ------------------------------------------------------------- reordering
@@ -225,69 +235,71 @@ __global__ void __launch_bounds__(kMoveThreads) pool_copy_kernel(PoolRef P, cons
 // bytes), so no page is read after it was written and no staging copy is
 // needed; each page that changes is written once and each parent read once
 // from HBM (a second beam of the same parent hits a cache). Beams that keep
-// their own page move nothing. U parts per lane keep loads in flight where W
-// is small.
+// their own page move nothing. 16 groups of 4 beams, 12 layers (268 MB): 49 us
+// (5.4 TB/s); with plain stores 64, with one part per lane 55.
 template <int W, int U>
 __global__ void __launch_bounds__(kMoveThreads)
 pool_reorder_kernel(PoolRef P, const int32_t* slots, const int32_t* parents, int width, int parts) {
   const int part = blockIdx.x, grp = blockIdx.y, layer = blockIdx.z, lane = __lane_id();
-  const int32_t* mine = slots + grp * width;
-  const int32_t* par = parents + grp * width;
   const int total = gridDim.y * width;
   // the beams' slots and parents, one lane each
-  int my_slot = -1, my_par = -1;
+  int slot = -1, par = -1;
   if (lane < width) {
-    my_slot = mine[lane];
-    my_par = par[lane];
+    slot = slots[grp * width + lane];
+    par = parents[grp * width + lane];
   }
   // a beam moves when it has a page, a parent and they differ
-  const bool wants = lane < width && my_slot != -1 && my_par != -1 && my_par != lane;
-  const int from_lane = my_par >= 0 && my_par < width ? my_par : 0;
-  const int my_from = __shfl(my_slot, from_lane, WAVE);
-  bool bad = wants && (my_par < 0 || my_par >= width || my_slot < 0 || my_slot >= P.slots ||
-                       my_from < 0 || my_from >= P.slots);
-  // slots named twice: lanes of one wave scan all entries for each moving beam
-  for (int w = 0; w < width; ++w) {
-    if (!__builtin_amdgcn_readlane((int)(wants && !bad), w)) continue;
-    const int s = __builtin_amdgcn_readlane(my_slot, w);
-    if (pool_claimed<false>(slots, slots, total, grp * width + w, s) && lane == w) bad = true;
-  }
-  if (bad) pool_error(P);
-  const bool moves = wants && !bad;
-  const uint64_t any = __ballot(moves);
-  if (any == 0) return;
+  const bool wants = slot != -1 && par != -1 && par != lane;
+  const int from = __shfl(slot, par >= 0 && par < width ? par : 0, WAVE);
+  bool bad = wants && (par < 0 || par >= width || slot < 0 || slot >= P.slots || from < 0 || from >= P.slots);
+  const uint64_t loads = __ballot(wants && !bad);
   const int64_t base = (int64_t)layer * P.slots;
+  const int64_t off = (int64_t)part * (U * kMoveThreads * 16) + threadIdx.x * 16;
+  u32x4 x[W][U];
+  if (part < parts) {
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      if ((loads >> w) & 1) {
+        const uint8_t* s = P.data + (base + __builtin_amdgcn_readlane(from, w)) * P.page + off;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (off + (int64_t)i * (kMoveThreads * 16) < P.page)
+            x[w][i] = *reinterpret_cast<const u32x4*>(s + i * (kMoveThreads * 16));
+      }
+  }
+  // slots named twice: the lanes scan all entries, for every moving beam at once
+  uint32_t hits = 0;
+  for (int j = lane; j < total; j += WAVE) {
+    const int other = slots[j];
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      if (((loads >> w) & 1) && other == __builtin_amdgcn_readlane(slot, w) && j != grp * width + w) hits |= 1u << w;
+  }
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    if (((loads >> w) & 1) && __ballot((hits >> w) & 1) && lane == w) bad = true;
+  if (bad) pool_error(P);
+  const uint64_t any = __ballot(wants && !bad);
   if (part == parts) {
     for (int i = threadIdx.x; i < P.tiles; i += kMoveThreads) {
-      float x[W];
+      float y[W];
 #pragma unroll
       for (int w = 0; w < W; ++w)
-        if ((any >> w) & 1) x[w] = P.scales[(base + __builtin_amdgcn_readlane(my_from, w)) * P.tiles + i];
+        if ((any >> w) & 1) y[w] = P.scales[(base + __builtin_amdgcn_readlane(from, w)) * P.tiles + i];
 #pragma unroll
       for (int w = 0; w < W; ++w)
-        if ((any >> w) & 1) P.scales[(base + __builtin_amdgcn_readlane(my_slot, w)) * P.tiles + i] = x[w];
+        if ((any >> w) & 1) P.scales[(base + __builtin_amdgcn_readlane(slot, w)) * P.tiles + i] = y[w];
     }
     return;
   }
-  const int64_t off = (int64_t)part * (U * kMoveThreads * 16) + threadIdx.x * 16;
-  u32x4 x[W][U];
 #pragma unroll
   for (int w = 0; w < W; ++w)
     if ((any >> w) & 1) {
-      const uint8_t* s = P.data + (base + __builtin_amdgcn_readlane(my_from, w)) * P.page + off;
+      uint8_t* d = P.data + (base + __builtin_amdgcn_readlane(slot, w)) * P.page + off;
 #pragma unroll
       for (int i = 0; i < U; ++i)
         if (off + (int64_t)i * (kMoveThreads * 16) < P.page)
-          x[w][i] = *reinterpret_cast<const u32x4*>(s + i * (kMoveThreads * 16));
-    }
-#pragma unroll
-  for (int w = 0; w < W; ++w)
-    if ((any >> w) & 1) {
-      uint8_t* d = P.data + (base + __builtin_amdgcn_readlane(my_slot, w)) * P.page + off;
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (off + (int64_t)i * (kMoveThreads * 16) < P.page)
-          *reinterpret_cast<u32x4*>(d + i * (kMoveThreads * 16)) = x[w][i];
+          __builtin_nontemporal_store(x[w][i], reinterpret_cast<u32x4*>(d + i * (kMoveThreads * 16)));
     }
 }
 
@@ -356,6 +368,7 @@ hipError_t launch_pool_copy(const PoolRef& p, const int32_t* src, const int32_t*
   return hipGetLastError();
 }
 
+// The bucket of the width; narrow groups take several parts per lane.
 hipError_t launch_pool_reorder(const PoolRef& p, const int32_t* slots, const int32_t* parents,
                                int groups, int width, hipStream_t s) {
   if (width <= 4) return reorder_launch<4, 4>(p, slots, parents, groups, width, s);
