@@ -33,6 +33,19 @@
 // (Dv 256, 1.8 GB in and out), bound the step: 460 us.
 // Pages of FP32 states move four times the bytes; their sums stay on the
 // vector ALUs.
+//
+// Measured, E4M3 with bf16 inputs, read from one page and written to another: 1,024
+// sequences of 32 heads (128 x 256) 439 us, 4.1 TB/s; a plain copy of the same pages
+// at random places takes 360 to 400, this loop without its stores 303, with nothing but
+// loads and stores 445. 192 sequences of 16 heads (128 x 128) 25 us, 3.2 TB/s:
+// about two tiles per wave, so loads and stores of the ends stand alone.
+// One sequence 5.4 us: a launch and one trip to HBM after the slots. Dropped: two
+// tiles ahead at two waves per SIMD 508 us (spills at three), tiles unquantized twice
+// instead of held at four waves 457, non-temporal stores 474, one wave per
+// tile without the loop 530 to 555. Inputs in FP32 take 27 us where bf16 takes
+// 25: the parts of k and q are made once per head, in LDS (53 us when every
+// tile split them again). INT8 at 192 sequences: 36 us, the conversions to bf16 by
+// way of floats bind it.
 #include <algorithm>
 
 #include "gdn_device.h"
@@ -51,64 +64,17 @@ __device__ __forceinline__ float sum_row(float x) {
   return x;
 }
 
-// N consecutive bf16 or FP32 elements at p (aligned to their size, at most 16
-// bytes per access).
-template <int N, bool F32>
-__device__ __forceinline__ void ld_run(const void* p, float (&x)[N]) {
-  if constexpr (F32) {
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < N / 4; ++i) {
-        const f32x4 v = reinterpret_cast<const f32x4*>(p)[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[4 * i + e] = v[e];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = reinterpret_cast<const float*>(p)[i];
-    }
-  } else if constexpr (N % 8 == 0) {
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      const bf16x8 v = reinterpret_cast<const bf16x8*>(p)[i];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[8 * i + e] = from_bf16(v[e]);
-    }
-  } else if constexpr (N == 4) {
-    const bf16x4 v = *reinterpret_cast<const bf16x4*>(p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = from_bf16(v[e]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = from_bf16(reinterpret_cast<const bf16*>(p)[i]);
-  }
+// Four consecutive bf16 or FP32 elements.
+template <bool F32>
+__device__ __forceinline__ f32x4 load4(const void* p) {
+  if constexpr (F32) return *reinterpret_cast<const f32x4*>(p);
+  const bf16x4 v = *reinterpret_cast<const bf16x4*>(p);
+  return f32x4{from_bf16(v[0]), from_bf16(v[1]), from_bf16(v[2]), from_bf16(v[3])};
 }
-
-template <int N, bool F32>
-__device__ __forceinline__ void st_run(void* p, const float (&x)[N]) {
-  if constexpr (F32) {
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < N / 4; ++i)
-        reinterpret_cast<f32x4*>(p)[i] = f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) reinterpret_cast<float*>(p)[i] = x[i];
-    }
-  } else if constexpr (N % 8 == 0) {
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      bf16x8 v;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = to_bf16(x[8 * i + e]);
-      reinterpret_cast<bf16x8*>(p)[i] = v;
-    }
-  } else if constexpr (N == 4) {
-    *reinterpret_cast<bf16x4*>(p) = bf16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) reinterpret_cast<bf16*>(p)[i] = to_bf16(x[i]);
-  }
+template <bool F32>
+__device__ __forceinline__ void store4(void* p, f32x4 x) {
+  if constexpr (F32) *reinterpret_cast<f32x4*>(p) = x;
+  else *reinterpret_cast<bf16x4*>(p) = bf16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
 }
 
 // What every wave of a call does first: its sequence, head and rows, whether
@@ -149,13 +115,13 @@ __device__ __forceinline__ bf16 split_part(float x, int m) {
   return m == 0 ? h : m == 1 ? mid : m == 2 ? low : to_bf16(0.f);
 }
 
-// A wave's LDS: k and q as they come, zeros, and k laid out for the update:
+// A wave's LDS: k and q (FP32: also their bf16 parts), zeros, and k laid out for the update:
 // for result tile x = 4 s + c and row m, the A row of key 64 s + 16 (m >> 2) + 4 c
 // + (m & 3): bf16 (k, k, k, 0...), FP32 the parts (k1, k1, k1, k2, k2, k3, 0, 0).
 template <int DK, bool F32>
 struct HeadLds {
   static constexpr int ES = F32 ? 4 : 2, HB = 2 * DK * ES, LB = HB / WAVE;
-  static constexpr int ZERO = HB, ROWS = HB + DK * ES, BYTES = ROWS + 16 * DK;
+  static constexpr int ZERO = HB, PARTS = HB + DK * ES, ROWS = PARTS + (F32 ? 6 * DK * 2 : 0), BYTES = ROWS + 16 * DK;
 };
 
 // Writes a head's LDS from the lanes' shares of k and q (LB bytes each).
@@ -166,6 +132,16 @@ __device__ __forceinline__ void head_to_lds(char* hb, const uint32_t* share) {
   if constexpr (H::LB == 16) *reinterpret_cast<u32x4*>(hb + lane * 16) = u32x4{share[0], share[1], share[2], share[3]};
   else if constexpr (H::LB == 8) *reinterpret_cast<uint2*>(hb + lane * 8) = make_uint2(share[0], share[1]);
   else *reinterpret_cast<uint32_t*>(hb + lane * 4) = share[0];
+  if constexpr (F32) {
+    // a lane holds DK / 32 keys of k (lanes below 32) or q: their three parts, [which][part][key]
+#pragma unroll
+    for (int i = 0; i < DK / 32; ++i) {
+      const float x = __builtin_bit_cast(float, share[i]);
+      bf16* p = reinterpret_cast<bf16*>(hb + H::PARTS) + (lane >> 5) * 3 * DK + (lane & 31) * (DK / 32) + i;
+#pragma unroll
+      for (int m = 0; m < 3; ++m) p[m * DK] = split_part(x, m);
+    }
+  }
   // a lane below 32 holds DK / 32 keys of k
   if (lane < 32) {
 #pragma unroll
@@ -203,16 +179,10 @@ __device__ __forceinline__ void head_zeros(char* hb) {
 template <int DK, bool F32>
 __device__ __forceinline__ bf16x8 sum_row_of(const char* hb, int r, int g, int s, int i, int which) {
   using H = HeadLds<DK, F32>;
-  if constexpr (F32) {
-    const float* p = reinterpret_cast<const float*>(hb + which * (H::HB / 2)) + 64 * s + 16 * g + 8 * i;
-    bf16x8 x;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = split_part(p[c], r & 3);
-    return x;
-  } else {
-    const char* p = hb + ((r & 2) ? H::ZERO : (r & 1) * (H::HB / 2));
-    return *reinterpret_cast<const bf16x8*>(p + (64 * s + 16 * g + 8 * i) * 2);
-  }
+  int row;
+  if constexpr (F32) row = (r & 3) == 3 ? H::ZERO : H::PARTS + (which * 3 + (r & 3)) * DK * 2;
+  else row = (r & 2) ? H::ZERO : (r & 1) * (H::HB / 2);
+  return *reinterpret_cast<const bf16x8*>(hb + row + (64 * s + 16 * g + 8 * i) * 2);
 }
 
 // k . q, in every lane.
@@ -258,7 +228,11 @@ __device__ __forceinline__ void step_tile(const PoolRef& P, const char* hb, u32x
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) b[j][s][i] = codes8_bf16<FMT>(raw[j][s][2 * i], raw[j][s][2 * i + 1]);
+        for (int i = 0; i < 2; ++i) {
+          b[j][s][i] = codes8_bf16<FMT>(raw[j][s][2 * i], raw[j][s][2 * i + 1]);
+          // integers go through floats: eight at a time, not all at once
+          if constexpr (FMT == 2) __builtin_amdgcn_sched_barrier(0);
+        }
   };
   float p[NT], q[NT];
   auto row_sums = [&]() {
@@ -344,6 +318,7 @@ __device__ __forceinline__ void step_tile(const PoolRef& P, const char* hb, u32x
     for (int x = 0; x < 4 * NS; ++x) {
       const float y[4] = {S[j][x][0], S[j][x][1], S[j][x][2], S[j][x][3]};
       raw[j][x >> 2][x & 3] = quant_word<FMT>(y, rd);
+      if constexpr (FMT == 2) __builtin_amdgcn_sched_barrier(0);
     }
   if (after) {
     decode();
@@ -646,77 +621,94 @@ pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk
 // ------------------------------------------------------ pages of FP32 states
 // Eight lanes per row, four keys of every 32 each, so that they touch whole
 // 128-byte lines in each load; a row sum is DK / 8 FMAs and three DPP adds. One
-// wave holds 8 NLD rows; waves are independent.
-template <int DK, bool F32, int NLD>
+// wave holds kRows32 rows, four per eight lanes; waves are independent. 90
+// sequences of up to 5 tokens, 6 heads of 64 x 64 (9 MB in, 9 out): 7.6 us, 8.2
+// without the next token's loads ahead; bound by latency (four waves per CU).
+constexpr int kRows32 = 32;
+template <int DK, bool F32>
 __global__ void __launch_bounds__(4 * WAVE) pool_step_f32_kernel(PoolStepArgs a, int waves) {
-  constexpr int NV = DK / 32, EPL = 4 * NV, ES = F32 ? 4 : 2;
+  constexpr int NV = DK / 32, ES = F32 ? 4 : 2, NR = kRows32 / 8;
+  static_assert(NR == 4, "one vector of v and o per lane");
   const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (unit >= waves) return;
   const PoolRef& P = a.pool;
   const int lane = __lane_id(), c = lane & 7;
-  const StepUnit w = step_unit(a, unit, 8 * NLD);
+  const StepUnit w = step_unit(a, unit, kRows32);
   if (w.idle) return;
-  const int Hv = P.Hv, Dv = P.Dv, hk = w.h / (Hv / a.Hqk), row0 = w.row + (lane >> 3) * NLD;
+  const int Hv = P.Hv, Dv = P.Dv, hk = w.h / (Hv / a.Hqk), row0 = w.row + (lane >> 3) * NR;
   const int64_t tok0 = (int64_t)w.n * a.T, o_tok = (int64_t)Hv * Dv;
   const int64_t head = ((int64_t)w.h * Dv + row0) * DK + 4 * c;
-  f32x4 S[NLD][NV];
+  f32x4 S[NR][NV];
   if (step_in_ok(a, w)) {
     const float* src = reinterpret_cast<const float*>(P.data + (a.layer_page + w.slot) * P.page) + head;
 #pragma unroll
-    for (int j = 0; j < NLD; ++j)
+    for (int j = 0; j < NR; ++j)
 #pragma unroll
       for (int i = 0; i < NV; ++i) S[j][i] = *reinterpret_cast<const f32x4*>(src + j * DK + 32 * i);
   }
-  float k[EPL], q[EPL], v[NLD], o[NLD];
+  f32x4 k[NV], q[NV], v, o;
+  float gate = 0.f, beta = 0.f;
   auto load_token = [&](int t) {
     const char* kp = static_cast<const char*>(a.k) + ((tok0 + t) * a.ks + (int64_t)hk * DK + 4 * c) * ES;
     const char* qp = static_cast<const char*>(a.q) + ((tok0 + t) * a.qs + (int64_t)hk * DK + 4 * c) * ES;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      ld_run<4, F32>(kp + 32 * i * ES, *reinterpret_cast<float(*)[4]>(&k[4 * i]));
-      ld_run<4, F32>(qp + 32 * i * ES, *reinterpret_cast<float(*)[4]>(&q[4 * i]));
+      k[i] = load4<F32>(kp + 32 * i * ES);
+      q[i] = load4<F32>(qp + 32 * i * ES);
     }
-    ld_run<NLD, F32>(static_cast<const char*>(a.v) + ((tok0 + t) * a.vs + (int64_t)w.h * Dv + row0) * ES, v);
+    v = load4<F32>(static_cast<const char*>(a.v) + ((tok0 + t) * a.vs + (int64_t)w.h * Dv + row0) * ES);
+    gate = a.g[(tok0 + t) * Hv + w.h];
+    beta = a.beta[(tok0 + t) * Hv + w.h];
   };
   if (w.T > 0) load_token(0);
   char* op = static_cast<char*>(a.o) + (tok0 * o_tok + (int64_t)w.h * Dv + row0) * ES;
   if (step_refused(a, w)) {
     if (lane == 0) pool_error(P);
-#pragma unroll
-    for (int j = 0; j < NLD; ++j) o[j] = __builtin_nanf("");
+    const float nan = __builtin_nanf("");
     if (c == 0)
-      for (int t = 0; t < w.T; ++t) st_run<NLD, F32>(op + t * o_tok * ES, o);
+      for (int t = 0; t < w.T; ++t) store4<F32>(op + t * o_tok * ES, f32x4{nan, nan, nan, nan});
     return;
   }
   for (int t = 0; t < w.T; ++t) {
-    if (t > 0) load_token(t);
-    const int64_t gi = (tok0 + t) * Hv + w.h;
-    const float alpha = expf(a.g[gi]), beta = a.beta[gi];
+    const float alpha = expf(gate), bt = beta;
+    f32x4 kt[NV], qt[NV], vt = v;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      kt[i] = k[i];
+      qt[i] = q[i];
+    }
+    if (t + 1 < w.T) load_token(t + 1);          // while this token is computed
     float kq = 0.f;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) kq = fmaf(k[e], q[e], kq);
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) kq = fmaf(kt[i][e], qt[i][e], kq);
     kq = sum_row(kq);
 #pragma unroll
-    for (int j = 0; j < NLD; ++j) {
+    for (int j = 0; j < NR; ++j) {
       float p = 0.f, x = 0.f;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        p = fmaf(S[j][e / 4][e % 4], k[e], p);
-        x = fmaf(S[j][e / 4][e % 4], q[e], x);
-      }
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p = fmaf(S[j][i][e], kt[i][e], p);
+          x = fmaf(S[j][i][e], qt[i][e], x);
+        }
       p = sum_row(p);
       x = sum_row(x);
-      const float u = beta * fmaf(-alpha, p, v[j]);
+      const float u = bt * fmaf(-alpha, p, vt[j]);
       o[j] = a.scale * fmaf(kq, u, alpha * x);       // both readouts: nothing is rounded on the way
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) S[j][e / 4][e % 4] = fmaf(k[e], u, alpha * S[j][e / 4][e % 4]);
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[j][i][e] = fmaf(kt[i][e], u, alpha * S[j][i][e]);
     }
-    if (c == 0) st_run<NLD, F32>(op + t * o_tok * ES, o);
+    if (c == 0) store4<F32>(op + t * o_tok * ES, o);
   }
   if (w.to < 0) return;
   float* dst = reinterpret_cast<float*>(P.data + (a.layer_page + w.to) * P.page) + head;
 #pragma unroll
-  for (int j = 0; j < NLD; ++j)
+  for (int j = 0; j < NR; ++j)
 #pragma unroll
     for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + j * DK + 32 * i) = S[j][i];
 }
@@ -739,7 +731,7 @@ void launch_codes_wpt(const PoolStepArgs& a, hipStream_t s) {
     // group for its share of all elements was slower at 1,024 sequences of 32
     // heads (467 us against 439 with two and 442 with one).
     const int tph = a.pool.Dv / a.pool.block_v, gpb = NW / WPT, heads = a.B * a.pool.Hv;
-    const int room = device_cus() * (12 / NW) * gpb, span = heads >= room ? tph : 1;
+    const int room = device_cus() * std::max(1, 12 / NW) * gpb, span = heads >= room ? tph : 1;
     const int elems = heads * (tph / span), chunk = std::min(2, (elems + room - 1) / room);
     const int blocks = ((elems + chunk - 1) / chunk + gpb - 1) / gpb;
     if (a.readout)
@@ -754,14 +746,19 @@ void launch_codes_wpt(const PoolStepArgs& a, hipStream_t s) {
   }
 }
 
+// 16-row tiles per wave: two, or one where the integer format's conversions
+// would spill at 128 keys (192 sequences of 16 heads, Dv 128, tiles of 32, 64 and
+// 128: 32, 35 and 53 us with one, 57, 65 and 74 with two; E4M3 28, 29 and 35 with
+// one, 26, 26 and 30 with two).
 template <int DK, int FMT, bool F32>
 void launch_codes(const PoolStepArgs& a, hipStream_t s) {
+  constexpr int NT = FMT == 2 && DK == 128 ? 1 : 2;
   switch (a.pool.block_v) {
     case 16: return launch_codes_wpt<DK, FMT, F32, 1, 1>(a, s);
-    case 32: return launch_codes_wpt<DK, FMT, F32, 2, 1>(a, s);
-    case 64: return launch_codes_wpt<DK, FMT, F32, 2, 2>(a, s);
-    case 128: return launch_codes_wpt<DK, FMT, F32, 2, 4>(a, s);
-    default: return launch_codes_wpt<DK, FMT, F32, 2, 8>(a, s);
+    case 32: return launch_codes_wpt<DK, FMT, F32, NT, 2 / NT>(a, s);
+    case 64: return launch_codes_wpt<DK, FMT, F32, NT, 4 / NT>(a, s);
+    case 128: return launch_codes_wpt<DK, FMT, F32, NT, 8 / NT>(a, s);
+    default: return launch_codes_wpt<DK, FMT, F32, NT, 16 / NT>(a, s);
   }
 }
 
@@ -769,9 +766,8 @@ template <int DK, bool F32>
 void launch_dk(const PoolStepArgs& a, hipStream_t s) {
   if (a.pool.fmt == 1) return launch_codes<DK, 1, F32>(a, s);
   if (a.pool.fmt == 2) return launch_codes<DK, 2, F32>(a, s);
-  constexpr int NLD = 4;
-  const int waves = a.B * a.pool.Hv * (a.pool.Dv / (8 * NLD));
-  pool_step_f32_kernel<DK, F32, NLD><<<dim3((unsigned)((waves + 3) / 4)), 4 * WAVE, 0, s>>>(a, waves);
+  const int waves = a.B * a.pool.Hv * (a.pool.Dv / kRows32);
+  pool_step_f32_kernel<DK, F32><<<dim3((unsigned)((waves + 3) / 4)), 4 * WAVE, 0, s>>>(a, waves);
 }
 
 }  // namespace
