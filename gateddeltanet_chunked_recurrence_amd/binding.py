@@ -525,15 +525,22 @@ def _need(t, name, dtype, shape, dev):
                          f'{"" if t.is_contiguous() else ", not contiguous"}')
 
 
+# The current stream's handle; without building a Stream object where torch
+# has the shorter way (2 us of a call's 7).
+_raw_stream = getattr(torch._C, '_cuda_getCurrentRawStream',
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(fn, dev, *args):
     """fn(*args, stream) on dev, its current stream and as the current device."""
     if dev.type != 'cuda':
         raise ValueError(f'tensors must be on a GPU, not on {dev}')
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(index))
     if status:
         _check(status)
 
