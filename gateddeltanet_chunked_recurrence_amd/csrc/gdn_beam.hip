@@ -10,12 +10,20 @@
 // lane, all in flight at once) and leaves the part's maximum, its sum of
 // exponentials and its K largest logits with their tokens. The second kernel,
 // one workgroup per request, joins the parts: log-sums per beam, totals of
-// the candidates, the K best. Bound: reading the logits once from HBM.
+// the candidates, the K best. Bound: reading the logits once from HBM. 512 rows
+// of 100,003 bf16 logits (102 MB): 41 us, of which the parts 31.5 and the join 9.4;
+// the reading alone takes 19, with the maxima and exponentials (hidden behind it)
+// 22.5, and choosing adds the rest: three exchanges over LDS that each wait for
+// the slowest wave. 4 rows of
+// 131,072: 12 us (5.7 and 6.4), two launches and their dependent loads.
 //
-// The K largest of a part: the K-th largest of the workgroup's 256 lane maxima
-// is a bound that at least K elements reach, found by bisection over the upper
-// 16 bits of an order-preserving integer (16 rounds of four ballots; a bound too
-// low by less than one such step only lets a few more elements through).
+// The K largest of a part: a bound that at least K elements reach, from the
+// 256 lane maxima: the K-th largest of one wave's 64 is one (the best of the four
+// is taken), and the least of the four waves' ceil(K / 4)-th largest another,
+// closer one where the large elements are spread out. Each is found by
+// bisection over the upper bits (12 and 16) of an order-preserving integer, a
+// ballot per bit; a bound too low by less than one step only lets a few more
+// elements through.
 // Elements that reach it (little more than K) go to a list in LDS, where each
 // finds its rank by counting. Only a list that overflows (many equal logits)
 // takes the slow way, K passes that each find the next element in order.
@@ -23,8 +31,10 @@
 // the order in which the list was filled.
 //
 // Sums: FP32 within a part (at most 64 terms per lane, then a tree), FP64
-// across parts and for the totals. An exponent is exp2((x - m) log2(e)) with
-// the difference taken first, so its error is relative to x - m.
+// across parts and for the totals. An exponential is 2^(x L - C) with L =
+// fl(log2 e) and C = fl(m L), one FMA, rounded relative to the small difference;
+// that C and L are rounded themselves is taken back in FP64 at the end (see
+// log_sum).
 #include "gdn_device.h"
 #include "gdn_launch.h"
 
@@ -33,7 +43,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / WAVE;
-constexpr int kList = 512;                       // candidates of one part kept in LDS
+constexpr int kList = 128;                       // candidates that one wave keeps in LDS
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kMaxF = 3.4028234663852886e38f;
 
@@ -51,8 +61,8 @@ __device__ __forceinline__ uint64_t pick_key(float x, int token) {
   return (uint64_t)ord32(x) << 32 | (uint32_t)~token;
 }
 
-// The largest t of BITS upper bits such that at least `want` of the N keys per
-// lane are >= t << (32 - BITS) (keys: ord32 of values).
+// The largest t of BITS upper bits such that at least `want` of the keys are
+// >= t << (32 - BITS) (keys: ord32 of values; one per lane, or N per lane).
 template <int BITS, int N>
 __device__ __forceinline__ uint32_t kth_bound(const uint32_t (&key)[N], int want) {
   uint32_t t = 0;
@@ -65,6 +75,44 @@ __device__ __forceinline__ uint32_t kth_bound(const uint32_t (&key)[N], int want
     if (n >= want) t = c;
   }
   return t;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;    // L; L / log2(e) - 1 = kLDelta
+constexpr double kLDelta = (double)kLog2e / 1.4426950408889634074 - 1.0;
+constexpr float kBig = 0x1p100f;
+// The exponent base of maximum m, and 2^(x L - base): beyond 2^100 (masks of the
+// type's lowest value, or +inf) the products would overflow, and the difference
+// is taken first.
+__device__ __forceinline__ float base_of(float m) { return fabsf(m) < kBig ? m * kLog2e : m; }
+__device__ __forceinline__ float share_of(float x, float m, float base) {
+  return fabsf(m) < kBig ? fexp2(fmaf(x, kLog2e, -base)) : fexp2((x - m) * kLog2e);
+}
+// The factor that brings a sum from maximum m to maximum M >= m.
+__device__ __forceinline__ float rescale(float m, float M) {
+  if (fabsf(m) < kBig && fabsf(M) < kBig) return fexp2(m * kLog2e - M * kLog2e);
+  return fexp2((m - M) * kLog2e);
+}
+// log sum exp(x) - M of a sum s of shares of maximum M: ln 2 log2(s) plus what
+// the base was rounded by, fl(M L) / log2(e) - M, minus what the rounding of L adds, which
+// is kLDelta times the mean of x: M, but for kLDelta times their distance (1e-7).
+__device__ __forceinline__ double log_sum(double s, float M) {
+  if (!(fabsf(M) < kBig)) return log(s);
+  const double ln2 = 0.69314718055994530942;
+  return log(s) + ((double)(M * kLog2e) * ln2 - (double)M) - kLDelta * (double)M;
+}
+
+// A double moved between lanes by a DPP pattern (see dpp_f).
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// The set lanes of a mask below this one.
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
 // The sum over the 64 lanes, in every lane: DPP within rows of 16, then the
@@ -103,9 +151,9 @@ template <bool F32, int E>
 __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
   constexpr int ES = F32 ? 4 : 2, VE = 16 / ES;
   __shared__ float sm[kWaves], ss[kWaves];
-  __shared__ __attribute__((aligned(16))) uint32_t tops[kThreads];
-  __shared__ uint64_t list[kList], best;
-  __shared__ int count;
+  __shared__ uint32_t sb[kWaves][2];
+  __shared__ uint64_t list[kWaves][kList], best;
+  __shared__ int counts[kWaves];
   const int row = blockIdx.x / a.splits, split = blockIdx.x - row * a.splits, tid = threadIdx.x;
   const int wave = tid >> 6, lane = tid & 63;
   if (a.finished && a.finished[row]) return;
@@ -114,7 +162,6 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
   const int off = (int)((reinterpret_cast<uintptr_t>(base) & 15) / ES);
   const char* vec0 = base - (int64_t)off * ES;
   const int first = split * (E * kThreads) + tid;
-  if (tid == 0) count = 0;
   auto token0 = [&](int j) { return (first + j * kThreads) * VE - off; };   // of vector j's first element
   auto load = [&](int j) {
     const uint32_t ninf = F32 ? 0xFF800000u : 0xFF80FF80u;
@@ -154,13 +201,13 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
     }
     top = fmaxf(top, vtop[j]);
   }
-  constexpr float kLog2e = 1.4426950408889634f;
   // m: finite even where everything is masked, so that -inf - m is -inf
   float m = fmaxf(wave_max(top), -kMaxF), s = 0.f;
+  const float base0 = m * kLog2e;
 #pragma unroll
-  for (int i = 0; i < E * VE; ++i) s += fexp2((x[i] - m) * kLog2e);
-  // A NaN, or +inf (whose difference with itself is NaN), shows in the sum
-  if (__ballot(!(s <= kMaxF)) != 0) {
+  for (int i = 0; i < E * VE; ++i) s += fexp2(fmaf(x[i], kLog2e, -base0));
+  // Seldom: a NaN or +inf (both make the sum NaN), or a maximum beyond kBig
+  if (__ballot(!(s <= kMaxF) || !(fabsf(m) < kBig)) != 0) {
     top = -kInf;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
@@ -173,20 +220,28 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
       top = fmaxf(top, vtop[j]);
     }
     m = fmaxf(wave_max(top), -kMaxF);
+    const float base = base_of(m);
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < E * VE; ++i) s += fexp2((x[i] - m) * kLog2e);
+    for (int i = 0; i < E * VE; ++i) s += share_of(x[i], m, base);
   }
-  tops[tid] = ord32(top);
   s = wave_total(s);
+  const uint32_t tk[1] = {ord32(top)};
+  const uint32_t b0 = kth_bound<12>(tk, min(a.K, WAVE)), b1 = kth_bound<16>(tk, (a.K + kWaves - 1) / kWaves);
   if (lane == 0) {
     sm[wave] = m;
     ss[wave] = s;
+    sb[wave][0] = b0;
+    sb[wave][1] = b1;
   }
   __syncthreads();
-  const u32x4 t4 = *reinterpret_cast<const u32x4*>(tops + 4 * lane);
-  const uint32_t tk[4] = {t4[0], t4[1], t4[2], t4[3]};
-  const uint32_t bound = kth_bound<16>(tk, a.K);
+  uint32_t most = sb[0][0], least = sb[0][1];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) {
+    most = max(most, sb[i][0]);
+    least = min(least, sb[i][1]);
+  }
+  const uint32_t bound = max(most, least);
   // at least the smallest value above -inf (its upper 16 bits alone would let -inf through)
   const float reach = fmaxf(unord32(max(bound, ord32(-kInf))), -kMaxF);
   const int64_t part = (int64_t)row * a.splits + split;
@@ -197,35 +252,72 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
     for (int i = 1; i < kWaves; ++i) M = fmaxf(M, sm[i]);
     float S = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) S += ss[i] * fexp2((sm[i] - M) * kLog2e);
+    for (int i = 0; i < kWaves; ++i) S += ss[i] * rescale(sm[i], M);
     w.ms[part] = make_float2(M, S);
   }
+  // each wave's list: places by counting the lanes below, no atomics
+  int mine_n = 0;
   if (__ballot(top >= reach) != 0) {
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       if (__ballot(vtop[j] >= reach) == 0) continue;
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (x[j * VE + e] >= reach) {
-          const int p = atomicAdd(&count, 1);
-          if (p < kList) list[p] = pick_key(x[j * VE + e], token0(j) + e);
-        }
+      for (int e = 0; e < VE; ++e) {
+        const uint64_t hit = __ballot(x[j * VE + e] >= reach);
+        if (hit == 0) continue;
+        const int at = mine_n + lanes_below(hit);
+        if (x[j * VE + e] >= reach && at < kList) list[wave][at] = pick_key(x[j * VE + e], token0(j) + e);
+        mine_n += __builtin_popcountll(hit);
+      }
     }
   }
+  if (lane == 0) counts[wave] = mine_n;
   __syncthreads();
-  const int n = count;
+  int n = 0, longest = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    n += counts[i];
+    longest = max(longest, counts[i]);
+  }
   uint64_t* out = w.key + part * a.K;
-  if (n <= kList) {
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t mine = list[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += list[j] > mine;
-      if (rank < a.K) out[rank] = mine;
+  if (n <= WAVE) {
+    // the usual case: one wave, an element per lane, ranks by broadcasts
+    if (wave != 0) return;
+    int seg = 0, at = lane;
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i)
+      if (seg == i && at >= counts[i]) {
+        at -= counts[i];
+        ++seg;
+      }
+    const uint64_t mine = lane < n ? list[seg][at] : 0;
+    const int lo = (int)(uint32_t)mine, hi = (int)(uint32_t)(mine >> 32);
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, j) << 32 |
+                             (uint32_t)__builtin_amdgcn_readlane(lo, j);
+      rank += other > mine;
     }
-    for (int i = n + tid; i < a.K; i += kThreads) out[i] = 0;
+    if (lane < n) {
+      if (rank < a.K) out[rank] = mine;
+    } else if (lane < a.K) {
+      out[lane] = 0;
+    }
     return;
   }
-  // more ties than the list holds: the next element in order, K times, read
+  if (longest <= kList) {
+    for (int i = lane; i < mine_n; i += WAVE) {
+      const uint64_t mine = list[wave][i];
+      int rank = 0;
+      for (int o = 0; o < kWaves; ++o) {
+        const int c = counts[o];
+        for (int j = 0; j < c; ++j) rank += list[o][j] > mine;
+      }
+      if (rank < a.K) out[rank] = mine;
+    }
+    return;                                      // n > 64 >= K: every place is written
+  }
+  // more ties than a list holds: the next element in order, K times, read
   // again (the registers of the elements are given up by now)
   uint64_t prev = ~0ull;
   for (int found = 0; found < a.K; ++found) {
@@ -263,16 +355,18 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
 }
 
 // ONE: all candidates of a request fit kHeld per thread, and stay in registers.
-constexpr int kHeld = 12;
+constexpr int kHeld = 12, kParts = 1024;         // kParts: parts of a request kept in LDS
 template <bool ONE>
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
-  constexpr float kLog2e = 1.4426950408889634f;
   // total = (x - top) + shift, with the beam's largest logit and score - log
   // sum exp(x - top); shift -inf: no candidates
   __shared__ double topx[kBeamMaxW], shift[kBeamMaxW];
-  __shared__ Cand list[kList], best[kWaves];
+  __shared__ Cand list[kWaves][kList], best[kWaves];
   __shared__ __attribute__((aligned(16))) uint32_t tops[kThreads];
-  __shared__ int count;
+  __shared__ int counts[kWaves];
+  __shared__ float2 pms[kParts];
+  __shared__ float score_of[kBeamMaxW];
+  __shared__ uint8_t done_of[kBeamMaxW];
   const int b = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const Ws w = ws_of(a);
   const int per = a.splits * a.K, cand = a.W * per;
@@ -282,31 +376,38 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) held[u] = tid + u * kThreads < cand ? keys[tid + u * kThreads] : 0;
   }
-  if (tid == 0) count = 0;
-  for (int beam = wave; beam < a.W; beam += kWaves) {
-    const int row = b * a.W + beam;
-    const float score = a.scores[row];
-    double sh = -(double)kInf, tx = 0.0;
-    if (a.finished && a.finished[row]) {
-      sh = score;
-    } else {
-      const float2* ms = w.ms + (int64_t)row * a.splits;
-      float M = -kMaxF;
-      float2 f{-kMaxF, 0.f};
-      if (lane < a.splits) f = ms[lane];
-      for (int i = lane + WAVE; i < a.splits; i += WAVE) M = fmaxf(M, ms[i].x);
-      M = wave_max(fmaxf(M, f.x));
-      // each part's share relative to the largest: its FP32 error is that of
-      // an exponential of a difference, as within a part
-      double S = (double)(f.y * fexp2((f.x - M) * kLog2e));
-      for (int i = lane + WAVE; i < a.splits; i += WAVE) S += (double)(ms[i].y * fexp2((ms[i].x - M) * kLog2e));
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) S += __shfl_xor(S, o, WAVE);
-      tx = M;
-      if (S > 0.0) sh = (double)score - log(S);
+  // every part's maximum and sum, the scores and the flags, in one round trip
+  const int parts = a.W * a.splits;
+  const float2* ms = w.ms + (int64_t)b * parts;
+  for (int i = tid; i < parts && i < kParts; i += kThreads) pms[i] = ms[i];
+  if (tid < a.W) {
+    score_of[tid] = a.scores[b * a.W + tid];
+    done_of[tid] = a.finished ? a.finished[b * a.W + tid] : 0;
+  }
+  __syncthreads();
+  auto part_of = [&](int i) { return i < kParts ? pms[i] : ms[i]; };
+  // the log-sums: eight lanes per beam, all beams at once
+  static_assert(8 * kBeamMaxW <= kThreads, "eight lanes per beam");
+  if ((tid & ~63) < 8 * a.W) {
+    const int beam = min(tid >> 3, a.W - 1), sub = tid & 7;
+    float M = -kMaxF;
+    for (int i = sub; i < a.splits; i += 8) M = fmaxf(M, part_of(beam * a.splits + i).x);
+    M = fmaxf(M, dpp_f<0xB1>(M));
+    M = fmaxf(M, dpp_f<0x4E>(M));
+    M = fmaxf(M, dpp_f<0x141>(M));
+    // each part's share relative to the largest: its FP32 error is that of
+    // an exponential of a difference, as within a part
+    double S = 0.0;
+    for (int i = sub; i < a.splits; i += 8) {
+      const float2 f = part_of(beam * a.splits + i);
+      S += (double)(f.y * rescale(f.x, M));
     }
-    if (lane == 0) {
-      topx[beam] = tx;
+    S += dpp_d<0xB1>(S);
+    S += dpp_d<0x4E>(S);
+    S += dpp_d<0x141>(S);
+    const double score = (double)score_of[beam], sh = done_of[beam] ? score : S > 0.0 ? score - log_sum(S, M) : -(double)kInf;
+    if (sub == 0 && tid >> 3 < a.W) {
+      topx[beam] = done_of[beam] ? 0.0 : (double)M;
       shift[beam] = sh > -(double)kInf ? sh : -(double)kInf;
     }
   }
@@ -316,11 +417,13 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
     a.tokens[(int64_t)b * a.K + i] = -1;
   }
   __syncthreads();
+  // i / per: with at most kHeld kThreads candidates i per < 2^32, and the product is exact
+  const uint32_t magic = 0xFFFFFFFFu / (uint32_t)per + 1;
   auto get = [&](int i, uint64_t key, Cand& c) -> bool {
-    c.beam = i / per;
+    c.beam = ONE && per > 1 ? (int)__umulhi((uint32_t)i, magic) : i / per;
     const double sh = shift[c.beam];
     if (!(sh > -(double)kInf)) return false;
-    if (a.finished && a.finished[b * a.W + c.beam]) {
+    if (done_of[c.beam]) {
       c.total = sh;
       c.token = a.pad_token;
       return i == c.beam * per;
@@ -351,37 +454,74 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
   const u32x4 t4 = *reinterpret_cast<const u32x4*>(tops + 4 * lane);
   const uint32_t tk[4] = {t4[0], t4[1], t4[2], t4[3]};
   const uint32_t bound = max(kth_bound<20>(tk, a.K), 1u);
-  auto keep = [&](int i, uint64_t key) {
-    Cand c;
-    if (get(i, key, c) && ord32((float)c.total) >= bound) {
-      const int p = atomicAdd(&count, 1);
-      if (p < kList) list[p] = c;
-    }
+  int mine_n = 0;
+  auto keep = [&](int i, uint64_t key, bool likely) {
+    Cand c{};
+    const bool hit = likely && get(i, key, c) && ord32((float)c.total) >= bound;
+    const uint64_t lanes = __ballot(hit);
+    const int at = mine_n + lanes_below(lanes);
+    if (hit && at < kList) list[wave][at] = c;
+    mine_n += __builtin_popcountll(lanes);
   };
   if constexpr (ONE) {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u)
-      if (ck[u] >= bound) keep(tid + u * kThreads, held[u]);
+      if (__ballot(ck[u] >= bound) != 0) keep(tid + u * kThreads, held[u], ck[u] >= bound);
   } else {
-    for (int i = tid; i < cand; i += kThreads) keep(i, keys[i]);
+    for (int i0 = 0; i0 < cand; i0 += kThreads) keep(i0 + tid, i0 + tid < cand ? keys[i0 + tid] : 0, i0 + tid < cand);
   }
+  if (lane == 0) counts[wave] = mine_n;
   __syncthreads();
-  const int n = count;
+  int longest = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) longest = max(longest, counts[i]);
   auto put = [&](int rank, const Cand& c) {
     a.out_scores[(int64_t)b * a.K + rank] = (float)c.total;
     a.parents[(int64_t)b * a.K + rank] = c.beam;
     a.tokens[(int64_t)b * a.K + rank] = c.token;
   };
-  if (n <= kList) {
-    for (int i = tid; i < n; i += kThreads) {
-      const Cand mine = list[i];
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) n += counts[i];
+  if (n <= WAVE) {
+    // the usual case: one wave, a candidate per lane, ranks by broadcasts
+    if (wave != 0) return;
+    int seg = 0, at = lane;
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i)
+      if (seg == i && at >= counts[i]) {
+        at -= counts[i];
+        ++seg;
+      }
+    if (lane >= n) return;
+    const Cand mine = list[seg][at];
+    const uint64_t bits = __builtin_bit_cast(uint64_t, mine.total);
+    const int lo = (int)(uint32_t)bits, hi = (int)(uint32_t)(bits >> 32);
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      Cand c;
+      c.total = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, j) << 32 |
+                                               (uint32_t)__builtin_amdgcn_readlane(lo, j));
+      c.beam = __builtin_amdgcn_readlane(mine.beam, j);
+      c.token = __builtin_amdgcn_readlane(mine.token, j);
+      rank += before(c, mine);
+    }
+    if (rank < a.K) put(rank, mine);
+    return;
+  }
+  if (longest <= kList) {
+    for (int i = lane; i < mine_n; i += WAVE) {
+      const Cand mine = list[wave][i];
       int rank = 0;
-      for (int j = 0; j < n; ++j) rank += before(list[j], mine);
+      for (int o = 0; o < kWaves; ++o) {
+        const int c = counts[o];
+        for (int j = 0; j < c; ++j) rank += before(list[o][j], mine);
+      }
       if (rank < a.K) put(rank, mine);
     }
     return;
   }
-  // more equal totals than the list holds: the next candidate in order, K times
+  // more equal totals than a list holds: the next candidate in order, K times
   Cand prev{(double)kInf, -1, -1};
   for (int found = 0; found < a.K; ++found) {
     Cand mine{-(double)kInf, 0, 0};
@@ -414,8 +554,11 @@ void beam_plan(BeamArgs& a) {
   const int64_t rows = (int64_t)a.B * a.W;
   // one more vector than V / ve where a row starts off a 16-byte boundary
   const int64_t nv = (a.V + ve - 2) / ve + 1;
+  // As much per workgroup as leaves 64 of them: 4 rows of 131,072 bf16 logits take
+  // 12.6 us at one vector per lane (260 parts, whose candidates the second kernel
+  // reads), 11.7 at four (68) or eight (36); 512 rows of 100,003 take 90, 41 and 42.
   int e = 8;
-  while (e > 1 && rows * ((nv + e * kThreads - 1) / (e * kThreads)) < 1024) e /= 2;
+  while (e > 1 && rows * ((nv + e * kThreads - 1) / (e * kThreads)) < 64) e /= 2;
   a.vecs = e;
   a.splits = (int)((nv + e * kThreads - 1) / (e * kThreads));
 }
