@@ -1236,7 +1236,10 @@ gdn_status gdn_beam_select(const gdn_beam_args* a, void* stream) {
       {a->workspace, "workspace", false}};
   for (const auto& e : ptrs) {
     if (e.required && !e.p) return fail(GDN_E_INVALID, "gdn_beam_select: %s is NULL", e.name);
-    if (e.p && !aligned16(e.p)) return fail(GDN_E_INVALID, "gdn_beam_select: %s is not 16-byte aligned", e.name);
+    // rows of logits may start anywhere, so the first may too
+    const uintptr_t align = e.p == a->logits ? (a->io_dtype == GDN_F32 ? 4 : 2) : 16;
+    if (reinterpret_cast<uintptr_t>(e.p) % align)
+      return fail(GDN_E_INVALID, "gdn_beam_select: %s is not %d-byte aligned", e.name, (int)align);
   }
   if (!any) return GDN_OK;
   const gdn::BeamArgs k = beam_args(a);

@@ -498,7 +498,9 @@ typedef struct {
   int32_t io_dtype;            /* gdn_dtype of the logits                     */
   int32_t pad_token;
   int64_t row_stride;          /* elements between rows of logits; 0: V       */
-  const void* logits;          /* [B, W, V] (rows row_stride apart)           */
+  const void* logits;          /* [B, W, V] (rows row_stride apart; aligned to
+                                  an element only, so the last position of
+                                  [B, W, T, V] can be passed as it is)         */
   const float* scores;         /* [B, W]                                      */
   const uint8_t* finished;     /* [B, W] nonzero: finished; or NULL           */
   float* out_scores;           /* out [B, K]                                  */

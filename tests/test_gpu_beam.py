@@ -96,6 +96,31 @@ def test_rows_of_a_padded_vocabulary(dt):
     _check(x.view(3, 2, 500)[:, :1], s[::2].contiguous(), 3)
 
 
+@pytest.mark.parametrize("dt,Bn,W,V,K", [(torch.bfloat16, 3, 32, 40000, 64), (torch.float32, 1, 32, 280001, 64)])
+def test_many_candidates_per_request(dt, Bn, W, V, K):
+    """More candidates than a workgroup's registers hold; in the second case
+    more parts than its LDS does."""
+    say(f"beam select {dt} B={Bn} W={W} V={V} K={K}")
+    x, s = _logits(Bn, W, V, dt, seed=V)
+    _check(x, s * 0.05, K)
+    x[0].fill_(-3.0)                                      # all equal: the lowest tokens of the best beams
+    s = torch.zeros_like(s)
+    got = [t.cpu() for t in B.gdn_beam_select(x, s, K)]
+    assert got[1][0].tolist() == [0] * K and got[2][0].tolist() == list(range(K))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [1, 2, 9, 1003, 8191])
+def test_the_last_position_of_a_longer_block(dt, V):
+    """A view whose first row starts off a 16-byte boundary."""
+    T = 4 if V % 2 else 6
+    x, s = _logits(6, T, V, dt, seed=V)
+    x[:, :-1] = 99.0
+    last = x[:, -1].unflatten(0, (2, 3))
+    assert last.data_ptr() % 16 or V == 2
+    _check(last, s[:, 0].reshape(2, 3) * 0.1, 5)
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_masked_and_strange_logits(dt):
     V = 5000

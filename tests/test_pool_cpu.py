@@ -141,6 +141,8 @@ def _beam(**kw):
     (dict(io_dtype=5), B.GDN_E_INVALID, 'io_dtype'),
     (dict(row_stride=999), B.GDN_E_INVALID, 'row_stride'),
     (dict(logits=None), B.GDN_E_INVALID, 'logits is NULL'),
+    (dict(logits=FAKE + 1), B.GDN_E_INVALID, 'logits is not 2'),
+    (dict(logits=FAKE + 2, io_dtype=B.GDN_F32), B.GDN_E_INVALID, 'logits is not 4'),
     (dict(scores=FAKE + 4), B.GDN_E_INVALID, 'scores is not'),
     (dict(finished=FAKE + 1), B.GDN_E_INVALID, 'finished is not'),
     (dict(tokens=None), B.GDN_E_INVALID, 'tokens is NULL'),
