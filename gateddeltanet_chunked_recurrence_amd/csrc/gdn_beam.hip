@@ -11,11 +11,13 @@
 // exponentials and its K largest logits with their tokens. The second kernel,
 // one workgroup per request, joins the parts: log-sums per beam, totals of
 // the candidates, the K best. Bound: reading the logits once from HBM. 512 rows
-// of 100,003 bf16 logits (102 MB): 41 us, of which the parts 31.5 and the join 9.4;
+// of 100,003 bf16 logits (102 MB): 41 us, of which the parts 32.7 and the join 8.2;
 // the reading alone takes 19, with the maxima and exponentials (hidden behind it)
-// 22.5, and choosing adds the rest: three exchanges over LDS that each wait for
-// the slowest wave. 4 rows of
-// 131,072: 12 us (5.7 and 6.4), two launches and their dependent loads.
+// 22.5, and choosing adds the rest: scalar instructions, which a CU issues one at a
+// time, and three exchanges over LDS that each wait for the slowest wave. 4 rows
+// of 131,072: 12 us (5.9 and 6.4), two launches and their dependent loads. The same
+// 512 rows with all but 50 tokens masked: 48 us with -inf, 103 with the type's lowest
+// value (636 when equal logits were taken one by one).
 //
 // The K largest of a part: a bound that at least K elements reach, from the
 // 256 lane maxima: the K-th largest of one wave's 64 is one (the best of the four
@@ -25,8 +27,9 @@
 // ballot per bit; a bound too low by less than one step only lets a few more
 // elements through.
 // Elements that reach it (little more than K) go to a list in LDS, where each
-// finds its rank by counting. Only a list that overflows (many equal logits)
-// takes the slow way, K passes that each find the next element in order.
+// finds its rank by counting. Where a list overflows (a row's ragged end, or many
+// equal logits), the bound is bisected over all elements of the part; among those
+// equal to the K-th largest value, counts in token order give the places.
 // Elements are distinct by (value, token), so the result does not depend on
 // the order in which the list was filled.
 //
@@ -125,11 +128,14 @@ __device__ __forceinline__ float wave_total(float x) {
   return (read_lane(x, 0) + read_lane(x, 16)) + (read_lane(x, 32) + read_lane(x, 48));
 }
 
-// Workspace of one call: per (row, split) the maximum and the sum, and the K
-// best as keys (0 where there are fewer).
+// Workspace of one call: per (row, split) the maximum and the sum, and per
+// request the K best of its W * splits parts as keys (0 where there are fewer), all
+// parts' first, then all second and so on. The pitch of a rank is odd, so that
+// the join's threads, which take every 256th, meet all ranks of all parts.
 struct Ws {
   float2* ms;
   uint64_t* key;
+  int pitch;
 };
 __host__ __device__ inline int64_t up16(int64_t x) { return (x + 15) & ~int64_t(15); }
 __host__ __device__ inline Ws ws_of(const BeamArgs& a) {
@@ -138,6 +144,7 @@ __host__ __device__ inline Ws ws_of(const BeamArgs& a) {
   Ws w;
   w.ms = reinterpret_cast<float2*>(p);
   w.key = reinterpret_cast<uint64_t*>(p + up16(parts * 8));
+  w.pitch = (a.W * a.splits) | 1;
   return w;
 }
 
@@ -152,8 +159,8 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
   constexpr int ES = F32 ? 4 : 2, VE = 16 / ES;
   __shared__ float sm[kWaves], ss[kWaves];
   __shared__ uint32_t sb[kWaves][2];
-  __shared__ uint64_t list[kWaves][kList], best;
-  __shared__ int counts[kWaves];
+  __shared__ uint64_t list[kWaves][kList];
+  __shared__ int counts[kWaves], tally[2][kWaves], equals[E][kWaves];
   const int row = blockIdx.x / a.splits, split = blockIdx.x - row * a.splits, tid = threadIdx.x;
   const int wave = tid >> 6, lane = tid & 63;
   if (a.finished && a.finished[row]) return;
@@ -241,23 +248,25 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
     most = max(most, sb[i][0]);
     least = min(least, sb[i][1]);
   }
-  const uint32_t bound = max(most, least);
-  // at least the smallest value above -inf (its upper 16 bits alone would let -inf through)
-  const float reach = fmaxf(unord32(max(bound, ord32(-kInf))), -kMaxF);
-  const int64_t part = (int64_t)row * a.splits + split;
+  // at least the smallest value above -inf
+  const uint32_t bound = max(max(most, least), ord32(-kMaxF));
+  float M = sm[0];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) M = fmaxf(M, sm[i]);
   const Ws w = ws_of(a);
   if (tid == 0) {
-    float M = sm[0];
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) M = fmaxf(M, sm[i]);
     float S = 0.f;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) S += ss[i] * rescale(sm[i], M);
-    w.ms[part] = make_float2(M, S);
+    w.ms[(int64_t)row * a.splits + split] = make_float2(M, S);
   }
+  const int request = row / a.W, part = (row - request * a.W) * a.splits + split;
+  uint64_t* out = w.key + (int64_t)request * a.K * w.pitch + part;
+  auto put = [&](int rank, uint64_t key) { out[(int64_t)rank * w.pitch] = key; };
   // each wave's list: places by counting the lanes below, no atomics
   int mine_n = 0;
-  if (__ballot(top >= reach) != 0) {
+  if (__ballot(top >= unord32(bound)) != 0) {
+    const float reach = unord32(bound);
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       if (__ballot(vtop[j] >= reach) == 0) continue;
@@ -271,15 +280,111 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
       }
     }
   }
-  if (lane == 0) counts[wave] = mine_n;
-  __syncthreads();
   int n = 0, longest = 0;
+  auto count = [&]() {
+    if (lane == 0) counts[wave] = mine_n;
+    __syncthreads();
+    n = longest = 0;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    n += counts[i];
-    longest = max(longest, counts[i]);
+    for (int i = 0; i < kWaves; ++i) {
+      n += counts[i];
+      longest = max(longest, counts[i]);
+    }
+  };
+  count();
+  int first_free = a.K;                          // places from here on hold no candidate of the lists
+  if (longest > kList) {
+    // Seldom: the bound is too low for the lists. Raise it by bisection, all
+    // elements counted, until one list could hold those that reach it or it is
+    // the K-th largest value itself. The elements are read again and stay
+    // packed, so that this part takes no registers from the usual case.
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < E; ++j) raw[j] = load(j);
+    auto repack = [&]() {                        // not unpacked once for all the passes
+#pragma unroll
+      for (int j = 0; j < E; ++j) asm volatile("" : "+v"(raw[j]));
+    };
+    auto value = [&](int j, int e) { return plain(elem<F32>(raw[j], e)); };
+    uint32_t lo = bound, hi = ord32(M) + 1;      // n >= K elements reach lo, `above` < K reach hi
+    uint32_t c = hi - 1;                         // the maximum first: a masked part is all equal
+    int above = 0, turn = 0;
+    while (n > kList && hi - lo > 1) {
+      const float y = unord32(c);
+      repack();
+      // counts in lanes: with a ballot per element the scalar registers spill,
+      // in the usual case too (512 rows of 100,003: 36 us instead of 33)
+      float mine = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) mine += value(j, e) >= y ? 1.f : 0.f;
+      mine = wave_total(mine);
+      if (lane == 0) tally[turn][wave] = (int)mine;
+      __syncthreads();                           // the buffers alternate
+      int have = 0;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) have += tally[turn][i];
+      turn ^= 1;
+      if (have >= a.K) {
+        lo = c;
+        n = have;
+      } else {
+        hi = c;
+        above = have;
+      }
+      c = lo + (hi - lo) / 2;
+    }
+    repack();
+    if (n > kList) {
+      // more elements of the K-th largest value than a list holds: the places
+      // behind the larger ones go to the first of them by token
+      const float y = unord32(lo);
+      lo = hi;
+      first_free = above;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        float mine = 0.f;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) mine += value(j, e) == y ? 1.f : 0.f;
+        mine = wave_total(mine);
+        if (lane == 0) equals[j][wave] = (int)mine;
+      }
+      __syncthreads();
+      int from = above;                          // vectors of all waves in turn: the order of the tokens
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+#pragma unroll 1
+        for (int o = 0; o < kWaves; ++o) {
+          if (o == wave && from < a.K && equals[j][o] != 0) {
+            int at = from;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) at += lanes_below(__ballot(value(j, e) == y));
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+              if (value(j, e) == y) {
+                if (at < a.K) put(at, pick_key(y, token0(j) + e));
+                ++at;
+              }
+          }
+          from += equals[j][o];
+        }
+    }
+    repack();
+    const float reach = unord32(lo);
+    mine_n = 0;
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float y = value(j, e);
+        const uint64_t hit = __ballot(y >= reach);
+        if (hit == 0) continue;
+        if (y >= reach) list[wave][mine_n + lanes_below(hit)] = pick_key(y, token0(j) + e);
+        mine_n += __builtin_popcountll(hit);
+      }
+    count();
   }
-  uint64_t* out = w.key + part * a.K;
   if (n <= WAVE) {
     // the usual case: one wave, an element per lane, ranks by broadcasts
     if (wave != 0) return;
@@ -299,48 +404,21 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
       rank += other > mine;
     }
     if (lane < n) {
-      if (rank < a.K) out[rank] = mine;
-    } else if (lane < a.K) {
-      out[lane] = 0;
+      if (rank < a.K) put(rank, mine);
+    } else if (lane < first_free) {
+      put(lane, 0);
     }
     return;
   }
-  if (longest <= kList) {
-    for (int i = lane; i < mine_n; i += WAVE) {
-      const uint64_t mine = list[wave][i];
-      int rank = 0;
-      for (int o = 0; o < kWaves; ++o) {
-        const int c = counts[o];
-        for (int j = 0; j < c; ++j) rank += list[o][j] > mine;
-      }
-      if (rank < a.K) out[rank] = mine;
+  // n > 64 >= K: every place is written
+  for (int i = lane; i < mine_n; i += WAVE) {
+    const uint64_t mine = list[wave][i];
+    int rank = 0;
+    for (int o = 0; o < kWaves; ++o) {
+      const int c = counts[o];
+      for (int j = 0; j < c; ++j) rank += list[o][j] > mine;
     }
-    return;                                      // n > 64 >= K: every place is written
-  }
-  // more ties than a list holds: the next element in order, K times, read
-  // again (the registers of the elements are given up by now)
-  uint64_t prev = ~0ull;
-  for (int found = 0; found < a.K; ++found) {
-    uint64_t mine = 0;
-#pragma unroll 1
-    for (int j = 0; j < E; ++j) {
-      asm volatile("" ::: "memory");             // not hoisted out of the passes, which would take the registers
-      const u32x4 v = load(j);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float y = plain(elem<F32>(v, e));
-        const uint64_t k = pick_key(y, token0(j) + e);
-        if (y >= reach && k < prev && k > mine) mine = k;
-      }
-    }
-    __syncthreads();
-    if (tid == 0) best = 0;
-    __syncthreads();
-    if (mine) atomicMax(reinterpret_cast<unsigned long long*>(&best), (unsigned long long)mine);
-    __syncthreads();
-    prev = best;
-    if (tid == 0) out[found] = prev;
-    if (prev == 0) prev = 1;                     // none left: the rest is 0 too
+    if (rank < a.K) put(rank, mine);
   }
 }
 
@@ -369,7 +447,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
   __shared__ uint8_t done_of[kBeamMaxW];
   const int b = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const Ws w = ws_of(a);
-  const int per = a.splits * a.K, cand = a.W * per;
+  const int parts = a.W * a.splits, cand = a.K * w.pitch;
   const uint64_t* keys = w.key + (int64_t)b * cand;
   uint64_t held[ONE ? kHeld : 1];
   if constexpr (ONE) {
@@ -377,7 +455,6 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
     for (int u = 0; u < kHeld; ++u) held[u] = tid + u * kThreads < cand ? keys[tid + u * kThreads] : 0;
   }
   // every part's maximum and sum, the scores and the flags, in one round trip
-  const int parts = a.W * a.splits;
   const float2* ms = w.ms + (int64_t)b * parts;
   for (int i = tid; i < parts && i < kParts; i += kThreads) pms[i] = ms[i];
   if (tid < a.W) {
@@ -417,16 +494,19 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(BeamArgs a) {
     a.tokens[(int64_t)b * a.K + i] = -1;
   }
   __syncthreads();
-  // i / per: with at most kHeld kThreads candidates i per < 2^32, and the product is exact
-  const uint32_t magic = 0xFFFFFFFFu / (uint32_t)per + 1;
+  // i / d: exact for d > 1 and i d < 2^32, as i < kHeld kThreads
+  const uint32_t by_pitch = 0xFFFFFFFFu / (uint32_t)w.pitch + 1, by_splits = 0xFFFFFFFFu / (uint32_t)a.splits + 1;
+  auto over = [&](int i, int d, uint32_t magic) { return ONE && d > 1 ? (int)__umulhi((uint32_t)i, magic) : i / d; };
   auto get = [&](int i, uint64_t key, Cand& c) -> bool {
-    c.beam = ONE && per > 1 ? (int)__umulhi((uint32_t)i, magic) : i / per;
+    const int rank = over(i, w.pitch, by_pitch), part = i - rank * w.pitch;
+    if (part >= parts) return false;             // the pitch's last column
+    c.beam = over(part, a.splits, by_splits);
     const double sh = shift[c.beam];
     if (!(sh > -(double)kInf)) return false;
     if (done_of[c.beam]) {
       c.total = sh;
       c.token = a.pad_token;
-      return i == c.beam * per;
+      return rank == 0 && part == c.beam * a.splits;
     }
     if (key == 0) return false;
     c.total = ((double)unord32((uint32_t)(key >> 32)) - topx[c.beam]) + sh;
@@ -565,7 +645,7 @@ void beam_plan(BeamArgs& a) {
 
 int64_t beam_workspace_bytes(const BeamArgs& a) {
   const int64_t parts = (int64_t)a.B * a.W * a.splits;
-  return up16(parts * 8) + parts * a.K * 8;
+  return up16(parts * 8) + (int64_t)a.B * a.K * ((a.W * a.splits) | 1) * 8;
 }
 
 namespace {
@@ -587,7 +667,7 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)a.B);
-  if ((int64_t)a.W * a.splits * a.K <= kHeld * kThreads) beam_join_kernel<true><<<grid, kThreads, 0, s>>>(a);
+  if (((int64_t)a.W * a.splits | 1) * a.K <= kHeld * kThreads) beam_join_kernel<true><<<grid, kThreads, 0, s>>>(a);
   else beam_join_kernel<false><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
