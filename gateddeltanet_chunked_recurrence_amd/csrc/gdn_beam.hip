@@ -170,33 +170,51 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
   const char* vec0 = base - (int64_t)off * ES;
   const int first = split * (E * kThreads) + tid;
   auto token0 = [&](int j) { return (first + j * kThreads) * VE - off; };   // of vector j's first element
-  auto load = [&](int j) {
+  // The part's vectors, -inf outside the row. Only the row's first and last parts
+  // have vectors that are not whole: code for ends in every load took 80 KB,
+  // more than the instruction cache holds.
+  auto load_part = [&](u32x4 (&raw)[E]) {
+    const char* at = vec0 + (int64_t)first * 16;
+    const int whole = split * (E * kThreads) * VE - off;
+    if (whole >= 0 && whole + E * kThreads * VE <= a.V) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) raw[j] = *reinterpret_cast<const u32x4*>(at + j * (kThreads * 16));
+      return;
+    }
     const uint32_t ninf = F32 ? 0xFF800000u : 0xFF80FF80u;
-    const int lo = token0(j);
-    u32x4 raw{ninf, ninf, ninf, ninf};
-    if (lo >= 0 && lo + VE <= a.V) {
-      raw = *reinterpret_cast<const u32x4*>(vec0 + (int64_t)(first + j * kThreads) * 16);
-    } else if (lo + VE > 0 && lo < a.V) {
-      // the row's ends: single elements
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      raw[j] = u32x4{ninf, ninf, ninf, ninf};
+      if (token0(j) >= 0 && token0(j) + VE <= a.V) raw[j] = *reinterpret_cast<const u32x4*>(at + j * (kThreads * 16));
+    }
+    // the row's two ends, element by element
+    const int last = (a.V + off - 1) / VE;
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+      const int v = end == 0 ? 0 : last, lo = v * VE - off;
+      const bool ragged = lo < 0 || lo + VE > a.V;
+      if (!ragged || v < first || v >= first + E * kThreads || (v - first) % kThreads != 0) continue;
+      u32x4 x{ninf, ninf, ninf, ninf};
 #pragma unroll
       for (int e = 0; e < VE; ++e)
         if (lo + e >= 0 && lo + e < a.V) {
           if constexpr (F32) {
-            raw[e] = reinterpret_cast<const uint32_t*>(base)[lo + e];
+            x[e] = reinterpret_cast<const uint32_t*>(base)[lo + e];
           } else {
             const uint32_t h = reinterpret_cast<const uint16_t*>(base)[lo + e];
-            raw[e / 2] = e & 1 ? (raw[e / 2] & 0xFFFFu) | h << 16 : (raw[e / 2] & 0xFFFF0000u) | h;
+            x[e / 2] = e & 1 ? (x[e / 2] & 0xFFFFu) | h << 16 : (x[e / 2] & 0xFFFF0000u) | h;
           }
         }
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (v == first + j * kThreads) raw[j] = x;
     }
-    return raw;
   };
   // NaN counts as masked, +inf as the largest finite value
   auto plain = [](float v) { return v != v ? -kInf : fminf(v, kMaxF); };
 
   u32x4 raw[E];
-#pragma unroll
-  for (int j = 0; j < E; ++j) raw[j] = load(j);
+  load_part(raw);
   float x[E * VE], top = -kInf, vtop[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) {
@@ -299,8 +317,7 @@ __global__ void __launch_bounds__(kThreads) beam_part_kernel(BeamArgs a) {
     // the K-th largest value itself. The elements are read again and stay
     // packed, so that this part takes no registers from the usual case.
     asm volatile("" ::: "memory");
-#pragma unroll
-    for (int j = 0; j < E; ++j) raw[j] = load(j);
+    load_part(raw);
     auto repack = [&]() {                        // not unpacked once for all the passes
 #pragma unroll
       for (int j = 0; j < E; ++j) asm volatile("" : "+v"(raw[j]));
