@@ -11,13 +11,16 @@
 // exponentials and its K largest logits with their tokens. The second kernel,
 // one workgroup per request, joins the parts: log-sums per beam, totals of
 // the candidates, the K best. Bound: reading the logits once from HBM. 512 rows
-// of 100,003 bf16 logits (102 MB): 41 us, of which the parts 32.7 and the join 8.2;
-// the reading alone takes 19, with the maxima and exponentials (hidden behind it)
-// 22.5, and choosing adds the rest: scalar instructions, which a CU issues one at a
-// time, and three exchanges over LDS that each wait for the slowest wave. 4 rows
-// of 131,072: 12 us (5.9 and 6.4), two launches and their dependent loads. The same
-// 512 rows with all but 50 tokens masked: 48 us with -inf, 103 with the type's lowest
-// value (636 when equal logits were taken one by one).
+// of 100,003 bf16 logits (102 MB): 40 us, of which the parts 32.0 and the join 8.2.
+// Reading alone takes 19 and the vector ALUs are busy for 16.5 (630 instructions per
+// wave of 4,096 elements: five per element for maximum and sum, the rest for the
+// choice); the two overlap little, as a workgroup waits for its loads first and
+// three times for its slowest wave later. Elements kept packed (74 VGPRs instead of
+// 100, more workgroups per CU) give the same time, workgroups that walk over
+// parts and load the next one early 44 (153 VGPRs). 4 rows of 131,072: 12 us (5.8 and
+// 6.4), two launches and their dependent loads. The 512 rows with all but 50 tokens
+// masked: 46 us with -inf, 100 with the type's lowest value (636 when equal logits
+// were taken one by one).
 //
 // The K largest of a part: a bound that at least K elements reach, from the
 // 256 lane maxima: the K-th largest of one wave's 64 is one (the best of the four
