@@ -551,6 +551,8 @@ def _token_stride(t, name, shape, dtype, dev):
     if t.dtype is not dtype or t.shape != shape or t.device != dev:
         raise ValueError(f'{name}: {str(dtype)[6:]} {list(shape)} on {dev}; got '
                          f'{str(t.dtype)[6:]} {list(t.shape)} on {t.device}')
+    if t.is_contiguous():
+        return 0
     sb, st, sh, sd = t.stride()
     B, T, H, D = shape
     ts = st if T > 1 else sb
