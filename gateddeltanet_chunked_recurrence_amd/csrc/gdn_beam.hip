@@ -93,9 +93,16 @@ __device__ __forceinline__ float base_of(float m) { return fabsf(m) < kBig ? m *
 __device__ __forceinline__ float share_of(float x, float m, float base) {
   return fabsf(m) < kBig ? fexp2(fmaf(x, kLog2e, -base)) : fexp2((x - m) * kLog2e);
 }
-// The factor that brings a sum from maximum m to maximum M >= m.
+// The factor that brings a sum from maximum m to maximum M >= m. Both bases round
+// on their own, as the shares were taken against fl(m L) and log_sum takes
+// fl(M L) back; one fused multiply-add over the two products would leave
+// out the rounding of one of them, 6e-5 of a log-sum at logits near 1,000.
 __device__ __forceinline__ float rescale(float m, float M) {
-  if (fabsf(m) < kBig && fabsf(M) < kBig) return fexp2(m * kLog2e - M * kLog2e);
+#pragma clang fp contract(off)
+  if (fabsf(m) < kBig && fabsf(M) < kBig) {
+    const float bm = m * kLog2e, bM = M * kLog2e;
+    return fexp2(bm - bM);
+  }
   return fexp2((m - M) * kLog2e);
 }
 // log sum exp(x) - M of a sum s of shares of maximum M: ln 2 log2(s) plus what

@@ -213,3 +213,14 @@ def test_calls_on_two_streams_at_once():
     for i in range(2):
         for r in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
+
+
+@pytest.mark.parametrize("V", [1021, 60001])
+def test_rows_shifted_by_a_constant(V):
+    """Each beam's logits shifted by another constant, up to 10,000: over several
+    waves and parts of a row the log-sum's error is that of the differences, so
+    the bound at the top holds at every shift."""
+    x, s = _logits(3, 6, V, torch.float32, seed=V)
+    shift = torch.tensor([0.0, 101.3, -1000.7, 3001.9, 10000.1, 20.6], device='cuda')
+    _check((x + shift[:, None]).contiguous(), s * 0.05, 12)
+    _check((x - 7.0 * shift[:, None]).contiguous(), s * 0.05, 12)
