@@ -85,25 +85,26 @@ __device__ __forceinline__ uint32_t kth_bound(const uint32_t (&key)[N], int want
 
 constexpr float kLog2e = 1.4426950408889634f;    // L; L / log2(e) - 1 = kLDelta
 constexpr double kLDelta = (double)kLog2e / 1.4426950408889634074 - 1.0;
-constexpr float kBig = 0x1p100f;
-// The exponent base of maximum m, and 2^(x L - base): beyond 2^100 (masks of the
-// type's lowest value, or +inf) the products would overflow, and the difference
-// is taken first.
+constexpr float kBig = 0x1p20f;
+// The exponent base of maximum m, and 2^(x L - base). The base is rounded, so
+// the share of x = m itself is 2^(m L - fl(m L)): taken back at the end, but
+// beyond 2^32 it overflows or vanishes. From 2^20 on (rows masked throughout
+// with a large finite number, or +inf) the difference is taken first, and the
+// base is m L as it is.
 __device__ __forceinline__ float base_of(float m) { return fabsf(m) < kBig ? m * kLog2e : m; }
 __device__ __forceinline__ float share_of(float x, float m, float base) {
   return fabsf(m) < kBig ? fexp2(fmaf(x, kLog2e, -base)) : fexp2((x - m) * kLog2e);
 }
-// The factor that brings a sum from maximum m to maximum M >= m. Both bases round
-// on their own, as the shares were taken against fl(m L) and log_sum takes
-// fl(M L) back; one fused multiply-add over the two products would leave
-// out the rounding of one of them, 6e-5 of a log-sum at logits near 1,000.
+// The factor that brings a sum from maximum m to maximum M >= m: 2 to the
+// difference of their bases, (m - M) L and what each base was rounded by. Not
+// one fused multiply-add over m L and M L: that leaves out one of the roundings
+// (6e-5 of a log-sum at logits near 1,000).
+__device__ __forceinline__ float base_error(float m) {
+  return fabsf(m) < kBig ? fmaf(m, kLog2e, -(m * kLog2e)) : 0.f;
+}
 __device__ __forceinline__ float rescale(float m, float M) {
 #pragma clang fp contract(off)
-  if (fabsf(m) < kBig && fabsf(M) < kBig) {
-    const float bm = m * kLog2e, bM = M * kLog2e;
-    return fexp2(bm - bM);
-  }
-  return fexp2((m - M) * kLog2e);
+  return fexp2((m - M) * kLog2e + (base_error(M) - base_error(m)));
 }
 // log sum exp(x) - M of a sum s of shares of maximum M: ln 2 log2(s) plus what
 // the base was rounded by, fl(M L) / log2(e) - M, minus what the rounding of L adds, which

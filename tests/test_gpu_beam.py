@@ -224,3 +224,25 @@ def test_rows_shifted_by_a_constant(V):
     shift = torch.tensor([0.0, 101.3, -1000.7, 3001.9, 10000.1, 20.6], device='cuda')
     _check((x + shift[:, None]).contiguous(), s * 0.05, 12)
     _check((x - 7.0 * shift[:, None]).contiguous(), s * 0.05, 12)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [900, 70001])
+def test_rows_of_large_finite_logits(dt, V):
+    """Rows masked throughout with a large finite number, rows whose logits
+    are that large, and rows around the size where the kernel's form changes."""
+    for base in (-1e9, -1e10, 1e10, -1e12, 3e15, -1e30, 2.0 ** 99, -2.0 ** 101):
+        x, s = _logits(2, 4, V, dt, seed=V)
+        s = s * 0.05
+        x[0, 0] = base                                    # nothing but the mask
+        x[0, 1] = base
+        x[0, 1, V // 2] = base * (1 - 2.0 ** -7)          # one logit apart from the rest
+        x[0, 2, 11:] = -abs(base)                         # all masked but a few
+        x[1, 1, 1::2] = -abs(base)
+        x[1, 2, : V // 2] = base                          # whole waves of the mask
+        _check(x, s, 7)
+    edge = 2.0 ** torch.arange(18, 34, device='cuda', dtype=torch.float32)
+    rows = edge.repeat_interleave(2) * torch.tensor([1.0, -1.0], device='cuda').repeat(16)
+    step = torch.linspace(-3.0, 3.0, V, device='cuda')
+    x = (rows[:, None] + step).to(dt).view(4, 8, V)       # waves on both sides of a power of two
+    _check(x, -0.05 * torch.rand(4, 8, device='cuda'), 9)
