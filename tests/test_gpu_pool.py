@@ -645,3 +645,68 @@ def test_calls_run_on_the_current_stream():
     B.gdn_pool_write(want, 0, _ints([2]), new)
     B.gdn_pool_reorder(want, _ints([[0, 1, 2, 3]]), _ints([[3, 2, 1, 0]]))
     assert torch.equal(o, o2) and _pool_same(pool, _snapshot(want)) and B.device_errors() == 0
+
+
+# ------------------------------------------------------------- large batches
+# One token of so many heads that a group of waves walks over the tiles of a
+# head and over two heads (256 CUs hold 256 to 3,072 groups, by the tile).
+LARGE = [(E4M3, torch.bfloat16, 128, 128, 64, 1, 31, 51, True, BEFORE),      # two tiles a head, odd number of heads
+         (E4M3, torch.bfloat16, 128, 128, 64, 2, 32, 64, False, AFTER),
+         (E4M3, torch.bfloat16, 128, 128, 64, 1, 31, 37, True, AFTER),       # one tile, two elements
+         (INT8, torch.bfloat16, 128, 256, 64, 4, 32, 65, False, BEFORE),
+         (INT8, torch.bfloat16, 128, 256, 64, 1, 13, 77, True, AFTER),
+         (INT8, torch.float32, 128, 256, 256, 1, 9, 39, True, BEFORE),       # one tile a head, of 16 waves
+         (INT8, torch.float32, 64, 128, 128, 1, 32, 67, False, AFTER),
+         (E4M3, torch.float32, 64, 256, 32, 1, 31, 103, False, BEFORE),      # independent waves, eight tiles
+         (E4M3, torch.float32, 128, 256, 128, 1, 11, 71, True, AFTER),
+         (E4M3, torch.bfloat16, 64, 64, 16, 1, 31, 101, True, BEFORE),
+         (OFF, torch.float32, 64, 128, 64, 2, 32, 64, True, BEFORE)]
+
+
+@pytest.mark.parametrize("fmt,dt,Dk,Dv,bv,Hqk,Hv,Bn,fork,readout", LARGE)
+def test_large_batches_equal_small_ones(fmt, dt, Dk, Dv, bv, Hqk, Hv, Bn, fork, readout):
+    """Absent and refused entries next to others, first, last and in a row: the
+    same bits as the other entries stepped four at a time, and FP64 for some."""
+    say(f"pool step of {Bn} x {Hv} heads fmt={fmt} {dt} Dk={Dk} Dv={Dv} block_v={bv} fork={fork}")
+    n = 2 * Bn + 2
+    big, small = (_random_pool(fmt, 1, n, Hv, Dk, Dv, bv, seed=40) for _ in range(2))
+    snap = _snapshot(big)
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(Bn)).tolist()
+    slots, out = order[:Bn], order[Bn: 2 * Bn]
+    absent, refused = [1, 7, 8, Bn // 2], [0, 2, 9, Bn // 2 + 1, Bn - 1]
+    if fork:
+        slots = [slots[i // 3] for i in range(Bn)]        # three children each
+        out[0] = out[2]                                   # one page for two children
+        out[9], out[Bn // 2 + 1], out[Bn - 1] = n, -2, n + 5
+    else:
+        slots[0] = slots[2]
+        slots[9], slots[Bn // 2 + 1], slots[Bn - 1] = n, -2, n + 5
+        out = None
+    for i in absent:
+        slots[i] = -1
+    x = _draw(Bn, 1, Hqk, Hv, Dk, Dv, dt, seed=41)
+    o = torch.full((Bn, 1, Hv, Dv), 7.0, dtype=dt, device='cuda')
+    B.gdn_pool_step(big, 0, _ints(slots), slots_out=None if out is None else _ints(out), readout=readout, out=o, **x)
+    assert B.device_errors() == B.DEVERR_POOL_SLOT
+    want = torch.full_like(o, 7.0)
+    for i in range(0, Bn, 4):
+        rows = range(i, min(i + 4, Bn))
+        part = [-1 if j in refused else slots[j] for j in rows]
+        to = None if out is None else _ints([-1 if j in refused else out[j] for j in rows])
+        got = torch.full((len(part), 1, Hv, Dv), 7.0, dtype=dt, device='cuda')
+        B.gdn_pool_step(small, 0, _ints(part), slots_out=to, readout=readout, out=got,
+                        **{k: v[i: i + 4].contiguous() for k, v in x.items()})
+        want[i: i + 4] = got
+    assert B.device_errors() == 0
+    want[refused] = float('nan')
+    assert bool(o[refused].isnan().all()) and bool((o[absent] == 7.0).all())
+    assert torch.equal(o.nan_to_num(nan=-5.0), want.nan_to_num(nan=-5.0))
+    assert _pool_same(big, _snapshot(small))
+    values = B.StatePool.from_tensors(snap[0][:, [slots[j] for j in (3, 10, Bn - 2)]].contiguous() if fmt == OFF else
+                                      snap[0].view(torch.uint8)[:, [slots[j] for j in (3, 10, Bn - 2)]].view(snap[0].dtype),
+                                      None if fmt == OFF else snap[1][:, [slots[j] for j in (3, 10, Bn - 2)]], fmt, bv)
+    before = _values(values)[0]
+    for i, j in enumerate((3, 10, Bn - 2)):
+        to = slots[j] if out is None else out[j]
+        _check_step(big, before[i], big.data[0, to], None if fmt == OFF else big.scales[0, to], x, o[j, 0], j, to,
+                    Dk ** -0.5, readout)
