@@ -264,12 +264,16 @@ __device__ __forceinline__ void step_tile(const PoolRef& P, const char* hb, u32x
   // The update in units of a, or of 2^-64 where a is smaller (a state forgotten
   // within a token, or the zero page with its scale 2^-126), so that u / unit
   // cannot overflow for |u| < 2^63; the codes then count a / unit < 1 each,
-  // rounded to bf16: that rounds values below 2^-55 only.
-  const float unit = fmaxf(alpha, 0x1p-64f), ru = 1.0f / unit;
-  const uint32_t one = alpha >= 0x1p-64f ? 0x3F803F80u : [&]() {
-    const uint32_t h = __builtin_bit_cast(uint16_t, to_bf16(alpha * ru));
-    return h | h << 16;
-  }();
+  // rounded to bf16: that rounds values below 2^-55 only. From a = 2 on the codes
+  // count a's power of two (exact in bf16) and the unit is the rest, so that unit / d
+  // below stays finite down to the smallest d, 2^-126 (a tile that becomes zero).
+  const uint32_t abits = __builtin_bit_cast(uint32_t, alpha);
+  const float unit = fmaxf(alpha >= 2.f ? __builtin_bit_cast(float, (abits & 0x007FFFFFu) | 0x3F800000u) : alpha, 0x1p-64f);
+  const float ru = 1.0f / unit;
+  const uint32_t half = alpha >= 2.f         ? (abits >> 16) & 0x7F80u
+                        : alpha >= 0x1p-64f ? 0x3F80u
+                                             : __builtin_bit_cast(uint16_t, to_bf16(alpha * ru));
+  const uint32_t one = half | half << 16;
   // A of tiles with even and odd c: row m picks, for lanes g == m >> 2, element 4 (c & 1) + (m & 3)
   bf16x8 pick[2];
 #pragma unroll

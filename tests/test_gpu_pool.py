@@ -710,3 +710,45 @@ def test_large_batches_equal_small_ones(fmt, dt, Dk, Dv, bv, Hqk, Hv, Bn, fork, 
         to = slots[j] if out is None else out[j]
         _check_step(big, before[i], big.data[0, to], None if fmt == OFF else big.scales[0, to], x, o[j, 0], j, to,
                     Dk ** -0.5, readout)
+
+
+# ------------------------------------------------------------- tiles of zeros
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("fmt,dt,Dk,bv", [(E4M3, torch.bfloat16, 128, 64), (INT8, torch.bfloat16, 128, 64),
+                                          (INT8, torch.float32, 64, 128), (E4M3, torch.float32, 64, 16)])
+def test_a_tile_that_becomes_zero_or_tiny(fmt, dt, Dk, bv, T):
+    """A zero tile under a large scale, a state that one token erases, and an
+    update far below the tile's scale: codes 0 (or those of the tiny values)
+    under the smallest scale, 2^-126."""
+    Hv, Dv = 2, 128
+    pool = B.StatePool(1, 4, Hv, Dk, Dv, fmt, bv)
+    pool.scales.fill_(8.0)
+    codes = torch.zeros(4, Hv, Dv, Dk, device='cuda')
+    codes[1, :, :, 5] = torch.arange(Dv, device='cuda') % 13 - 6.0         # states along one key
+    pool.data[0] = codes.to(pool.data.dtype)
+    x = _draw(4, T, 1, Hv, Dk, Dv, dt, seed=50)
+    x['k'].zero_()
+    x['k'][:, :, :, 5] = 1.0
+    x['v'].zero_()
+    x['g'].zero_()
+    x['beta'].fill_(1.0)
+    tiny = fmt != OFF and dt is torch.float32
+    if tiny:                                              # 2^-122 is code 16 under 2^-126
+        x['v'][2] = 2.0 ** -122
+    for readout in (BEFORE, AFTER):
+        p = B.StatePool.from_tensors(pool.data.clone(), pool.scales.clone(), fmt, bv)
+        o = B.gdn_pool_step(p, 0, _ints([0, 1, 2, -1]), readout=readout, **x)
+        assert B.device_errors() == 0
+        assert bool(p.data[0, :2].float().eq(0).all()) and bool((p.scales[0, :3] == 2.0 ** -126).all())
+        # |states| <= 48 with four roundings each in k . q, S^T q and their sum; the half step of o is within
+        assert bool((o[:2].float().abs() <= 48 * 4 * U).all()) and bool(o.isfinite().all())
+        want = torch.zeros(Hv, Dv, Dk, device='cuda')
+        if tiny:
+            want[:, :, 5] = 16.0
+        assert torch.equal(p.data[0, 2].float(), want)
+        # what follows is a step from the zero state
+        y = _draw(4, 1, 1, Hv, Dk, Dv, dt, seed=51)
+        fresh = B.StatePool(1, 4, Hv, Dk, Dv, fmt, bv)
+        a = B.gdn_pool_step(p, 0, _ints([0, 1, -1, -1]), readout=readout, **y)
+        b = B.gdn_pool_step(fresh, 0, _ints([0, 1, -1, -1]), readout=readout, **y)
+        assert torch.equal(a, b) and _pool_same(p, _snapshot(fresh), [0, 1])
