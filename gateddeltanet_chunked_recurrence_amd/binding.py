@@ -653,7 +653,7 @@ def gdn_pool_copy(pool, src, dst):
     """page[dst[m]] <- page[src[m]] in every layer (int32 [n] each): forks,
     moves, compaction. src -1 clears the page, dst -1 skips the entry. No
     destination may be named twice or be another entry's source (such pages
-    are left as they were, with DEVERR_POOL_SLOT)."""
+    are left as they were, with DEVERR_POOL_SLOT); src == dst does nothing."""
     n = src.shape[0]
     _need(src, 'src', torch.int32, (n,), pool.device)
     _need(dst, 'dst', torch.int32, (n,), pool.device)
@@ -664,7 +664,8 @@ def gdn_pool_reorder(pool, slots, parents):
     """In place and in every layer, page[slots[g, w]] <- the page that
     slots[g, parents[g, w]] held (int32 [groups, width] each, width up to 32):
     the beams of each group take their parents' states. Parent -1 leaves a
-    page alone; slot -1 is a beam that is not there."""
+    page alone; slot -1 is a beam that is not there. A page that changes may be
+    named by no other beam of the call."""
     if slots.dim() != 2:
         raise ValueError(f'slots: [groups, width]; got {list(slots.shape)}')
     _need(slots, 'slots', torch.int32, slots.shape, pool.device)
@@ -680,8 +681,9 @@ def gdn_pool_step(pool, layer, slots, q, k, v, g, beta, scale=None, slots_out=No
     or FP32; token strides are free) and g, beta [B, T, Hv] FP32, from the
     states in `slots` (int32 [B], -1: no sequence) to `slots_out` (default:
     the same; -1: not kept; parents may be shared, a page written may not be
-    named by another sequence). Returns o [B, T, Hv, Dv] in q's type; rows
-    past lens and of absent sequences are not written (zero in a new o)."""
+    named by another sequence that has tokens or copies its state). Returns o
+    [B, T, Hv, Dv] in q's type; rows past lens and of absent sequences are not
+    written (zero in a new o)."""
     dev, shape = pool.device, q.shape
     if len(shape) != 4:
         raise ValueError(f'q: [B, T, Hqk, Dk]; got {list(shape)}')

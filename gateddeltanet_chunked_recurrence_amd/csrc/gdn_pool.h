@@ -10,22 +10,30 @@ __device__ __forceinline__ void pool_error(const PoolRef& p) {
 }
 
 // Whether another entry than `n` reads (in[j]) or writes (out[j]) slot `dst`,
-// so that entry `n` may not write it. COPY: entries do something where out[j]
-// >= 0 (in -1 clears the page); otherwise where in[j] >= 0, and an entry with out
-// -1 still reads. Every wave that writes a part of the page asks this, with the
-// same answer in each, so an index given twice leaves the page as it was
-// instead of a mixture of two results. All 64 lanes call it together; each
-// takes four entries per load (the arrays are 16-byte aligned), and four
-// loads are in flight at once: 1,024 entries cost one round trip to L2. The
-// last vector is read again by lanes past it (asking twice changes nothing).
+// so that entry `n` may not write it. Every wave that writes a part of the page
+// asks this, with the same answer in each, so an index given twice leaves the
+// page as it was instead of a mixture of two results. Entries that touch no
+// page do not count: those refused for a slot outside the pool, and those with
+// nothing to do. COPY: an entry reads in[j] (-1: none, the page is cleared) and
+// writes out[j] >= 0, unless the two are one. Otherwise it reads in[j] >= 0 and
+// writes out[j] (-1: not kept), unless it has no token (lens, of T at most) and
+// no other page to copy to. All 64 lanes call this together; each takes four
+// entries per load (the arrays are 16-byte aligned), and four loads are in
+// flight at once: 1,024 entries cost one round trip to L2. The last vector is
+// read again by lanes past it (asking twice changes nothing). lens is read only
+// where an entry names the slot.
 template <bool COPY>
-__device__ __forceinline__ bool pool_claimed(const int32_t* in, const int32_t* out, int count, int n,
-                                             int dst) {
+__device__ __forceinline__ bool pool_claimed(const PoolRef& p, const int32_t* in, const int32_t* out, int count,
+                                             int n, int dst, int T = 1, const int32_t* lens = nullptr) {
   typedef int i32x4 __attribute__((ext_vector_type(4)));
   const int lane = __lane_id(), nv = count >> 2;
   bool hit = false;
+  const uint32_t slots = (uint32_t)p.slots;
   auto test = [&](int j, int a, int b) {
-    hit |= (j != n) & (COPY ? (a >= -1) & (b >= 0) : a >= 0) & ((a == dst) | (b == dst));
+    bool names = (j != n) & ((a == dst) | (b == dst));
+    if constexpr (COPY) names &= ((uint32_t)a + 1u <= slots) & ((uint32_t)b < slots) & (a != b);
+    else names &= ((uint32_t)a < slots) & ((uint32_t)b + 1u <= slots);
+    hit |= names;
   };
   for (int v0 = 0; v0 < nv; v0 += 4 * WAVE) {
     i32x4 a[4], b[4];
@@ -44,9 +52,19 @@ __device__ __forceinline__ bool pool_claimed(const int32_t* in, const int32_t* o
         for (int e = 0; e < 4; ++e)
           test(4 * min(v0 + u * WAVE + lane, nv - 1) + e, a[u][e], in != out ? b[u][e] : a[u][e]);
   }
-  const int j = 4 * nv + lane;
-  if (j < count) test(j, in[j], out[j]);
-  return __ballot(hit) != 0;
+  const int last = 4 * nv + lane;
+  if (last < count) test(last, in[last], out[last]);
+  if (__ballot(hit) == 0) return false;
+  if (!COPY && (T == 0 || lens)) {               // seldom: the entries that name the slot, by their tokens
+    hit = false;
+    for (int j = lane; j < count; j += WAVE) {
+      const int a = in[j], b = out[j];
+      if (j == n || (a != dst && b != dst) || (uint32_t)a >= slots || (uint32_t)b + 1u > slots) continue;
+      hit |= (T > 0 && (!lens || lens[j] > 0)) || (b != a && b != -1);
+    }
+    return __ballot(hit) != 0;
+  }
+  return true;
 }
 
 // The tile scale under the pool's rule: amax / q_max as gdn_qdq_state, or amax

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(512) pool_write_kernel(PoolRef P, int64_t laye
   f32x4 x[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = *reinterpret_cast<const f32x4*>(src + (int64_t)(key + i) * P.Dv);
-  if (slot < 0 || slot >= P.slots || pool_claimed<false>(slots, slots, count, w.n, slot)) {
+  if (slot < 0 || slot >= P.slots || pool_claimed<false>(P, slots, slots, count, w.n, slot)) {
     if (lane == 0) pool_error(P);
     return;
   }
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256) pool_f32_kernel(PoolRef P, int64_t layer_
   const int slot = slots[n];
   if (WRITE && slot == -1) return;
   bool ok = slot >= 0 && slot < P.slots;
-  if (WRITE && ok) ok = !pool_claimed<false>(slots, slots, count, n, slot);
+  if (WRITE && ok) ok = !pool_claimed<false>(P, slots, slots, count, n, slot);
   if (!ok && slot != -1 && lane == 0) pool_error(P);
   if (WRITE && !ok) return;
   const int64_t page_off = ok ? (layer_page + slot) * P.page : 0;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kMoveThreads) pool_copy_kernel(PoolRef P, cons
         x[i] = *reinterpret_cast<const u32x4*>(s + i * (kMoveThreads * 16));
     }
   }
-  if (!ok || pool_claimed<true>(src, dst, count, m, to)) {
+  if (!ok || pool_claimed<true>(P, src, dst, count, m, to)) {
     if (lane == 0) pool_error(P);
     return;
   }

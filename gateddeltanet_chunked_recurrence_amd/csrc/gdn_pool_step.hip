@@ -102,7 +102,7 @@ __device__ __forceinline__ bool step_in_ok(const PoolStepArgs& a, const StepUnit
 }
 __device__ __forceinline__ bool step_refused(const PoolStepArgs& a, const StepUnit& w) {
   if (!step_in_ok(a, w) || w.to < -1 || w.to >= a.pool.slots) return true;
-  return w.to >= 0 && pool_claimed<false>(a.slots, a.slots_out ? a.slots_out : a.slots, a.B, w.n, w.to);
+  return w.to >= 0 && pool_claimed<false>(a.pool, a.slots, a.slots_out ? a.slots_out : a.slots, a.B, w.n, w.to, a.T, a.lens);
 }
 
 // ------------------------------------------------------------ pages of codes
@@ -546,7 +546,7 @@ pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk
       checked = cur.n;
       refused = cur.slot < 0 || cur.slot >= P.slots || cur.to < -1 || cur.to >= P.slots ||
                 (cur.to >= 0 &&
-                 pool_claimed<false>(a.slots, a.slots_out ? a.slots_out : a.slots, a.B, cur.n, cur.to));
+                 pool_claimed<false>(P, a.slots, a.slots_out ? a.slots_out : a.slots, a.B, cur.n, cur.to));
       if (refused && cur.slot != -1 && lane == 0) pool_error(P);
     }
     char* op = static_cast<char*>(a.o) + ((int64_t)cur.n * Hv * tph + cur.h * tph + cur.tile) * (BV * ES);

@@ -401,7 +401,10 @@ gdn_status gdn_decode_bwd(const gdn_decode_bwd_args* a, void* stream);
  * slot outside [-1, slots), or one that a call would write while another
  * entry of the same call reads or writes it, is refused on the device: the
  * pages stay as they were, outputs of the refused entries are NaN, and
- * GDN_DEVERR_POOL_SLOT is set. States must be finite.
+ * GDN_DEVERR_POOL_SLOT is set. Entries refused for a slot outside the pool,
+ * and entries with nothing to do (a step without tokens that copies to no
+ * other page, a copy of a page to itself), read and write no page. States must be
+ * finite.
  *
  * Sizes: Dk in {64, 128}; Dv in {64, 128, 256}; block_v 16, 32, 64, 128 or
  * 256 dividing Dv (ignored when OFF); at most 65535 entries, layers and groups per
@@ -447,7 +450,8 @@ gdn_status gdn_pool_copy(const gdn_pool* pool, const int32_t* src, const int32_t
  * groups of `width` (1 to 32) beams, page[slots[g, w]] <- the page that
  * slots[g, parents[g, w]] held before the call, for all w at once. Parent -1
  * leaves the beam's page as it is, slot -1 is a beam that is not there (it
- * may not be a parent). */
+ * may not be a parent). A page that changes may be named by no other beam of
+ * the call, also not by one whose page stays. */
 gdn_status gdn_pool_reorder(const gdn_pool* pool, const int32_t* slots, const int32_t* parents,
                             int32_t groups, int32_t width, void* stream);
 

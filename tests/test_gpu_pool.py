@@ -752,3 +752,78 @@ def test_a_tile_that_becomes_zero_or_tiny(fmt, dt, Dk, bv, T):
         a = B.gdn_pool_step(p, 0, _ints([0, 1, -1, -1]), readout=readout, **y)
         b = B.gdn_pool_step(fresh, 0, _ints([0, 1, -1, -1]), readout=readout, **y)
         assert torch.equal(a, b) and _pool_same(p, _snapshot(fresh), [0, 1])
+
+
+# ------------------------------------------------ entries that claim no page
+@pytest.mark.parametrize("fmt", [E4M3, INT8, OFF])
+def test_entries_that_do_nothing_claim_no_page(fmt):
+    """Padding rows of length 0 may name a live page, and an entry refused for
+    a slot outside the pool does not keep another from its pages."""
+    Hv, D, bad = 2, 128, B.DEVERR_POOL_SLOT
+    pool, want = (_random_pool(fmt, 1, 9, Hv, D, D, 64, seed=60) for _ in range(2))
+    x = _draw(6, 2, 1, Hv, D, D, torch.bfloat16, seed=61)
+    # 3 is stepped by entry 0; entries 1 and 4 name it with nothing to do; entry 3 names 5, which entry 2 steps
+    slots, lens = [3, 3, 5, 5, 3, 7], [2, 0, 1, -4, 0, 2]
+    o = B.gdn_pool_step(pool, 0, _ints(slots), lens=_ints(lens), **x)
+    assert B.device_errors() == 0
+    o2 = B.gdn_pool_step(want, 0, _ints([3, -1, 5, -1, -1, 7]), lens=_ints(lens), **x)
+    assert torch.equal(o, o2) and _pool_same(pool, _snapshot(want))
+    # with slots_out: length 0 to the own page or to none does nothing, length 0 to another page is a copy
+    out = [4, -1, 5, 5, 3, 2]
+    o = B.gdn_pool_step(pool, 0, _ints([3, 4, 5, 5, 3, 7]), slots_out=_ints(out), lens=_ints([2, 0, 1, 0, 0, 0]), **x)
+    assert B.device_errors() == 0
+    o2 = B.gdn_pool_step(want, 0, _ints([3, -1, 5, -1, -1, 7]), slots_out=_ints(out), lens=_ints([2, 0, 1, 0, 0, 0]), **x)
+    assert torch.equal(o, o2) and _pool_same(pool, _snapshot(want))
+    # a length of 0 whose copy reads the page still claims it
+    snap = _snapshot(pool)
+    o = B.gdn_pool_step(pool, 0, _ints([3, 3, -1, -1, -1, -1]), slots_out=_ints([3, 8, 0, 0, 0, 0]),
+                        lens=_ints([2, 0, 0, 0, 0, 0]), **x)
+    assert B.device_errors() == bad and bool(o[0].isnan().all()) and _pool_same(pool, snap, [3])
+    assert _pool_same(pool, (pool.data[:, [3] * 9].contiguous() if fmt == OFF else
+                             pool.data.view(torch.uint8)[:, [3] * 9].view(pool.data.dtype),
+                             None if fmt == OFF else pool.scales[:, [3] * 9]), [8])
+    # one token: entries refused for their own slots
+    want.data.view(torch.uint8).copy_(pool.data.view(torch.uint8))
+    if fmt != OFF:
+        want.scales.copy_(pool.scales)
+    y = {k: v[:, :1].contiguous() for k, v in x.items()}
+    o = B.gdn_pool_step(pool, 0, _ints([1, 2, 9, 0, -1, -1]), slots_out=_ints([1, 9, 2, 2, 1, -1]), **y)
+    assert B.device_errors() == bad and bool(o[[1, 2]].isnan().all())
+    o2 = B.gdn_pool_step(want, 0, _ints([1, -1, -1, 0, -1, -1]), slots_out=_ints([1, 9, 2, 2, 1, -1]), **y)
+    assert torch.equal(o[[0, 3, 4, 5]], o2[[0, 3, 4, 5]]) and _pool_same(pool, _snapshot(want))
+    # no token at all: only copies to another page touch one
+    none = {k: v[:, :0] for k, v in x.items()}
+    B.gdn_pool_step(pool, 0, _ints([3, 4, 8, 5, 4, -1]), slots_out=_ints([3, 8, 8, -1, 5, -1]), **none)
+    assert B.device_errors() == 0
+    B.gdn_pool_copy(want, _ints([4, 4]), _ints([8, 5]))
+    assert _pool_same(pool, _snapshot(want))
+    # pages in
+    z = torch.randn(3, Hv, D, D, device='cuda')
+    B.gdn_pool_write(pool, 0, _ints([4, 9, -3]), z)
+    B.gdn_pool_write(want, 0, _ints([4, -1, -1]), z)
+    assert B.device_errors() == bad and _pool_same(pool, _snapshot(want))
+
+
+def test_moves_that_do_nothing_claim_no_page():
+    pool = _random_pool(E4M3, 2, 10, 2, 64, 64, 64, seed=62)
+    snap = _snapshot(pool)
+    # 3 <- 3 does nothing, so 3 may be written; 6 <- 3 reads it and so may not stand beside
+    B.gdn_pool_copy(pool, _ints([3, 0, 5, 5]), _ints([3, 3, 1, 5]))
+    assert B.device_errors() == 0
+    for s, w in ((3, 0), (1, 5), (5, 5), (0, 0)):
+        assert _same(pool.data[:, s], snap[0][:, w]), s
+    snap = _snapshot(pool)
+    # 4 -> 10 and 11 -> 6 are refused for their own slots; the copies to 4 and 6 are done
+    B.gdn_pool_copy(pool, _ints([4, 2, 11, 2, 7, 8]), _ints([10, 4, 6, 6, 9, 7]))
+    assert B.device_errors() == B.DEVERR_POOL_SLOT
+    for s, w in ((4, 2), (6, 2), (9, 7), (7, 7), (2, 2)):  # 7 is read by another entry
+        assert _same(pool.data[:, s], snap[0][:, w]), s
+
+
+def test_reorder_takes_a_page_only_where_no_other_beam_names_it():
+    """Every beam of the call counts, also one that keeps its page."""
+    pool = _random_pool(E4M3, 1, 8, 2, 64, 64, 64, seed=63)
+    snap = _snapshot(pool)
+    B.gdn_pool_reorder(pool, _ints([[0, 1], [2, 0]]), _ints([[1, 0], [-1, -1]]))
+    assert B.device_errors() == B.DEVERR_POOL_SLOT
+    assert _same(pool.data[:, 0], snap[0][:, 0]) and _same(pool.data[:, 1], snap[0][:, 0])
