@@ -525,6 +525,12 @@ def _need(t, name, dtype, shape, dev):
                          f'{"" if t.is_contiguous() else ", not contiguous"}')
 
 
+def _aligned(t):
+    """t, or a copy of it where it is a view off a 16-byte boundary (small
+    arrays of one element per sequence)."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 # The current stream's handle; without building a Stream object where torch
 # has the shorter way (2 us of a call's 7).
 _raw_stream = getattr(torch._C, '_cuda_getCurrentRawStream',
@@ -707,6 +713,7 @@ def gdn_pool_step(pool, layer, slots, q, k, v, g, beta, scale=None, slots_out=No
         a.slots_out = slots_out.data_ptr()
     if lens is not None:
         _need(lens, 'lens', torch.int32, (B,), dev)
+        lens = _aligned(lens)
         a.lens = lens.data_ptr()
     if out is None:
         out = torch.zeros(shape_v, dtype=dt, device=dev)
@@ -754,12 +761,14 @@ def gdn_beam_select(logits, scores, num_select=None, finished=None, pad_token=0)
         raise ValueError(f'logits: rows must be contiguous and evenly spaced; got strides '
                          f'{logits.stride()}')
     _need(scores, 'scores', torch.float32, (B, W), dev)
+    scores = _aligned(scores)
     a = BeamArgs(B=B, W=W, V=V, K=K, io_dtype=GDN_BF16 if dt is torch.bfloat16 else GDN_F32,
                  pad_token=pad_token, row_stride=rs if B * W > 1 else 0, logits=logits.data_ptr(),
                  scores=scores.data_ptr())
     if finished is not None:
         _need(finished, 'finished', torch.bool if finished.dtype is torch.bool else torch.uint8,
               (B, W), dev)
+        finished = _aligned(finished)
         a.finished = finished.data_ptr()
     lib = load_library()
     nbytes = lib.gdn_beam_workspace_bytes(ctypes.byref(a))

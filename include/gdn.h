@@ -395,7 +395,8 @@ gdn_status gdn_decode_bwd(const gdn_decode_bwd_args* a, void* stream);
  * with the format off). The caller allocates both. A page of zero bytes with
  * scales 2^-126 is the zero state.
  *
- * Slots are device arrays of int32 (16-byte aligned like every pointer). In
+ * Slots are device arrays of int32 (16-byte aligned like every pointer, unless
+ * it says otherwise). In
  * all calls slot -1 means "no sequence here": nothing is read or written for
  * it, so batches of a fixed size may be padded (and captured into a graph). A
  * slot outside [-1, slots), or one that a call would write while another
@@ -480,7 +481,8 @@ typedef struct {
   const void* q;               /* [B, T, Hqk, Dk]                             */
   const void* k;               /* [B, T, Hqk, Dk]                             */
   const void* v;               /* [B, T, Hv, Dv]                              */
-  const float* g;              /* [B, T, Hv] log-gate                         */
+  const float* g;              /* [B, T, Hv] log-gate; aligned to an element
+                                  only, as beta                               */
   const float* beta;           /* [B, T, Hv]                                  */
   void* o;                     /* out [B, T, Hv, Dv]; rows past lens, and of
                                   slot -1, are left as they were              */

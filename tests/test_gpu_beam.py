@@ -246,3 +246,14 @@ def test_rows_of_large_finite_logits(dt, V):
     step = torch.linspace(-3.0, 3.0, V, device='cuda')
     x = (rows[:, None] + step).to(dt).view(4, 8, V)       # waves on both sides of a power of two
     _check(x, -0.05 * torch.rand(4, 8, device='cuda'), 9)
+
+
+def test_one_request_of_a_larger_batch():
+    """Contiguous slices of scores and finished off 16-byte boundaries."""
+    x, s = _logits(5, 3, 777, torch.bfloat16, seed=6)
+    done = torch.rand(5, 3, generator=torch.Generator().manual_seed(1)).cuda() < 0.3
+    for b in range(5):
+        assert b != 1 or (s[b:b + 1].data_ptr() % 16 and done[b:b + 1].data_ptr() % 16)
+        got = B.gdn_beam_select(x[b:b + 1], s[b:b + 1], 4, done[b:b + 1], 5)
+        want = B.gdn_beam_select(x[b:b + 1].clone(), s[b:b + 1].clone(), 4, done[b:b + 1].clone(), 5)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))

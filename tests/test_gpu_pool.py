@@ -827,3 +827,24 @@ def test_reorder_takes_a_page_only_where_no_other_beam_names_it():
     B.gdn_pool_reorder(pool, _ints([[0, 1], [2, 0]]), _ints([[1, 0], [-1, -1]]))
     assert B.device_errors() == B.DEVERR_POOL_SLOT
     assert _same(pool.data[:, 0], snap[0][:, 0]) and _same(pool.data[:, 1], snap[0][:, 0])
+
+
+# ------------------------------------------------------------- unaligned views
+def test_tokens_out_of_a_longer_block():
+    """One sequence's gates at any token: contiguous slices whose address is a
+    multiple of 4 bytes only."""
+    Hv, D = 3, 64
+    for fmt in (E4M3, OFF):
+        a, b = (_random_pool(fmt, 1, 1, Hv, D, D, 32, seed=66) for _ in range(2))
+        x = _draw(1, 5, 1, Hv, D, D, torch.bfloat16, seed=67)
+        for t in range(5):
+            view = {k: v[:, t:t + 1] for k, v in x.items()}
+            assert t != 1 or view['g'].data_ptr() % 16
+            o1 = B.gdn_pool_step(a, 0, _ints([0]), **view)
+            o2 = B.gdn_pool_step(b, 0, _ints([0]), **{k: v.clone() for k, v in view.items()})
+            assert torch.equal(o1, o2)
+        view = {k: v[:, 1:4] for k, v in x.items()}       # three tokens of it
+        lens = _ints([9, 2, 9])[1:2]
+        o1 = B.gdn_pool_step(a, 0, _ints([0]), lens=lens, **view)
+        o2 = B.gdn_pool_step(b, 0, _ints([0]), lens=lens.clone(), **{k: v.clone() for k, v in view.items()})
+        assert torch.equal(o1, o2) and _pool_same(a, _snapshot(b)) and B.device_errors() == 0

@@ -257,3 +257,12 @@ def test_beam_select_refuses_other_tensors():
             call()
     with pytest.raises(B.GdnError, match='K 65'):
         B.gdn_beam_select(x, s, 65)
+
+
+@pytest.mark.parametrize("name", ['g', 'beta'])
+def test_gates_are_aligned_to_an_element(name):
+    got, text = _call('gdn_pool_step', ctypes.byref(_pool()), ctypes.byref(_step(**{name: FAKE + 2})), None)
+    assert got == B.GDN_E_INVALID and f'{name} is not 4-byte' in text, (got, text)
+    # at 4 bytes the next check speaks, not this one
+    got, text = _call('gdn_pool_step', ctypes.byref(_pool()), ctypes.byref(_step(**{name: FAKE + 4}, q_stride=255)), None)
+    assert got == B.GDN_E_INVALID and 'q_stride' in text, (got, text)
