@@ -67,12 +67,32 @@ __device__ __forceinline__ bool pool_claimed(const PoolRef& p, const int32_t* in
   return true;
 }
 
+// An E4M3 code can be NaN, an integer one cannot: an INT8 tile with a value that
+// is not finite takes the scale NaN, so that every later read and step of it is
+// NaN instead of what the codes happen to be. So its amax keeps a NaN
+// (v_maximum3_f32: as many instructions as a maximum that leaves NaN out).
+template <int FMT>
+__device__ __forceinline__ float larger(float m, float x) {
+  if constexpr (FMT == 2) return __builtin_elementwise_maximum(m, fabsf(x));
+  else return fmaxf(m, fabsf(x));
+}
+template <int FMT>
+__device__ __forceinline__ float wave_largest(float m) {  // as wave_max
+  m = larger<FMT>(m, dpp_f<0xB1>(m));
+  m = larger<FMT>(m, dpp_f<0x4E>(m));
+  m = larger<FMT>(m, dpp_f<0x141>(m));
+  m = larger<FMT>(m, dpp_f<0x140>(m));
+  return larger<FMT>(larger<FMT>(read_lane(m, 0), read_lane(m, 16)), larger<FMT>(read_lane(m, 32), read_lane(m, 48)));
+}
+
 // The tile scale under the pool's rule: amax / q_max as gdn_qdq_state, or amax
 // times the FP32-rounded 1 / q_max as PyTorch divides a tensor by a number.
+// INT8: plus 0, or NaN where amax is not finite.
 template <int FMT>
 __device__ __forceinline__ float pool_scale(const PoolRef& p, float amax) {
   constexpr float kRecip = 1.0f / QdqFmt<FMT>::qmax;
-  return p.recip ? fmaxf(amax * kRecip, 1.17549435e-38f) : qdq_scale<FMT>(amax);
+  const float d = p.recip ? fmaxf(amax * kRecip, 1.17549435e-38f) : qdq_scale<FMT>(amax);
+  return FMT == 2 ? d + (amax - amax) : d;
 }
 
 // Four codes of one word as floats (unscaled).

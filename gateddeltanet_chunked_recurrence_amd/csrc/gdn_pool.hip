@@ -58,12 +58,12 @@ __global__ void __launch_bounds__(512) pool_write_kernel(PoolRef P, int64_t laye
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[i][e]));
+    for (int e = 0; e < 4; ++e) m = larger<FMT>(m, x[i][e]);
   // over the 16 columns of four lanes and the wave's 64 keys
-  m = fmaxf(m, dpp_f<0xB1>(m));
-  m = fmaxf(m, dpp_f<0x4E>(m));
-  m = fmaxf(m, __shfl_xor(m, 16, WAVE));
-  m = fmaxf(m, __shfl_xor(m, 32, WAVE));
+  m = larger<FMT>(m, dpp_f<0xB1>(m));
+  m = larger<FMT>(m, dpp_f<0x4E>(m));
+  m = larger<FMT>(m, __shfl_xor(m, 16, WAVE));
+  m = larger<FMT>(m, __shfl_xor(m, 32, WAVE));
   if (lane < 16 && (lane & 3) == 0) xm[wave][lane >> 2] = m;
   __syncthreads();
   // the tile's waves: its keys (KW of them) and, above 64 columns, its column blocks
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(512) pool_write_kernel(PoolRef P, int64_t laye
   const int q0 = bv >= 64 ? 0 : (cq >> 2) & ~(bv / 16 - 1), nq = bv >= 64 ? 4 : bv / 16;
   float amax = 0.f;
   for (int i = 0; i < KW * nb; ++i)
-    for (int q = 0; q < nq; ++q) amax = fmaxf(amax, xm[w0 + i][q0 + q]);
+    for (int q = 0; q < nq; ++q) amax = larger<FMT>(amax, xm[w0 + i][q0 + q]);
   const float d = pool_scale<FMT>(P, amax), r = 1.0f / d;
   uint8_t* dst = P.data + (layer_page + slot) * P.page + (int64_t)w.h * P.Dv * DK;
 #pragma unroll

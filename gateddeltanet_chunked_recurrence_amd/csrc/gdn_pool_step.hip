@@ -310,11 +310,11 @@ __device__ __forceinline__ void step_tile(const PoolRef& P, const char* hb, u32x
       f32x4 acc = mfma(pick[x & 1], b[j][x >> 2][(x >> 1) & 1], zero4());
       acc = mfma(kr, ub, acc);
       S[j][x] = acc;
-      m = fmaxf(fmaxf(m, fabsf(acc[0])), fabsf(acc[1]));
-      m = fmaxf(fmaxf(m, fabsf(acc[2])), fabsf(acc[3]));
+      m = larger<FMT>(larger<FMT>(m, acc[0]), acc[1]);
+      m = larger<FMT>(larger<FMT>(m, acc[2]), acc[3]);
     }
   }
-  d = pool_scale<FMT>(P, join(wave_max(m)) * unit);
+  d = pool_scale<FMT>(P, join(wave_largest<FMT>(m)) * unit);
   const float rd = (1.0f / d) * unit;
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -434,7 +434,7 @@ pool_step_many_kernel(PoolStepArgs a, int waves) {
             if (lane == 0) xm[t & 1][wave] = m;
             lds_barrier();
 #pragma unroll
-            for (int i = 0; i < NW; ++i) m = fmaxf(m, xm[t & 1][i]);
+            for (int i = 0; i < NW; ++i) m = larger<FMT>(m, xm[t & 1][i]);
           }
           return m;
         });
@@ -600,7 +600,7 @@ pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk
               if (lane == 0) xm[turn][wave] = m;
               lds_barrier();
 #pragma unroll
-              for (int i = 0; i < NW; ++i) m = fmaxf(m, xm[turn][i]);
+              for (int i = 0; i < NW; ++i) m = larger<FMT>(m, xm[turn][i]);
               turn ^= 1;
             }
             return m;

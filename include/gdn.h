@@ -404,8 +404,11 @@ gdn_status gdn_decode_bwd(const gdn_decode_bwd_args* a, void* stream);
  * pages stay as they were, outputs of the refused entries are NaN, and
  * GDN_DEVERR_POOL_SLOT is set. Entries refused for a slot outside the pool,
  * and entries with nothing to do (a step without tokens that copies to no
- * other page, a copy of a page to itself), read and write no page. States must be
- * finite.
+ * other page, a copy of a page to itself), read and write no page.
+ *
+ * States and inputs must be finite. What is not leaves NaN in the states that it
+ * reaches, for every later read and step to show: in the value row with FP32
+ * and E4M3 pages, in the whole scale tile (whose scale becomes NaN) with INT8.
  *
  * Sizes: Dk in {64, 128}; Dv in {64, 128, 256}; block_v 16, 32, 64, 128 or
  * 256 dividing Dv (ignored when OFF); at most 65535 entries, layers and groups per

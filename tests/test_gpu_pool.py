@@ -848,3 +848,66 @@ def test_tokens_out_of_a_longer_block():
         o1 = B.gdn_pool_step(a, 0, _ints([0]), lens=lens, **view)
         o2 = B.gdn_pool_step(b, 0, _ints([0]), lens=lens.clone(), **{k: v.clone() for k, v in view.items()})
         assert torch.equal(o1, o2) and _pool_same(a, _snapshot(b)) and B.device_errors() == 0
+
+
+# ------------------------------------------------------------- NaN and infinities
+@pytest.mark.parametrize("T", [1, 2])
+@pytest.mark.parametrize("fmt,dt,bv", [(INT8, torch.bfloat16, 64), (INT8, torch.float32, 16), (INT8, torch.bfloat16, 128),
+                                       (E4M3, torch.bfloat16, 64), (OFF, torch.float32, 64)])
+def test_a_nan_stays_in_the_page(fmt, dt, bv, T):
+    """A token whose inputs are not finite leaves NaN in the states that it
+    reaches, with every format, and the next tokens show it; other tiles and
+    sequences keep their bits."""
+    Hv, D, Bn = 2, 128, 7
+    pool, clean = (_random_pool(fmt, 1, Bn, Hv, D, D, bv, seed=68) for _ in range(2))
+    x = _draw(Bn, T, 1, Hv, D, D, dt, seed=69)
+    y = _draw(Bn, 1, 1, Hv, D, D, dt, seed=70)
+    lens = {} if T == 1 else dict(lens=_ints([T] * Bn))
+    slots = _ints(list(range(Bn)))
+    B.gdn_pool_step(clean, 0, slots, **lens, **x)
+    bad = {k: v.clone() for k, v in x.items()}
+    nan, inf = float('nan'), math.inf
+    bad['g'][1, 0, 0] = nan                               # head 0 of sequence 1
+    bad['beta'][2, 0, 1] = nan
+    bad['k'][3, 0, 0, 9] = nan                            # both heads
+    bad['v'][4, 0, 1, 70] = nan                           # one value row
+    bad['v'][5, 0, 0, 3] = inf
+    o = B.gdn_pool_step(pool, 0, slots, **lens, **bad)
+    rows = bv if fmt == INT8 else 1
+    hit = torch.zeros(Bn, Hv, D, dtype=torch.bool, device='cuda')
+    hit[1, 0] = hit[2, 1] = hit[3] = True
+    hit[4, 1, 70 // rows * rows: 70 // rows * rows + rows] = True
+    hit[5, 0, 3 // rows * rows: 3 // rows * rows + rows] = True
+    states = B.gdn_pool_read(pool, 0, slots)              # [Bn, Hv, Dk, Dv]
+    assert bool((~states.isfinite()).any(2)[hit].all())
+    if fmt == INT8:
+        assert bool(states.isnan().all(2)[hit].all())
+    tiles = hit.unflatten(-1, (-1, bv)).any(-1).repeat_interleave(bv, -1)
+    want = B.gdn_pool_read(clean, 0, slots)
+    assert torch.equal(states.mT[~tiles], want.mT[~tiles])
+    o2, o3 = (B.gdn_pool_step(p, 0, slots, **y) for p in (pool, clean))
+    assert not bool(o2[:, 0][hit].isfinite().any())
+    assert torch.equal(o2[:, 0][~tiles], o3[:, 0][~tiles])
+    assert not bool(B.gdn_pool_read(pool, 0, slots).isfinite().all(2)[hit].any())
+    assert B.device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt,Dk,Dv,bv", [(INT8, 128, 128, 64), (INT8, 64, 256, 16), (INT8, 128, 256, 256),
+                                          (E4M3, 128, 128, 64)])
+def test_a_nan_state_is_written_as_one(fmt, Dk, Dv, bv):
+    x = torch.randn(5, 2, Dk, Dv, device='cuda')
+    pool, clean = (B.StatePool(1, 5, 2, Dk, Dv, fmt, bv) for _ in range(2))
+    slots = _ints([0, 1, 2, 3, 4])
+    B.gdn_pool_write(clean, 0, slots, x)
+    hit = torch.zeros(5, 2, Dv // bv, dtype=torch.bool, device='cuda')
+    for n, h, i, j, val in ((0, 1, 0, 0, math.nan), (1, 0, Dk - 1, Dv - 1, math.nan), (3, 1, 37, 21, math.inf),
+                            (3, 0, 50, bv - 1, -math.nan)):
+        x[n, h, i, j] = val
+        hit[n, h, j // bv] = True
+    B.gdn_pool_write(pool, 0, slots, x)
+    got, want = (B.gdn_pool_read(p, 0, slots).unflatten(-1, (-1, bv)) for p in (pool, clean))
+    bad = ~got.isfinite()
+    assert torch.equal(bad.any(-1).any(2), hit)
+    if fmt == INT8:
+        assert bool(bad.all(-1).all(2)[hit].all())
+    assert torch.equal(got.permute(0, 1, 3, 2, 4)[~hit], want.permute(0, 1, 3, 2, 4)[~hit])
