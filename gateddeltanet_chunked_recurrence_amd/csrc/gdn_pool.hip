@@ -198,9 +198,9 @@ __global__ void __launch_bounds__(kMoveThreads) pool_copy_kernel(PoolRef P, cons
                                                                  int parts) {
   const int part = blockIdx.x, m = blockIdx.y, layer = blockIdx.z, lane = __lane_id();
   const int from = src[m], to = dst[m];
-  if (to == -1 || from == to) return;
-  const int64_t base = (int64_t)layer * P.slots;
   const bool ok = from >= -1 && from < P.slots && to >= 0 && to < P.slots;
+  if (to == -1 || (from == to && ok)) return;
+  const int64_t base = (int64_t)layer * P.slots;
   u32x4 x[U];
   const int64_t off = (int64_t)part * (U * kMoveThreads * 16) + threadIdx.x * 16;
   if (part < parts) {
@@ -248,10 +248,11 @@ pool_reorder_kernel(PoolRef P, const int32_t* slots, const int32_t* parents, int
     slot = slots[grp * width + lane];
     par = parents[grp * width + lane];
   }
-  // a beam moves when it has a page, a parent and they differ
+  // a beam moves when it has a page, a parent and they differ; a slot outside
+  // the pool is an error also where nothing moves
   const bool wants = slot != -1 && par != -1 && par != lane;
   const int from = __shfl(slot, par >= 0 && par < width ? par : 0, WAVE);
-  bool bad = wants && (par < 0 || par >= width || slot < 0 || slot >= P.slots || from < 0 || from >= P.slots);
+  bool bad = slot < -1 || slot >= P.slots || (wants && (par < 0 || par >= width || from < 0 || from >= P.slots));
   const uint64_t loads = __ballot(wants && !bad);
   const int64_t base = (int64_t)layer * P.slots;
   const int64_t off = (int64_t)part * (U * kMoveThreads * 16) + threadIdx.x * 16;

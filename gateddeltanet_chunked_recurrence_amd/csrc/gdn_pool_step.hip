@@ -368,7 +368,10 @@ pool_step_many_kernel(PoolStepArgs a, int waves) {
   const PoolRef& P = a.pool;
   const int r = lane & 15, g = lane >> 4;
   const StepUnit w = step_unit(a, wunit, RPW);
-  if (w.idle) return;                           // uniform over a tile's waves
+  if (w.idle) {                                 // uniform over a tile's waves
+    if (w.slot != -1 && !step_in_ok(a, w) && lane == 0) pool_error(P);
+    return;
+  }
   const int Hv = P.Hv, Dv = P.Dv, hk = w.h / (Hv / a.Hqk);
   const int64_t tok0 = (int64_t)w.n * a.T, o_tok = (int64_t)Hv * Dv;
   u32x4 raw[NT][NS];
@@ -638,7 +641,10 @@ __global__ void __launch_bounds__(4 * WAVE) pool_step_f32_kernel(PoolStepArgs a,
   const PoolRef& P = a.pool;
   const int lane = __lane_id(), c = lane & 7;
   const StepUnit w = step_unit(a, unit, kRows32);
-  if (w.idle) return;
+  if (w.idle) {
+    if (w.slot != -1 && !step_in_ok(a, w) && lane == 0) pool_error(P);
+    return;
+  }
   const int Hv = P.Hv, Dv = P.Dv, hk = w.h / (Hv / a.Hqk), row0 = w.row + (lane >> 3) * NR;
   const int64_t tok0 = (int64_t)w.n * a.T, o_tok = (int64_t)Hv * Dv;
   const int64_t head = ((int64_t)w.h * Dv + row0) * DK + 4 * c;

@@ -911,3 +911,28 @@ def test_a_nan_state_is_written_as_one(fmt, Dk, Dv, bv):
     if fmt == INT8:
         assert bool(bad.all(-1).all(2)[hit].all())
     assert torch.equal(got.permute(0, 1, 3, 2, 4)[~hit], want.permute(0, 1, 3, 2, 4)[~hit])
+
+
+# ------------------------------------------------------------- slots outside
+@pytest.mark.parametrize("fmt", [E4M3, OFF])
+def test_slots_outside_the_pool_are_always_reported(fmt):
+    """Also where the entry would have done nothing."""
+    pool = _random_pool(fmt, 1, 6, 2, 64, 64, 64, seed=64)
+    snap = _snapshot(pool)
+    x = _draw(2, 2, 1, 2, 64, 64, torch.bfloat16, seed=65)
+    calls = [lambda: B.gdn_pool_copy(pool, _ints([6, 0]), _ints([6, -1])),
+             lambda: B.gdn_pool_copy(pool, _ints([-2, 0]), _ints([-2, -1])),
+             lambda: B.gdn_pool_step(pool, 0, _ints([6, -1]), lens=_ints([0, 0]), **x),
+             lambda: B.gdn_pool_step(pool, 0, _ints([-1, -2]), lens=_ints([0, 0]), **x),
+             lambda: B.gdn_pool_step(pool, 0, _ints([7, -1]), slots_out=_ints([7, -1]), lens=_ints([0, 1]), **x),
+             lambda: B.gdn_pool_step(pool, 0, _ints([6, -1]), slots_out=_ints([-1, -1]), lens=_ints([0, 1]), **x),
+             lambda: B.gdn_pool_reorder(pool, _ints([[0, 6]]), _ints([[0, 1]])),
+             lambda: B.gdn_pool_reorder(pool, _ints([[0, -2]]), _ints([[-1, -1]]))]
+    for i, call in enumerate(calls):
+        call()
+        assert B.device_errors() == B.DEVERR_POOL_SLOT, i
+        assert _pool_same(pool, snap), i
+    B.gdn_pool_copy(pool, _ints([-1, -1, 0]), _ints([-1, -1, 0]))
+    B.gdn_pool_step(pool, 0, _ints([-1, 2]), lens=_ints([0, 0]), **x)
+    B.gdn_pool_reorder(pool, _ints([[0, -1, 2]]), _ints([[0, 1, -1]]))
+    assert B.device_errors() == 0 and _pool_same(pool, snap)
