@@ -731,7 +731,9 @@ def gdn_pool_prefill(pool, layer, slots, q, k, v, g, beta, scale=None, cu_seqlen
     not read), its final states written to the pages. Arguments as
     gdn_chunk_fwd; the state site uses the pool's format and tiles. Returns
     o. The final state passes the quantizer once, as in
-    gdn_prefill_decode_fwd."""
+    gdn_prefill_decode_fwd. The chunk forward has one scale rule, the division:
+    with a SCALE_RECIPROCAL pool the states between chunks are rounded by that,
+    and only the page is written by the pool's rule."""
     h0 = gdn_pool_read(pool, layer, slots) if resume else None
     o, ht, _ = gdn_chunk_fwd(q, k, v, g, beta, scale, h0, cu_seqlens, pool.state_fmt, w_fmt,
                              pool.block_v)

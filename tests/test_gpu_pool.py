@@ -936,3 +936,18 @@ def test_slots_outside_the_pool_are_always_reported(fmt):
     B.gdn_pool_step(pool, 0, _ints([-1, 2]), lens=_ints([0, 0]), **x)
     B.gdn_pool_reorder(pool, _ints([[0, -1, 2]]), _ints([[0, 1, -1]]))
     assert B.device_errors() == 0 and _pool_same(pool, snap)
+
+
+# ------------------------------------------------------------- scale rules
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
+def test_prefill_into_a_reciprocal_pool(fmt):
+    """The chunk forward divides; its final state is written by the pool's rule."""
+    N, T, Hv, D = 2, 70, 2, 128
+    x = _draw(N, T, 1, Hv, D, D, torch.bfloat16, seed=71)
+    pool, want = (B.StatePool(1, 3, Hv, D, D, fmt, 32, scale_rule=B.SCALE_RECIPROCAL) for _ in range(2))
+    slots = _ints([2, 0])
+    o = B.gdn_pool_prefill(pool, 0, slots, **x)
+    o2, ht, _ = B.gdn_chunk_fwd(x['q'], x['k'], x['v'], x['g'], x['beta'], h0=torch.zeros(N, Hv, D, D, device='cuda'),
+                                state_fmt=fmt, block_v=32)
+    B.gdn_pool_write(want, 0, slots, ht)
+    assert torch.equal(o, o2) and _pool_same(pool, _snapshot(want)) and B.device_errors() == 0
