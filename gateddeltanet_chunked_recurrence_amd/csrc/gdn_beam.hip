@@ -11,14 +11,15 @@
 // exponentials and its K largest logits with their tokens. The second kernel,
 // one workgroup per request, joins the parts: log-sums per beam, totals of
 // the candidates, the K best. Bound: reading the logits once from HBM. 512 rows
-// of 100,003 bf16 logits (102 MB): 40 us, of which the parts 32.0 and the join 8.2.
-// Reading alone takes 19 and the vector ALUs are busy for 16.5 (630 instructions per
+// of 100,003 bf16 logits (102 MB): 40 us, of which the parts 32.0 and the join 8.4
+// (FP32, 205 MB: 44 to 50). 100,003 logits are 6.1 parts of eight vectors per lane, so a
+// row's seventh part is a tenth full and costs what the others do. Reading alone takes 19 and the vector ALUs are busy for 16.5 (630 instructions per
 // wave of 4,096 elements: five per element for maximum and sum, the rest for the
 // choice); the two overlap little, as a workgroup waits for its loads first and
 // three times for its slowest wave later. Elements kept packed (74 VGPRs instead of
 // 100, more workgroups per CU) give the same time, workgroups that walk over
-// parts and load the next one early 44 (153 VGPRs). 4 rows of 131,072: 12 us (5.8 and
-// 6.4), two launches and their dependent loads. The 512 rows with all but 50 tokens
+// parts and load the next one early 44 (153 VGPRs). 4 rows of 131,072: 12 us (5.9 and
+// 6.5), two launches and their dependent loads. The 512 rows with all but 50 tokens
 // masked: 46 us with -inf, 100 with the type's lowest value (636 when equal logits
 // were taken one by one).
 //
@@ -40,7 +41,7 @@
 // across parts and for the totals. An exponential is 2^(x L - C) with L =
 // fl(log2 e) and C = fl(m L), one FMA, rounded relative to the small difference;
 // that C and L are rounded themselves is taken back in FP64 at the end (see
-// log_sum).
+// log_sum); from |m| = 2^20 on the difference is taken first.
 #include "gdn_device.h"
 #include "gdn_launch.h"
 

@@ -22,8 +22,8 @@ constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126, the scale of a zero t
 // accesses, 256 contiguous bytes per key, and 16-byte code accesses, 64
 // contiguous bytes per value row; the transposition between the key-major
 // states and the value-major pages is then only the choice of registers. 64
-// sequences of 16 heads of 128 x 128 (67 MB of FP32, 17 MB of codes): 16.7 us to
-// pages, 14.5 from them, 5.0 and 5.8 TB/s.
+// sequences of 16 heads of 128 x 128 (67 MB of FP32, 17 MB of codes): 17.2 us to
+// pages, 14.8 from them, 4.9 and 5.7 TB/s.
 template <int DK>
 struct XchgPos {
   int n, h, col, key;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(512) pool_read_kernel(PoolRef P, int64_t layer
 // keys; lane (cq = lane & 7, kq = lane >> 3) moves 4 x 4 blocks at columns
 // 4 cq and keys 4 kq (+ 32 for the second block), whole 128-byte lines on both
 // sides: eight lanes along the columns in a load, eight along the keys in a
-// store.
+// store. 64 sequences of 16 heads of 128 x 128, out and in (268 MB): 60 us, 4.5 TB/s.
 template <bool WRITE>
 __global__ void __launch_bounds__(256) pool_f32_kernel(PoolRef P, int64_t layer_page,
                                                        const int32_t* slots, int count,
@@ -235,8 +235,10 @@ __global__ void __launch_bounds__(kMoveThreads) pool_copy_kernel(PoolRef P, cons
 // bytes), so no page is read after it was written and no staging copy is
 // needed; each page that changes is written once and each parent read once
 // from HBM (a second beam of the same parent hits a cache). Beams that keep
-// their own page move nothing. 16 groups of 4 beams, 12 layers (268 MB): 49 us
-// (5.4 TB/s); with plain stores 64, with one part per lane 55.
+// their own page move nothing. 16 groups of 4 beams, 12 layers (268 MB): 47 us
+// (5.7 TB/s; 44 to 49 by what the caches still hold); with plain stores 64, with one
+// part per lane 55. 4 groups of 16 (314 MB) take 57 us, 2 of 32 (321 MB) 56, though
+// the widest bucket holds 167 registers and spills scalars.
 template <int W, int U>
 __global__ void __launch_bounds__(kMoveThreads)
 pool_reorder_kernel(PoolRef P, const int32_t* slots, const int32_t* parents, int width, int parts) {

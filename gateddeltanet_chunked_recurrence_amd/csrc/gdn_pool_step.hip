@@ -35,17 +35,23 @@
 // vector ALUs.
 //
 // Measured, E4M3 with bf16 inputs, read from one page and written to another: 1,024
-// sequences of 32 heads (128 x 256) 439 us, 4.1 TB/s; a plain copy of the same pages
+// sequences of 32 heads (128 x 256) 436 us; a plain copy of the same pages
 // at random places takes 360 to 400, this loop without its stores 303, with nothing but
-// loads and stores 445. 192 sequences of 16 heads (128 x 128) 25 us, 3.2 TB/s:
+// loads and stores 445. Counters: 1,096 MB read and 1,094 written, 5.0 TB/s, where
+// the distinct parents and the inputs are 713 MB: each child of a parent reads it
+// from beyond L2 again. 192 sequences of 16 heads (128 x 128) 25.6 us, 3.2 TB/s:
 // about two tiles per wave, so loads and stores of the ends stand alone.
-// One sequence 5.4 us: a launch and one trip to HBM after the slots. Dropped: two
-// tiles ahead at two waves per SIMD 508 us (spills at three), tiles unquantized twice
-// instead of held at four waves 457, non-temporal stores 474, one wave per
-// tile without the loop 530 to 555. Inputs in FP32 take 27 us where bf16 takes
-// 25: the parts of k and q are made once per head, in LDS (53 us when every
-// tile split them again). INT8 at 192 sequences: 36 us, the conversions to bf16 by
-// way of floats bind it.
+// One sequence 5.5 us: a launch and one trip to HBM after the slots. Dropped: two
+// tiles ahead at two waves per SIMD 508 us (it spills at three), tiles unquantized
+// twice instead of held at four waves 457, non-temporal stores 474, one wave per tile
+// without the loop 530 to 555. What is kept fills the 168 registers of three waves
+// too: with 128 keys and two row tiles most E4M3 variants keep up to 60 bytes a lane in
+// scratch (the 192 sequences 28, 5 MB written; the 1,024 none). Inputs in FP32 take 27 to 30 us where bf16 takes 25: the parts of k and q are
+// made once per head, in LDS (53 us when every tile split them again). INT8 at 192
+// sequences: 35 us. Two things bind it: the conversions to bf16 by way of floats
+// (a shift, an extraction and a conversion per element), and that the compiler
+// carries the next tile's codes as bytes, whose shifts stand right behind their
+// loads and wait for them before this tile's products.
 #include <algorithm>
 
 #include "gdn_device.h"
@@ -629,7 +635,7 @@ pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk
 // Eight lanes per row, four keys of every 32 each, so that they touch whole
 // 128-byte lines in each load; a row sum is DK / 8 FMAs and three DPP adds. One
 // wave holds kRows32 rows, four per eight lanes; waves are independent. 90
-// sequences of up to 5 tokens, 6 heads of 64 x 64 (9 MB in, 9 out): 7.6 us, 8.2
+// sequences of up to 5 tokens, 6 heads of 64 x 64 (9 MB in, 9 out): 7.5 us, 8.2
 // without the next token's loads ahead; bound by latency (four waves per CU).
 constexpr int kRows32 = 32;
 template <int DK, bool F32>
@@ -739,7 +745,7 @@ void launch_codes_wpt(const PoolStepArgs& a, hipStream_t s) {
     // Groups that fit the device at three waves per SIMD. With at least as many
     // heads, an element is a whole head, and at most two per group: one
     // group for its share of all elements was slower at 1,024 sequences of 32
-    // heads (467 us against 439 with two and 442 with one).
+    // heads (467 us against 439 with two and 442 with one, of one build).
     const int tph = a.pool.Dv / a.pool.block_v, gpb = NW / WPT, heads = a.B * a.pool.Hv;
     const int room = device_cus() * std::max(1, 12 / NW) * gpb, span = heads >= room ? tph : 1;
     const int elems = heads * (tph / span), chunk = std::min(2, (elems + room - 1) / room);
@@ -757,9 +763,11 @@ void launch_codes_wpt(const PoolStepArgs& a, hipStream_t s) {
 }
 
 // 16-row tiles per wave: two, or one where the integer format's conversions
-// would spill at 128 keys (192 sequences of 16 heads, Dv 128, tiles of 32, 64 and
-// 128: 32, 35 and 53 us with one, 57, 65 and 74 with two; E4M3 28, 29 and 35 with
-// one, 26, 26 and 30 with two).
+// would spill at 128 keys (192 sequences of 16 heads; tiles of 32, 64 and 128 at Dv
+// 128, of 256 at Dv 256: 31, 35, 53 and 111 us with one, 74, 77, 85 and 186 with two;
+// E4M3 27.5, 28, 34 and 71 with one, 25.4, 25.4, 30 and 65.5 with two). A tile of 16
+// is one. INT8 tiles of 256 at 128 keys are 16 waves, which caps them at 128
+// registers: they spill 25 to 51.
 template <int DK, int FMT, bool F32>
 void launch_codes(const PoolStepArgs& a, hipStream_t s) {
   constexpr int NT = FMT == 2 && DK == 128 ? 1 : 2;

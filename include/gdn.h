@@ -462,7 +462,10 @@ gdn_status gdn_pool_reorder(const gdn_pool* pool, const int32_t* slots, const in
 /* Recurrent step: tokens 0 .. lens[b] - 1 of each of B sequences from the
  * states in `slots`, as gdn_decode_fwd computes them (the state is a written
  * one already: there is no first write), the last written state to
- * `slots_out`. FP32 arithmetic. */
+ * `slots_out`. FP32 arithmetic; with pages of codes the sums run on the matrix
+ * cores and the update is formed in units of the decayed scale, so that a code
+ * next to a border, or a scale's last place, may come out as the other one
+ * than gdn_decode_fwd's. There |beta (v - alpha S^T k)| has to stay below 2^63. */
 typedef struct {
   int32_t B, T, Hqk;           /* T tokens per row of the batch               */
   int32_t io_dtype;            /* gdn_dtype of q, k, v and o                  */
@@ -496,7 +499,8 @@ gdn_status gdn_pool_step(const gdn_pool* pool, const gdn_pool_step_args* a, void
  * beams: with logp[b, w, t] = x - log sum exp x over the vocabulary and total =
  * scores[b, w] + logp, the K best (w, t) of each request, best first; equal
  * totals go to the lower beam, then the lower token. Totals are compared in
- * 64 bits (two beams' totals seldom differ by much) and returned in FP32. A
+ * 64 bits (two beams' totals seldom differ by much) and returned in FP32 (-inf
+ * for one below its range, with its parent and token all the same). A
  * finished beam offers one candidate, pad_token with logp 0. Logits of -inf
  * are masked and NaN counts as masked; +inf counts as the largest finite
  * value. Candidates with total -inf are never chosen: where fewer than K
