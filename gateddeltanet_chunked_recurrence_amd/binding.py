@@ -72,6 +72,19 @@ class BeamArgs(ctypes.Structure):
                 ('workspace', c_vp), ('workspace_bytes', c_sz)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [('B', c_i32), ('T', c_i32), ('Hqk', c_i32), ('Hv', c_i32), ('Dk', c_i32), ('Dv', c_i32),
+                ('num_seqs', c_i32), ('io_dtype', c_i32), ('g_per_head', c_i32), ('scale', c_f32),
+                ('q_stride', c_i64), ('k_stride', c_i64), ('v_stride', c_i64), ('q', c_vp), ('k', c_vp),
+                ('v', c_vp), ('g', c_vp), ('h0', c_vp), ('cu_seqlens', c_vp), ('o', c_vp), ('ht', c_vp),
+                ('workspace', c_vp), ('workspace_bytes', c_sz)]
+
+
+class LinearBwdArgs(ctypes.Structure):
+    _fields_ = [('fwd', LinearArgs), ('do_', c_vp), ('dht', c_vp), ('dq', c_vp), ('dk', c_vp), ('dv', c_vp),
+                ('dg', c_vp), ('dh0', c_vp), ('workspace', c_vp), ('workspace_bytes', c_sz)]
+
+
 class SavedLayout(ctypes.Structure):
     _fields_ = [('num_slots', c_i64), ('off_state', c_i64), ('off_state_scale', c_i64),
                 ('off_w', c_i64), ('off_w_scale', c_i64), ('off_x', c_i64), ('off_anchor', c_i64),
@@ -115,7 +128,9 @@ def load_library():
                                              c_vp]),
                        ('gdn_pool_step', [ctypes.POINTER(PoolStruct), ctypes.POINTER(PoolStepArgs),
                                           c_vp]),
-                       ('gdn_beam_select', [ctypes.POINTER(BeamArgs), c_vp])):
+                       ('gdn_beam_select', [ctypes.POINTER(BeamArgs), c_vp]),
+                       ('gdn_linear_fwd', [ctypes.POINTER(LinearArgs), c_vp]),
+                       ('gdn_linear_bwd', [ctypes.POINTER(LinearBwdArgs), c_vp])):
         f = getattr(lib, name)
         f.argtypes = argt
         f.restype = c_i32
@@ -135,6 +150,10 @@ def load_library():
     lib.gdn_decode_bwd_workspace_bytes.restype = c_sz
     lib.gdn_beam_workspace_bytes.argtypes = [ctypes.POINTER(BeamArgs)]
     lib.gdn_beam_workspace_bytes.restype = c_sz
+    lib.gdn_linear_fwd_workspace_bytes.argtypes = [ctypes.POINTER(LinearArgs)]
+    lib.gdn_linear_fwd_workspace_bytes.restype = c_sz
+    lib.gdn_linear_bwd_workspace_bytes.argtypes = [ctypes.POINTER(LinearBwdArgs)]
+    lib.gdn_linear_bwd_workspace_bytes.restype = c_sz
     _LIB = lib
     return lib
 
@@ -798,3 +817,93 @@ def gdn_beam_advance(pool, slots, logits, scores, finished=None, pad_token=0):
     out, parents, tokens = gdn_beam_select(logits, scores, None, finished, pad_token)
     gdn_pool_reorder(pool, slots, parents)
     return out, parents, tokens
+
+
+# ------------------------------------------------------------ linear attention
+def _linear_args(q, k, v, g, scale, h0, cu_seqlens):
+    """The forward arguments of linear attention, from checked tensors; and (N, Hv, Dk, Dv)."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f'q: [B, T, Hqk, Dk], v: [B, T, Hv, Dv]; got {list(q.shape)} and {list(v.shape)}')
+    (B, T, Hqk, Dk), (Hv, Dv), dt, dev = q.shape, v.shape[2:], q.dtype, q.device
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f'q: bfloat16 or float32, not {dt}')
+    N = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError(f'cu_seqlens: [N + 1]; got {list(cu_seqlens.shape)}')
+        _need(cu_seqlens, 'cu_seqlens', torch.int32, cu_seqlens.shape, dev)
+        N = cu_seqlens.shape[0] - 1
+    a = LinearArgs(B=B, T=T, Hqk=Hqk, Hv=Hv, Dk=Dk, Dv=Dv, num_seqs=N,
+                   io_dtype=GDN_BF16 if dt is torch.bfloat16 else GDN_F32, g_per_head=g.dim() == 1,
+                   scale=Dk ** -0.5 if scale is None else scale)
+    a.q_stride = _token_stride(q, 'q', (B, T, Hqk, Dk), dt, dev)
+    a.k_stride = _token_stride(k, 'k', (B, T, Hqk, Dk), dt, dev)
+    a.v_stride = _token_stride(v, 'v', (B, T, Hv, Dv), dt, dev)
+    _need(g, 'g', torch.float32, (Hv,) if g.dim() == 1 else (B, T, Hv), dev)
+    a.q, a.k, a.v, a.g = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr()
+    if h0 is not None:
+        _need(h0, 'h0', torch.float32, (N, Hv, Dk, Dv), dev)
+        a.h0 = h0.data_ptr()
+    if cu_seqlens is not None:
+        a.cu_seqlens = cu_seqlens.data_ptr()
+    return a, (N, Hv, Dk, Dv)
+
+
+def gdn_linear_fwd(q, k, v, g, scale=None, h0=None, cu_seqlens=None, output_final_state=True, out=None):
+    """Linear attention with a decay per head, S <- exp(g) S + k v^T and
+    o = scale S^T q, over whole prompts: q, k [B, T, Hqk, Dk], v [B, T, Hv, Dv]
+    (bf16 or FP32; token strides are free), g FP32, the log-decay [B, T, Hv], or [Hv]
+    for one per head; h0 [N, Hv, Dk, Dv] FP32 or None; cu_seqlens int32 [N + 1]
+    (B = 1) or None. Returns (o [B, T, Hv, Dv] in q's type, ht FP32 or None).
+    Tokens that no sequence holds are not written."""
+    a, state = _linear_args(q, k, v, g, scale, h0, cu_seqlens)
+    dev, shape = q.device, (a.B, a.T, a.Hv, a.Dv)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    else:
+        _need(out, 'out', q.dtype, shape, dev)
+    ht = torch.empty(state, dtype=torch.float32, device=dev) if output_final_state else None
+    a.o, a.ht = out.data_ptr(), None if ht is None else ht.data_ptr()
+    lib = load_library()
+    ref = ctypes.byref(a)
+    nbytes = lib.gdn_linear_fwd_workspace_bytes(ref)
+    if nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+    _launch(lib.gdn_linear_fwd, dev, ref)
+    return out, ht
+
+
+def gdn_linear_bwd(q, k, v, g, do, dht=None, scale=None, h0=None, cu_seqlens=None, out=None):
+    """Gradients of gdn_linear_fwd from its inputs, do [B, T, Hv, Dv] (the type of
+    q, contiguous) and dht [N, Hv, Dk, Dv] FP32 or None. Returns dict dq, dk, dv (the
+    type of q), dg FP32 in g's shape, and dh0 FP32 when h0 is given. Tokens
+    that no sequence holds are not written. out: optional dict of dq, dk, dv, dg to
+    write to."""
+    a, state = _linear_args(q, k, v, g, scale, h0, cu_seqlens)
+    dev, dt = q.device, q.dtype
+    _need(do, 'do', dt, (a.B, a.T, a.Hv, a.Dv), dev)
+    if out is None:
+        out = dict(dq=torch.empty(q.shape, dtype=dt, device=dev), dk=torch.empty(k.shape, dtype=dt, device=dev),
+                   dv=torch.empty(v.shape, dtype=dt, device=dev),
+                   dg=torch.empty(g.shape, dtype=torch.float32, device=dev))
+    else:
+        out = dict(out)
+        for name, t, of in (('dq', q, dt), ('dk', k, dt), ('dv', v, dt), ('dg', g, torch.float32)):
+            _need(out[name], name, of, t.shape, dev)
+    if h0 is not None:
+        out['dh0'] = torch.empty(state, dtype=torch.float32, device=dev)
+    b = LinearBwdArgs(fwd=a, do_=do.data_ptr(), dq=out['dq'].data_ptr(), dk=out['dk'].data_ptr(),
+                      dv=out['dv'].data_ptr(), dg=out['dg'].data_ptr(),
+                      dh0=out['dh0'].data_ptr() if h0 is not None else None)
+    if dht is not None:
+        _need(dht, 'dht', torch.float32, state, dev)
+        b.dht = dht.data_ptr()
+    lib = load_library()
+    ref = ctypes.byref(b)
+    nbytes = lib.gdn_linear_bwd_workspace_bytes(ref)
+    if nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        b.workspace, b.workspace_bytes = ws.data_ptr(), nbytes
+    _launch(lib.gdn_linear_bwd, dev, ref)
+    return out

@@ -856,6 +856,134 @@ gdn_status check_beam_parts(const gdn::BeamArgs& k) {
   return GDN_OK;
 }
 
+// ------------------------------------------------------- linear attention
+gdn_status check_linear(const gdn_linear_args* a, const char* what) {
+  if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
+  if (a->B < 0 || a->T < 0 || a->Hqk <= 0 || a->Hv <= 0 || a->num_seqs < 0)
+    return fail(GDN_E_INVALID, "%s: bad sizes B=%d T=%d Hqk=%d Hv=%d", what, a->B, a->T, a->Hqk, a->Hv);
+  if (a->Hv % a->Hqk != 0)
+    return fail(GDN_E_INVALID, "%s: Hv (%d) must be a multiple of Hqk (%d)", what, a->Hv, a->Hqk);
+  if (a->Hv > 65535) return fail(GDN_E_UNSUPPORTED, "%s: Hv %d exceeds 65535", what, a->Hv);
+  if (a->Dk != 64 && a->Dk != 128) return fail(GDN_E_UNSUPPORTED, "%s: Dk %d: supported 64, 128", what, a->Dk);
+  if (a->Dv != 64 && a->Dv != 128 && a->Dv != 256)
+    return fail(GDN_E_UNSUPPORTED, "%s: Dv %d: supported 64, 128, 256", what, a->Dv);
+  if (a->io_dtype != GDN_BF16 && a->io_dtype != GDN_F32)
+    return fail(GDN_E_INVALID, "io_dtype %d: use 0 bf16 or 1 f32", a->io_dtype);
+  if (a->g_per_head != 0 && a->g_per_head != 1)
+    return fail(GDN_E_INVALID, "%s: g_per_head %d: use 0 per token or 1 per head", what, a->g_per_head);
+  if (!std::isfinite(a->scale)) return fail(GDN_E_INVALID, "scale is not finite");
+  if (a->cu_seqlens) {
+    if (a->B != 1) return fail(GDN_E_INVALID, "cu_seqlens needs B == 1 (got %d)", a->B);
+    if (a->num_seqs < 1) return fail(GDN_E_INVALID, "num_seqs %d < 1 with cu_seqlens", a->num_seqs);
+  } else if (a->num_seqs != a->B) {
+    return fail(GDN_E_INVALID, "num_seqs (%d) must equal B (%d) without cu_seqlens", a->num_seqs, a->B);
+  }
+  if (a->num_seqs > 65535) return fail(GDN_E_UNSUPPORTED, "num_seqs %d exceeds 65535", a->num_seqs);
+  const int64_t tokens = (int64_t)a->B * a->T;
+  if (tokens > (1 << 30)) return fail(GDN_E_UNSUPPORTED, "B*T = %lld tokens exceeds 2^30", (long long)tokens);
+  const int64_t es = a->io_dtype == GDN_F32 ? 4 : 2;
+  const int64_t row_qk = (int64_t)a->Hqk * a->Dk, row_v = (int64_t)a->Hv * a->Dv;
+  const struct { int64_t stride, row; const char* name; } strides[] = {
+      {a->q_stride, row_qk, "q"}, {a->k_stride, row_qk, "k"}, {a->v_stride, row_v, "v"}};
+  for (const auto& e : strides)
+    if (e.stride != 0 && (e.stride < e.row || e.stride * es % 16 != 0 || e.stride >= (1 << 24)))
+      return fail(GDN_E_INVALID, "%s: %s_stride %lld: at least %lld, below 2^24 and a multiple of 16 bytes", what,
+                  e.name, (long long)e.stride, (long long)e.row);
+  // every grid: (segments, at most chunks + sequences) x heads x slabs, and vectors of a state per head
+  if ((tokens / 32 + a->num_seqs + 1) * a->Hv * 4 > INT32_MAX || (int64_t)a->num_seqs * a->Hv * 32 > INT32_MAX)
+    return fail(GDN_E_UNSUPPORTED, "%s: (chunks + sequences) * Hv is too large", what);
+  return GDN_OK;
+}
+
+gdn::LinearPlan plan_linear(const gdn_linear_args* a, bool bwd) {
+  return gdn::linear_plan(a->num_seqs, a->T, (int64_t)a->B * a->T, a->cu_seqlens != nullptr, a->Hv, a->Dv,
+                          a->io_dtype == GDN_F32, bwd);
+}
+
+// Offsets of the workspace's parts.
+struct LinearWs {
+  int64_t state = 0, dstate = 0, decay = 0, qdq = 0, kdk = 0, end = 0, dgsum = 0, dq = 0, dk = 0, total = 0;
+};
+LinearWs linear_ws(const gdn_linear_args* a, const gdn::LinearPlan& p, bool bwd) {
+  LinearWs w;
+  const int64_t sh = p.slots * a->Hv, state = sh * a->Dk * a->Dv * 4;
+  auto part = [&](int64_t& off, int64_t bytes) {
+    off = w.total;
+    w.total = round256(w.total + bytes);
+  };
+  if (p.segmented) {
+    part(w.state, state);
+    if (bwd) part(w.dstate, state);
+    part(w.decay, sh * 4);
+  }
+  if (bwd) {
+    const int64_t dots = p.chunk_slots * a->Hv * p.chunk * 4;
+    part(w.qdq, dots);
+    part(w.kdk, dots);
+    part(w.end, sh * 4);
+    if (a->g_per_head) part(w.dgsum, sh * 8);
+    if (a->Hv != a->Hqk) {
+      const int64_t parts = (int64_t)a->B * a->T * a->Hv * a->Dk * 4;
+      part(w.dq, parts);
+      part(w.dk, parts);
+    }
+  }
+  return w;
+}
+
+gdn::LinearArgs linear_args(const gdn_linear_args* a, const gdn::LinearPlan& p, const LinearWs& w, bool bwd, void* ws) {
+  gdn::LinearArgs k{};
+  k.q = a->q;
+  k.k = a->k;
+  k.v = a->v;
+  k.g = a->g;
+  k.h0 = a->h0;
+  k.cu_seqlens = a->cu_seqlens;
+  k.qs = a->q_stride ? a->q_stride : (int64_t)a->Hqk * a->Dk;
+  k.ks = a->k_stride ? a->k_stride : (int64_t)a->Hqk * a->Dk;
+  k.vs = a->v_stride ? a->v_stride : (int64_t)a->Hv * a->Dv;
+  k.gs = a->g_per_head ? 0 : a->Hv;
+  char* b = static_cast<char*>(ws);
+  auto at = [&](int64_t off) { return reinterpret_cast<float*>(b + off); };
+  if (p.segmented) {
+    k.ws_state = at(w.state);
+    if (bwd) k.ws_dstate = at(w.dstate);
+    k.ws_decay = at(w.decay);
+  }
+  if (bwd) {
+    k.ws_qdq = at(w.qdq);
+    k.ws_kdk = at(w.kdk);
+    k.ws_end = at(w.end);
+    if (a->g_per_head) k.ws_dgsum = reinterpret_cast<double*>(b + w.dgsum);
+    if (a->Hv != a->Hqk) {
+      k.ws_dq = at(w.dq);
+      k.ws_dk = at(w.dk);
+    }
+  }
+  k.N = a->num_seqs;
+  k.T = a->T;
+  k.tokens = a->B * a->T;
+  k.Hqk = a->Hqk;
+  k.Hv = a->Hv;
+  k.Dk = a->Dk;
+  k.Dv = a->Dv;
+  k.seg = p.seg;
+  k.slots = (int32_t)p.slots;
+  k.scale = a->scale;
+  return k;
+}
+
+struct LinearPtr { const void* p; const char* name; bool required; };
+gdn_status check_linear_ptrs(const char* what, const LinearPtr* e, int n, const float* g) {
+  for (int i = 0; i < n; ++i) {
+    if (e[i].required && !e[i].p) return fail(GDN_E_INVALID, "%s: %s is NULL", what, e[i].name);
+    const uintptr_t align = e[i].p == g ? 4 : 16;
+    if (reinterpret_cast<uintptr_t>(e[i].p) % align)
+      return fail(GDN_E_INVALID, "%s: %s is not %d-byte aligned", what, e[i].name, (int)align);
+  }
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1251,6 +1379,68 @@ gdn_status gdn_beam_select(const gdn_beam_args* a, void* stream) {
   if (!a->workspace || a->workspace_bytes < need)
     return fail(GDN_E_WORKSPACE, "workspace of %zu bytes given, %zu needed", a->workspace_bytes, need);
   return hip_status(gdn::launch_beam_select(k, static_cast<hipStream_t>(stream)), "gdn_beam_select launch");
+}
+
+size_t gdn_linear_fwd_workspace_bytes(const gdn_linear_args* a) {
+  if (check_linear(a, "gdn_linear_fwd") != GDN_OK) return 0;
+  const gdn::LinearPlan p = plan_linear(a, false);
+  return (size_t)linear_ws(a, p, false).total;
+}
+
+gdn_status gdn_linear_fwd(const gdn_linear_args* a, void* stream) {
+  const char* what = "gdn_linear_fwd";
+  gdn_status s = check_linear(a, what);
+  if (s != GDN_OK) return s;
+  const bool any = (int64_t)a->B * a->T > 0;
+  const LinearPtr ptrs[] = {{a->q, "q", any}, {a->k, "k", any}, {a->v, "v", any}, {a->g, "g", any},
+                            {a->o, "o", any}, {a->h0, "h0", false}, {a->ht, "ht", false},
+                            {a->workspace, "workspace", false}};
+  if ((s = check_linear_ptrs(what, ptrs, sizeof(ptrs) / sizeof(*ptrs), a->g)) != GDN_OK) return s;
+  if (a->num_seqs == 0 || (!any && !a->ht)) return GDN_OK;
+  const gdn::LinearPlan p = plan_linear(a, false);
+  const LinearWs w = linear_ws(a, p, false);
+  if (w.total && (!a->workspace || a->workspace_bytes < (size_t)w.total))
+    return fail(GDN_E_WORKSPACE, "workspace of %zu bytes given, %lld needed", a->workspace_bytes, (long long)w.total);
+  gdn::LinearArgs k = linear_args(a, p, w, false, a->workspace);
+  k.o = a->o;
+  k.ht = a->ht;
+  return hip_status(gdn::launch_linear_fwd(k, a->io_dtype == GDN_F32, static_cast<hipStream_t>(stream)),
+                    "gdn_linear_fwd launch");
+}
+
+size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_bwd_args* a) {
+  if (!a || check_linear(&a->fwd, "gdn_linear_bwd") != GDN_OK) return 0;
+  const gdn::LinearPlan p = plan_linear(&a->fwd, true);
+  return (size_t)linear_ws(&a->fwd, p, true).total;
+}
+
+gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* a, void* stream) {
+  const char* what = "gdn_linear_bwd";
+  if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
+  const gdn_linear_args* f = &a->fwd;
+  gdn_status s = check_linear(f, what);
+  if (s != GDN_OK) return s;
+  const bool any = (int64_t)f->B * f->T > 0;
+  const LinearPtr ptrs[] = {{f->q, "q", any},  {f->k, "k", any},   {f->v, "v", any},   {f->g, "g", any},
+                            {a->do_, "do", any}, {a->dq, "dq", any}, {a->dk, "dk", any}, {a->dv, "dv", any},
+                            {a->dg, "dg", any || f->g_per_head}, {f->h0, "h0", false}, {a->dht, "dht", false},
+                            {a->dh0, "dh0", false}, {a->workspace, "workspace", false}};
+  if ((s = check_linear_ptrs(what, ptrs, sizeof(ptrs) / sizeof(*ptrs), f->g)) != GDN_OK) return s;
+  if (f->num_seqs == 0 && !f->g_per_head) return GDN_OK;
+  const gdn::LinearPlan p = plan_linear(f, true);
+  const LinearWs w = linear_ws(f, p, true);
+  if (w.total && (!a->workspace || a->workspace_bytes < (size_t)w.total))
+    return fail(GDN_E_WORKSPACE, "workspace of %zu bytes given, %lld needed", a->workspace_bytes, (long long)w.total);
+  gdn::LinearArgs k = linear_args(f, p, w, true, a->workspace);
+  k.dout = a->do_;
+  k.dht = a->dht;
+  k.dq = a->dq;
+  k.dk = a->dk;
+  k.dv = a->dv;
+  k.dg = a->dg;
+  k.dh0 = a->dh0;
+  return hip_status(gdn::launch_linear_bwd(k, f->io_dtype == GDN_F32, static_cast<hipStream_t>(stream)),
+                    "gdn_linear_bwd launch");
 }
 
 }  // extern "C"

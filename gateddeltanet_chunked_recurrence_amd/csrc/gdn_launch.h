@@ -323,6 +323,47 @@ void beam_plan(BeamArgs& a);
 int64_t beam_workspace_bytes(const BeamArgs& a);
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
 
+// Linear attention with a decay per head (gdn_linear.hip).
+struct LinearArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* dout;           // backward only, contiguous
+  const float* g;
+  const float* h0;            // nullable (zero states)
+  const float* dht;           // nullable (zero)
+  const int32_t* cu_seqlens;  // nullable
+  void* o;
+  float* ht;                  // nullable
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dg;                  // [tokens, Hv], or [Hv] with ws_dgsum
+  float* dh0;                 // nullable
+  int64_t qs, ks, vs, gs;     // elements between tokens (gs 0: one gate per head)
+  // workspace
+  float* ws_state;            // [slots, Hv, Dk, Dv] state before each segment, nullable (one segment each)
+  float* ws_dstate;           // same, gradient of the state after it
+  float* ws_decay;            // [slots, Hv] decay over each segment
+  float* ws_qdq;              // [chunk slots, Hv, C] q . dq, the state's part
+  float* ws_kdk;              // same, the pairs' row minus column sums minus k . dk of the state's part
+  float* ws_end;              // [slots, Hv] <dS, S> at the segment's end
+  double* ws_dgsum;           // [slots, Hv], one gate per head only
+  float* ws_dq;               // [tokens, Hv, Dk] per value head, where heads share q and k
+  float* ws_dk;
+  int32_t N, T, tokens, Hqk, Hv, Dk, Dv;
+  int32_t seg, slots;         // chunks per segment, segments
+  float scale;
+};
+struct LinearPlan {
+  int seg, chunk;             // chunks per segment, tokens per chunk
+  bool segmented;             // some sequence may have several segments
+  int64_t slots, chunk_slots;
+};
+LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dv, bool f32, bool bwd);
+hipError_t launch_linear_fwd(const LinearArgs& a, bool f32, hipStream_t s);
+hipError_t launch_linear_bwd(const LinearArgs& a, bool f32, hipStream_t s);
+
 hipError_t launch_decode_fwd(const DecodeConfig& c, const DecodeKernelArgs& a, hipStream_t s);
 hipError_t launch_decode_bwd(const DecodeConfig& c, const DecodeKernelArgs& a, hipStream_t s);
 

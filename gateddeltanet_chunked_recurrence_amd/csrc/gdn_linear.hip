@@ -1,0 +1,824 @@
+// Linear attention with a decay per head: chunked forward and its gradients.
+//
+// Per (sequence, value head), with S_0 = h0:
+//   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+// In chunks of C tokens (gam the inclusive cumsum of g within the chunk, S the
+// state before it, n its last token):
+//   o_i = scale (e^gam_i S^T q_i + sum_{j <= i} e^(gam_i - gam_j) (q_i . k_j) v_j)
+//   S' = e^gam_n S + sum_j e^(gam_n - gam_j) k_j v_j^T
+// The gradients are walks of the same form. With dS the gradient of the state
+// after the chunk:
+//   dq: the forward walk of (do, v, k): state S^T
+//   dk: the reverse walk of (v, do, q): state dS^T, weights scale e^(gam_i - gam_j), i >= j
+//   dv: the reverse walk of (k, q, do): state dS
+//   dS <- e^gam_n dS + scale sum_i e^gam_i q_i do_i^T
+// so one walk over (X, Y, Z) serves all: out = x S + (X Y^T * weights) Z, and S
+// takes Y^T Z. Gates: only the terms of a chunk t that reach over it,
+//   dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <dS, S'>,
+// where pairs (i, j) of one chunk enter as row and column sums of M = P * dP, the
+// reads and writes of states as q . dq and k . dk of the state's part alone, and
+// <dS, S'> is taken from both states at the end of each segment and carried
+// from chunk to chunk by these sums. So dg has no rounded product in it.
+//
+// A walk is sequential in its chunks. Where the heads alone do not fill the
+// device, sequences are cut into segments: a first kernel forms what each
+// segment adds to the state, a second folds these along the sequence, and the
+// walks start at every segment.
+#include <algorithm>
+
+#include "gdn_device.h"
+#include "gdn_launch.h"
+
+namespace gdn {
+
+namespace {
+
+enum Role { kFwd, kDq, kDk, kDv, kStateFwd, kStateRev };
+
+// Tokens [bos, bos + len) of sequence n; offsets out of range give no token.
+__device__ __forceinline__ void lin_seq(const LinearArgs& a, int n, int& bos, int& len) {
+  if (a.cu_seqlens) {
+    const int lo = min(max(a.cu_seqlens[n], 0), a.tokens);
+    const int hi = min(max(a.cu_seqlens[n + 1], lo), a.tokens);
+    bos = lo;
+    len = hi - lo;
+  } else {
+    bos = n * a.T;
+    len = a.T;
+  }
+}
+
+// Segment `slot`: sequence n's segment s is slot base(n) + s, with base(n) =
+// n + bos / (segment's tokens) for packed sequences. False: no such segment.
+struct Segment {
+  int n, s, bos, len, first, count;      // first chunk and chunks of the segment
+  int cslot;                             // slot of the sequence's first chunk
+};
+template <int C>
+__device__ __forceinline__ bool lin_segment(const LinearArgs& a, int slot, Segment& x) {
+  const int m = a.seg * C;
+  int base;
+  if (a.cu_seqlens) {
+    int lo = 0, hi = a.N - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (mid + min(max(a.cu_seqlens[mid], 0), a.tokens) / m <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    x.n = lo;
+    lin_seq(a, lo, x.bos, x.len);
+    base = lo + x.bos / m;
+    x.cslot = lo + x.bos / C;
+  } else {
+    const int per = max(1, (a.T + m - 1) / m);
+    x.n = slot / per;
+    lin_seq(a, x.n, x.bos, x.len);
+    base = x.n * per;
+    x.cslot = x.n * ((a.T + C - 1) / C);
+  }
+  x.s = slot - base;
+  const int chunks = (x.len + C - 1) / C;
+  x.first = x.s * a.seg;
+  x.count = min(a.seg, chunks - x.first);
+  // a sequence without tokens has one segment, without chunks
+  return x.s >= 0 && (x.count > 0 || (x.s == 0 && x.len == 0));
+}
+// Slot of segment s of sequence n.
+template <int C>
+__device__ __forceinline__ int lin_slot(const LinearArgs& a, int n, int s, int bos) {
+  const int m = a.seg * C;
+  return a.cu_seqlens ? n + bos / m + s : n * max(1, (a.T + m - 1) / m) + s;
+}
+
+// ------------------------------------------------------------- operand access
+template <class T> struct Lin;
+template <> struct Lin<bf16> {
+  static constexpr int C = 64, PAD = 8;
+  using Frag = bf16x8;
+  static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) { return mfma(a, b, c); }
+  // 8 consecutive elements
+  static __device__ __forceinline__ Frag row(const bf16* p) { return *reinterpret_cast<const Frag*>(p); }
+  // rows r0 + 8 g + e (e = 0..7) of the lane's column c0 + step (r16 >> 2) + (r16 & 3)
+  static __device__ __forceinline__ Frag col(const bf16* m, int ld, int r0, int c0, int step, int r16, int g) {
+    typedef short s16x4v __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4v* lds_s16x4;
+    const bf16* p = m + (r0 + 8 * g + (r16 >> 2)) * ld + c0 + step * (r16 & 3);
+    const bf16x4 x = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(const_cast<bf16*>(p))));
+    const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(const_cast<bf16*>(p + 4 * ld))));
+    return Frag{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  }
+  // two accumulator tiles as one operand (paired rows), rounded; and what the rounding left
+  template <bool SPLIT>
+  static __device__ __forceinline__ void pack(const f32x4& t0, const f32x4& t1, Frag& hi, Frag& lo) {
+    if constexpr (SPLIT) pack_pair_split(t0, t1, hi, lo);
+    else hi = pack_pair(t0, t1);
+  }
+  // elements times b, as a sum of two operands (2^-17 of each)
+  template <bool SPLIT>
+  static __device__ __forceinline__ void scaled(const Frag& x, const f32x4& b0, const f32x4& b1, Frag& hi, Frag& lo) {
+    f32x4 t0, t1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t0[e] = from_bf16(x[e]) * b0[e];
+      t1[e] = from_bf16(x[e + 4]) * b1[e];
+    }
+    pack<SPLIT>(t0, t1, hi, lo);
+  }
+  static __device__ __forceinline__ void put4(bf16* p, const f32x4& x) {
+    *reinterpret_cast<bf16x4*>(p) = bf16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
+  }
+  static __device__ __forceinline__ f32x4 get4(const bf16* p) {
+    const bf16x4 v = *reinterpret_cast<const bf16x4*>(p);
+    return f32x4{from_bf16(v[0]), from_bf16(v[1]), from_bf16(v[2]), from_bf16(v[3])};
+  }
+};
+template <> struct Lin<float> {
+  static constexpr int C = 32, PAD = 4;
+  struct Frag { f32x4 a, b; };
+  static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = mfma_f32(a.a[e], b.a[e], c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = mfma_f32(a.b[e], b.b[e], c);
+    return c;
+  }
+  static __device__ __forceinline__ Frag row(const float* p) {
+    return Frag{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)};
+  }
+  static __device__ __forceinline__ Frag col(const float* m, int ld, int r0, int c0, int step, int r16, int g) {
+    const float* p = m + (r0 + 8 * g) * ld + c0 + step * (r16 >> 2) + (r16 & 3);
+    Frag f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f.a[e] = p[e * ld];
+      f.b[e] = p[(e + 4) * ld];
+    }
+    return f;
+  }
+  template <bool SPLIT>
+  static __device__ __forceinline__ void pack(const f32x4& t0, const f32x4& t1, Frag& hi, Frag&) {
+    hi = Frag{t0, t1};
+  }
+  template <bool SPLIT>
+  static __device__ __forceinline__ void scaled(const Frag& x, const f32x4& b0, const f32x4& b1, Frag& hi, Frag&) {
+    hi = Frag{x.a * b0, x.b * b1};
+  }
+  static __device__ __forceinline__ void put4(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
+  static __device__ __forceinline__ f32x4 get4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+};
+
+constexpr int kThreads = 256, kWaves = 4;
+
+// C rows of D elements on their way from memory to LDS, 16 bytes per thread
+// and pass; rows from n on are zeros.
+template <class T, int D>
+struct Rows {
+  static constexpr int C = Lin<T>::C, LD = D + Lin<T>::PAD;
+  static constexpr int VPR = D * (int)sizeof(T) / 16, RPP = kThreads / VPR, NP = C / RPP;
+  static_assert(RPP * NP == C, "whole passes");
+  static constexpr int BYTES = C * LD * (int)sizeof(T);
+  u32x4 r[NP];
+  __device__ __forceinline__ void load(const char* base, int stride, int n) {
+    const int row = threadIdx.x / VPR, at = (threadIdx.x % VPR) * 16;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int t = row + p * RPP;
+      r[p] = t < n ? *reinterpret_cast<const u32x4*>(base + (t * stride + at)) : u32x4{0, 0, 0, 0};
+    }
+  }
+  __device__ __forceinline__ void store(T* lds) const {
+    const int row = threadIdx.x / VPR, at = (threadIdx.x % VPR) * (16 / (int)sizeof(T));
+#pragma unroll
+    for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4*>(lds + (row + p * RPP) * LD + at) = r[p];
+  }
+};
+
+// An operand in memory: rows of one head.
+struct Operand {
+  const char* p;
+  int64_t stride;                        // bytes between tokens
+};
+
+// Inclusive prefix sum over a wave's lanes in 64 bits (as wave_incl_scan).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_rows64(double x) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 w = __builtin_bit_cast(i32x2, x);
+  i32x2 y;
+  y[0] = __builtin_amdgcn_update_dpp(0, w[0], CTRL, ROWS, 0xF, false);
+  y[1] = __builtin_amdgcn_update_dpp(0, w[1], CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, y);
+}
+__device__ __forceinline__ double wave_incl_scan64(double x) {
+  x += dpp_rows64<0x111, 0xF>(x);
+  x += dpp_rows64<0x112, 0xF>(x);
+  x += dpp_rows64<0x114, 0xF>(x);
+  x += dpp_rows64<0x118, 0xF>(x);
+  x += dpp_rows64<0x142, 0xA>(x);
+  x += dpp_rows64<0x143, 0xC>(x);
+  return x;
+}
+__device__ __forceinline__ double read_lane64(double x, int l) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 w = __builtin_bit_cast(i32x2, x);
+  return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_readlane(w[0], l), __builtin_amdgcn_readlane(w[1], l)});
+}
+
+// Gates of a chunk in LDS. gam is kept in units of log 2 as a float and its
+// remainder, so that differences of far-decayed tokens keep 2^-24: a log-decay of
+// -inf (a reset) counts -128, whose exponential is zero in FP32 and whose sum
+// over a chunk leaves its neighbours' digits in place.
+template <int C>
+struct Gates {
+  float hi[C], lo[C];                    // gam
+  float query[C];                        // factor of the state's part of an output
+  float key[C];                          // factor of a token's addition to the state
+  float decay;                           // of the state over the chunk
+};
+constexpr float kResetGate = -128.f;
+
+template <int C, bool REV>
+__device__ __forceinline__ void lin_gates(Gates<C>& s, float g, float in_scale) {
+  const int t = __lane_id();
+  double x = g < kResetGate ? kResetGate : g;
+  x = wave_incl_scan64(x * 1.4426950408889634074);
+  const double total = read_lane64(x, C - 1);
+  if (t < C) {
+    const float hi = static_cast<float>(x);
+    s.hi[t] = hi;
+    s.lo[t] = static_cast<float>(x - static_cast<double>(hi));
+    const float grow = fexp2(hi), left = fexp2(static_cast<float>(total - x));
+    s.query[t] = REV ? left : grow;
+    s.key[t] = REV ? in_scale * grow : left;
+    if (t == 0) s.decay = fexp2(static_cast<float>(total));
+  }
+}
+
+template <class T, int DC, int CW, int ROLE>
+struct WalkLds {
+  using L = Lin<T>;
+  static constexpr int C = L::C, DO = 64 * CW;
+  static constexpr bool STATE = ROLE == kStateFwd || ROLE == kStateRev;
+  static constexpr int PLD = C + L::PAD;
+  static constexpr int X = 0, Y = X + (STATE ? 0 : Rows<T, DC>::BYTES), Z = Y + Rows<T, DC>::BYTES;
+  static constexpr int K = Z + Rows<T, DO>::BYTES, P = K + (ROLE == kDk ? Rows<T, DO>::BYTES : 0);
+  static constexpr int G = P + (STATE ? 0 : C * PLD * (int)sizeof(T));
+  static constexpr int SUMS = G + 2 * (int)((sizeof(Gates<C>) + 15) / 16 * 16);
+  static constexpr int BYTES = SUMS + (ROLE == kDk ? 3 : ROLE == kDq ? 1 : 0) * kWaves * C * 4;
+};
+
+// One walk of a workgroup: segment `slot`, value head h, columns 64 CW slab ...
+// of the output. State and output columns are split over the waves (16 CW
+// each); the state never leaves the registers. Its tiles' rows are numbered so
+// that two of them are an operand over 32 consecutive rows, and a lane holds
+// 4 CW consecutive columns of an output row.
+template <class T, int DC, int CW, int ROLE>
+__device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, int slab, char* lds) {
+  using L = Lin<T>;
+  using W = WalkLds<T, DC, CW, ROLE>;
+  using Frag = typename L::Frag;
+  constexpr int C = L::C, DO = 64 * CW, ES = sizeof(T), NQ = C / 16, NT = NQ * NQ / kWaves;
+  constexpr bool REV = ROLE == kDk || ROLE == kDv || ROLE == kStateRev, STATE = W::STATE;
+  constexpr bool TURNED = ROLE == kDq || ROLE == kDk;      // the state is held transposed
+  constexpr bool SPLIT_IN = TURNED, SPLIT_ADD = ROLE != kDv;
+  constexpr bool B16 = sizeof(T) == 2;
+  constexpr int LDX = Rows<T, DC>::LD, LDZ = Rows<T, DO>::LD, STEP = 4 * CW;
+
+  Segment seg;
+  if (!lin_segment<C>(a, slot, seg)) return;
+  const int lane = __lane_id(), r16 = lane & 15, grp = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = h / (a.Hv / a.Hqk), col0 = slab * DO;
+  T* const sX = reinterpret_cast<T*>(lds + W::X);
+  T* const sY = reinterpret_cast<T*>(lds + W::Y);
+  T* const sZ = reinterpret_cast<T*>(lds + W::Z);
+  T* const sK = reinterpret_cast<T*>(lds + W::K);
+  T* const sP = reinterpret_cast<T*>(lds + W::P);
+  Gates<C>* const gates[2] = {reinterpret_cast<Gates<C>*>(lds + W::G),
+                              reinterpret_cast<Gates<C>*>(lds + W::G + (W::SUMS - W::G) / 2)};
+  float* const sums = reinterpret_cast<float*>(lds + W::SUMS);
+
+  const Operand q{static_cast<const char*>(a.q) + (int64_t)hk * a.Dk * ES, a.qs * ES};
+  const Operand k{static_cast<const char*>(a.k) + (int64_t)hk * a.Dk * ES, a.ks * ES};
+  const Operand v{static_cast<const char*>(a.v) + (int64_t)h * a.Dv * ES, a.vs * ES};
+  const Operand d{static_cast<const char*>(a.dout) + (int64_t)h * a.Dv * ES, (int64_t)a.Hv * a.Dv * ES};
+  const Operand x = ROLE == kFwd ? q : ROLE == kDq ? d : ROLE == kDk ? v : k;
+  const Operand y = ROLE == kFwd || ROLE == kStateFwd ? k : ROLE == kDq ? v : ROLE == kDk ? d : q;
+  Operand z = ROLE == kFwd || ROLE == kStateFwd ? v : ROLE == kDq ? k : ROLE == kDk ? q : d;
+  z.p += col0 * ES;
+  // the operand that q . dq or k . dk needs
+  const Operand w = ROLE == kDq ? q : k;
+
+  // ---- the state before the first chunk
+  const int64_t elems = (int64_t)a.Dk * a.Dv;
+  const int colw = col0 + 16 * CW * wave;
+  // element r of tile (mt, ct)
+  auto dc_of = [&](int mt) { return 32 * (mt >> 1) + 8 * grp + 4 * (mt & 1); };
+  auto col_of = [&](int ct) { return colw + STEP * (r16 >> 2) + 4 * ct + (r16 & 3); };
+  auto get_state = [&](const float* p, int mt, int ct) {
+    if constexpr (TURNED) return *reinterpret_cast<const f32x4*>(p + (int64_t)col_of(ct) * a.Dv + dc_of(mt));
+    f32x4 s;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] = p[(int64_t)(dc_of(mt) + r) * a.Dv + col_of(ct)];
+    return s;
+  };
+  auto put_state = [&](float* p, int mt, int ct, const f32x4& s) {
+    if constexpr (TURNED) *reinterpret_cast<f32x4*>(p + (int64_t)col_of(ct) * a.Dv + dc_of(mt)) = s;
+    else
+#pragma unroll
+      for (int r = 0; r < 4; ++r) p[(int64_t)(dc_of(mt) + r) * a.Dv + col_of(ct)] = s[r];
+  };
+  f32x4 S[DC / 16][CW];
+  const int64_t seq_head = (int64_t)seg.n * a.Hv + h, slot_head = (int64_t)slot * a.Hv + h;
+  const float* start = nullptr;
+  if constexpr (!STATE) {
+    start = REV ? (a.ws_dstate ? a.ws_dstate + slot_head * elems : a.dht ? a.dht + seq_head * elems : nullptr)
+                : (a.ws_state ? a.ws_state + slot_head * elems : a.h0 ? a.h0 + seq_head * elems : nullptr);
+  }
+#pragma unroll
+  for (int mt = 0; mt < DC / 16; ++mt)
+#pragma unroll
+    for (int ct = 0; ct < CW; ++ct) S[mt][ct] = start ? get_state(start, mt, ct) : zero4();
+
+  // ---- chunks on their way to LDS
+  Rows<T, STATE ? 64 : DC> rx;
+  Rows<T, DC> ry;
+  Rows<T, DO> rz, rk;
+  float gate = 0.f;
+  auto fetch = [&](int c) {
+    const int t0 = c * C, n = min(C, seg.len - t0);
+    const int64_t tok = seg.bos + t0;
+    if (lane < C) gate = lane < n ? a.g[(tok + lane) * a.gs + h] : 0.f;
+    if constexpr (!STATE) rx.load(x.p + tok * x.stride, (int)x.stride, n);
+    ry.load(y.p + tok * y.stride, (int)y.stride, n);
+    rz.load(z.p + tok * z.stride, (int)z.stride, n);
+    if constexpr (ROLE == kDk) rk.load(w.p + tok * w.stride, (int)w.stride, n);
+  };
+  auto chunk_of = [&](int i) { return seg.first + (REV ? seg.count - 1 - i : i); };
+  double log_decay = 0.0;                                 // STATE: over the segment
+  if (seg.count > 0) {
+    fetch(chunk_of(0));
+    if (wave == 0) lin_gates<C, REV>(*gates[0], gate, a.scale);
+  }
+  for (int i = 0; i < seg.count; ++i) {
+    const int c = chunk_of(i), t0 = c * C, n = min(C, seg.len - t0);
+    const int64_t tok = seg.bos + t0;
+    lds_barrier();                                        // the last chunk's reads are done
+    if constexpr (!STATE) rx.store(sX);
+    ry.store(sY);
+    rz.store(sZ);
+    if constexpr (ROLE == kDk) rk.store(sK);
+    if constexpr (STATE) {
+      double x0 = gate < kResetGate ? kResetGate : gate;
+      log_decay += read_lane64(wave_incl_scan64(x0), C - 1);
+    }
+    lds_barrier();
+    const Gates<C>& G = *gates[i & 1];
+    if (i + 1 < seg.count) fetch(chunk_of(i + 1));
+
+    f32x4 O[CW][NQ];
+    if constexpr (!STATE) {
+      // ---- P = (X Y^T) * weights, rows are queries
+      const int qt = wave % NQ, kt0 = wave / NQ * NT;
+      {
+        Frag xf[DC / 32];
+#pragma unroll
+        for (int kb = 0; kb < DC / 32; ++kb) xf[kb] = L::row(sX + (16 * qt + r16) * LDX + 32 * kb + 8 * grp);
+        const float qhi = G.hi[16 * qt + r16], qlo = G.lo[16 * qt + r16];
+        float csum = 0.f;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          const int kt = kt0 + u;
+          const bool need = REV ? kt >= qt : kt <= qt;
+          f32x4 p = zero4();
+          float rsum[4] = {0.f, 0.f, 0.f, 0.f};
+          if (need) {
+#pragma unroll
+            for (int kb = 0; kb < DC / 32; ++kb)
+              p = L::mma(L::row(sY + (16 * kt + r16) * LDX + 32 * kb + 8 * grp), xf[kb], p);
+            const f32x4 khi = *reinterpret_cast<const f32x4*>(&G.hi[16 * kt + 4 * grp]);
+            const f32x4 klo = *reinterpret_cast<const f32x4*>(&G.lo[16 * kt + 4 * grp]);
+            f32x4 wt;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int key = 16 * kt + 4 * grp + r, qry = 16 * qt + r16;
+              const float diff = (qhi - khi[r]) + (qlo - klo[r]);
+              const float e = fexp2(REV ? -diff : diff);
+              wt[r] = (REV ? key >= qry : key <= qry) ? (REV ? a.scale * e : e) : 0.f;
+              // not a product where the weight is not taken: it may have overflowed there
+              p[r] = (REV ? key >= qry : key <= qry) ? p[r] * wt[r] : 0.f;
+            }
+            if constexpr (ROLE == kDk) {
+              // the other product of the pair, q_i . k_j
+              f32x4 m = zero4();
+#pragma unroll
+              for (int kb = 0; kb < DO / 32; ++kb)
+                m = L::mma(L::row(sZ + (16 * kt + r16) * LDZ + 32 * kb + 8 * grp),
+                           L::row(sK + (16 * qt + r16) * LDZ + 32 * kb + 8 * grp), m);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float mm = p[r] * m[r];
+                csum += mm;
+                float t = mm;
+                t += dpp_f<0xB1>(t);
+                t += dpp_f<0x4E>(t);
+                t += dpp_f<0x141>(t);
+                t += dpp_f<0x140>(t);
+                rsum[r] = t;
+              }
+            }
+          }
+          // a block of 32 keys is read whole: its masked half holds zeros
+          if (REV ? (kt | 1) >= qt : (kt & ~1) <= qt) L::put4(sP + (16 * qt + r16) * W::PLD + 16 * kt + 4 * grp, p);
+          if constexpr (ROLE == kDk) {
+            if (r16 == 0)
+              *reinterpret_cast<f32x4*>(sums + wave * C + 16 * kt + 4 * grp) = f32x4{rsum[0], rsum[1], rsum[2], rsum[3]};
+          }
+        }
+        if constexpr (ROLE == kDk) {
+          csum += __shfl_xor(csum, 16, WAVE);
+          csum += __shfl_xor(csum, 32, WAVE);
+          if (grp == 0) sums[(kWaves + wave) * C + 16 * qt + r16] = csum;
+        }
+      }
+      // ---- the state's part: out = factor x S
+#pragma unroll
+      for (int ct = 0; ct < CW; ++ct)
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) O[ct][t] = zero4();
+#pragma unroll
+      for (int kb = 0; kb < DC / 32; ++kb) {
+        Frag hi[CW], lo[CW];
+#pragma unroll
+        for (int ct = 0; ct < CW; ++ct) L::template pack<SPLIT_IN>(S[2 * kb][ct], S[2 * kb + 1][ct], hi[ct], lo[ct]);
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          const Frag xf = L::row(sX + (16 * t + r16) * LDX + 32 * kb + 8 * grp);
+#pragma unroll
+          for (int ct = 0; ct < CW; ++ct) {
+            O[ct][t] = L::mma(hi[ct], xf, O[ct][t]);
+            if constexpr (SPLIT_IN && B16) O[ct][t] = L::mma(lo[ct], xf, O[ct][t]);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) {
+        const float f = G.query[16 * t + r16];
+#pragma unroll
+        for (int ct = 0; ct < CW; ++ct) O[ct][t] *= f;
+        if constexpr (TURNED) {
+          // the row's product with q (dq) or k (dk)
+          float dot = 0.f;
+          const int row = 16 * t + r16, at = 16 * CW * wave + STEP * grp;
+#pragma unroll
+          for (int ct = 0; ct < CW; ++ct) {
+            f32x4 m;
+            if constexpr (ROLE == kDk) m = L::get4(sK + row * LDZ + at + 4 * ct);
+            else m = row < n ? L::get4(reinterpret_cast<const T*>(w.p + (tok + row) * w.stride) + at + 4 * ct) : zero4();
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dot = fmaf(O[ct][t][r], m[r], dot);
+          }
+          dot += __shfl_xor(dot, 16, WAVE);
+          dot += __shfl_xor(dot, 32, WAVE);
+          if (grp == 0) sums[((ROLE == kDk ? 2 * kWaves : 0) + wave) * C + row] = dot;
+        }
+      }
+    }
+    // ---- Z as an operand over tokens
+    Frag zf[C / 32][CW];
+#pragma unroll
+    for (int tb = 0; tb < C / 32; ++tb)
+#pragma unroll
+      for (int ct = 0; ct < CW; ++ct)
+        zf[tb][ct] = L::col(sZ, LDZ, 32 * tb, 16 * CW * wave + 4 * ct, STEP, r16, grp);
+    if constexpr (!STATE) {
+      lds_barrier();                                      // P and the sums are there
+#pragma unroll
+      for (int t = 0; t < NQ; ++t)
+#pragma unroll
+        for (int tb = 0; tb < C / 32; ++tb) {
+          if (REV ? 2 * tb + 1 < t : 2 * tb > t) continue;
+          const Frag pf = L::row(sP + (16 * t + r16) * W::PLD + 32 * tb + 8 * grp);
+#pragma unroll
+          for (int ct = 0; ct < CW; ++ct) O[ct][t] = L::mma(zf[tb][ct], pf, O[ct][t]);
+        }
+      // ---- the outputs
+      const float out_scale = REV ? 1.f : a.scale;
+      char* dst;
+      int64_t stride;
+      bool parts = false;
+      if constexpr (ROLE == kFwd || ROLE == kDv) {
+        dst = static_cast<char*>(ROLE == kFwd ? a.o : a.dv) + (int64_t)h * a.Dv * ES;
+        stride = (int64_t)a.Hv * a.Dv * ES;
+      } else {
+        float* part = ROLE == kDq ? a.ws_dq : a.ws_dk;     // per value head, where heads share q and k
+        parts = part != nullptr;
+        dst = parts ? reinterpret_cast<char*>(part + (int64_t)h * a.Dk)
+                    : static_cast<char*>(ROLE == kDq ? a.dq : a.dk) + (int64_t)hk * a.Dk * ES;
+        stride = parts ? (int64_t)a.Hv * a.Dk * 4 : (int64_t)a.Hqk * a.Dk * ES;
+      }
+      const int at = 16 * CW * wave + STEP * grp + col0;
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) {
+        const int row = 16 * t + r16;
+        if (row >= n) continue;
+        char* p = dst + (tok + row) * stride;
+#pragma unroll
+        for (int ct = 0; ct < CW; ++ct) {
+          const f32x4 o = O[ct][t] * out_scale;
+          if (parts) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + at + 4 * ct) = o;
+          else L::put4(reinterpret_cast<T*>(p) + at + 4 * ct, o);
+        }
+      }
+      if constexpr (TURNED) {
+        if ((int)threadIdx.x < C) {
+          const int t = threadIdx.x;
+          float s = 0.f;
+#pragma unroll
+          for (int u = 0; u < kWaves; ++u) s += sums[((ROLE == kDk ? 2 * kWaves : 0) + u) * C + t];
+          if constexpr (ROLE == kDk) {
+            const int tile = t >> 4;
+            float rows = 0.f, cols = 0.f;
+#pragma unroll
+            for (int u = 0; u < NQ; ++u) rows += sums[(tile / NT * NQ + u) * C + t];
+#pragma unroll
+            for (int u = 0; u < kWaves / NQ; ++u) cols += sums[(kWaves + u * NQ + tile) * C + t];
+            s = (rows - cols) - s;
+          } else {
+            s *= out_scale;
+          }
+          (ROLE == kDk ? a.ws_kdk : a.ws_qdq)[((int64_t)(seg.cslot + c) * a.Hv + h) * C + t] = s;
+        }
+      }
+    }
+    // ---- the state after the chunk
+    const float decay = G.decay;
+#pragma unroll
+    for (int mt = 0; mt < DC / 16; ++mt)
+#pragma unroll
+      for (int ct = 0; ct < CW; ++ct) S[mt][ct] *= decay;
+#pragma unroll
+    for (int tb = 0; tb < C / 32; ++tb) {
+      const f32x4 b0 = *reinterpret_cast<const f32x4*>(&G.key[32 * tb + 8 * grp]);
+      const f32x4 b1 = *reinterpret_cast<const f32x4*>(&G.key[32 * tb + 8 * grp + 4]);
+      Frag hi[CW], lo[CW];
+#pragma unroll
+      for (int ct = 0; ct < CW; ++ct) L::template scaled<SPLIT_ADD>(zf[tb][ct], b0, b1, hi[ct], lo[ct]);
+#pragma unroll
+      for (int mt = 0; mt < DC / 16; ++mt) {
+        const Frag yf = L::col(sY, LDX, 32 * tb, 32 * (mt >> 1) + 4 * (mt & 1), 8, r16, grp);
+#pragma unroll
+        for (int ct = 0; ct < CW; ++ct) {
+          S[mt][ct] = L::mma(yf, hi[ct], S[mt][ct]);
+          if constexpr (SPLIT_ADD && B16) S[mt][ct] = L::mma(yf, lo[ct], S[mt][ct]);
+        }
+      }
+    }
+    if (wave == 0 && i + 1 < seg.count) lin_gates<C, REV>(*gates[(i + 1) & 1], gate, a.scale);
+  }
+
+  // ---- the state after the last chunk
+  float* end = nullptr;
+  if constexpr (STATE) end = (ROLE == kStateFwd ? a.ws_state : a.ws_dstate) + slot_head * elems;
+  else if constexpr (ROLE == kFwd) {
+    if (a.ht && (seg.first + seg.count) * C >= seg.len) end = a.ht + seq_head * elems;
+  } else if constexpr (ROLE == kDk) {
+    if (a.dh0 && seg.s == 0) end = a.dh0 + seq_head * elems;
+  }
+  if (end) {
+#pragma unroll
+    for (int mt = 0; mt < DC / 16; ++mt)
+#pragma unroll
+      for (int ct = 0; ct < CW; ++ct) put_state(end, mt, ct, S[mt][ct]);
+  }
+  if constexpr (STATE) {
+    if (threadIdx.x == 0 && slab == 0) a.ws_decay[slot_head] = static_cast<float>(exp(log_decay));
+  }
+  if constexpr (ROLE == kDq) {
+    // <dS, S> at the segment's end
+    const float* other = a.ws_dstate ? a.ws_dstate + slot_head * elems : a.dht ? a.dht + seq_head * elems : nullptr;
+    float dot = 0.f;
+    if (other) {
+#pragma unroll
+      for (int mt = 0; mt < DC / 16; ++mt)
+#pragma unroll
+        for (int ct = 0; ct < CW; ++ct) {
+          const f32x4 o = get_state(other, mt, ct);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) dot = fmaf(S[mt][ct][r], o[r], dot);
+        }
+    }
+    dot = wave_sum(dot);
+    lds_barrier();
+    if (lane == 0) sums[wave] = dot;
+    lds_barrier();
+    if (threadIdx.x == 0) a.ws_end[slot_head] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  }
+}
+
+template <class T, int DC, int CW, int ROLE>
+__global__ void __launch_bounds__(kThreads) lin_walk_kernel(LinearArgs a, int slabs) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int unit = blockIdx.x, per = a.Hv * slabs;
+  const int slot = unit / per, rest = unit - slot * per;
+  lin_walk<T, DC, CW, ROLE>(a, slot, rest / slabs, rest % slabs, lds);
+}
+
+// Folds what each segment adds into the state before it (REV: the gradient of
+// the state after it): buf[slot] is replaced along each sequence.
+template <int C, bool REV>
+__global__ void __launch_bounds__(kThreads) lin_fold_kernel(LinearArgs a, int blocks) {
+  const int unit = blockIdx.x / blocks, n = unit / a.Hv, h = unit - n * a.Hv;
+  const int64_t elems = (int64_t)a.Dk * a.Dv, at = ((int64_t)(blockIdx.x % blocks) * kThreads + threadIdx.x) * 4;
+  if (at >= elems) return;
+  int bos, len;
+  lin_seq(a, n, bos, len);
+  const int segs = max(1, (len + a.seg * C - 1) / (a.seg * C));
+  const float* init = REV ? a.dht : a.h0;
+  float* buf = REV ? a.ws_dstate : a.ws_state;
+  f32x4 S = init ? *reinterpret_cast<const f32x4*>(init + ((int64_t)n * a.Hv + h) * elems + at) : zero4();
+  const int64_t slot0 = lin_slot<C>(a, n, 0, bos);
+  for (int i = 0; i < segs; ++i) {
+    const int64_t sh = (slot0 + (REV ? segs - 1 - i : i)) * a.Hv + h;
+    f32x4* p = reinterpret_cast<f32x4*>(buf + sh * elems + at);
+    const f32x4 add = *p;
+    const float decay = a.ws_decay[sh];
+    *p = S;
+    S = S * decay + add;
+  }
+}
+
+// dg of a segment's tokens, a wave per (segment, head): suffix sums over each
+// chunk on top of <dS, S> at its end.
+template <int C>
+__global__ void __launch_bounds__(kThreads) lin_dg_kernel(LinearArgs a, int units) {
+  const int unit = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit >= units) return;
+  const int slot = unit / a.Hv, h = unit - slot * a.Hv, lane = __lane_id();
+  Segment seg;
+  if (!lin_segment<C>(a, slot, seg)) {
+    if (a.ws_dgsum && lane == 0) a.ws_dgsum[unit] = 0.0;
+    return;
+  }
+  double end = a.ws_end[unit], sum = 0.0;
+  for (int c = seg.first + seg.count - 1; c >= seg.first; --c) {
+    const int n = min(C, seg.len - c * C);
+    // lanes backwards: a prefix sum over lanes is a suffix sum over tokens
+    const int t = C - 1 - lane;
+    const int64_t at = ((int64_t)(seg.cslot + c) * a.Hv + h) * C + t;
+    double x = 0.0;
+    if (t >= 0 && t < n) x = static_cast<double>(a.ws_qdq[at]) + static_cast<double>(a.ws_kdk[at]);
+    x = wave_incl_scan64(x);
+    if (t >= 0 && t < n) {
+      const int64_t tok = seg.bos + c * C + t;
+      // where exp(g) is zero in FP32 nothing reaches over the token
+      const double y = a.g[tok * a.gs + h] < -88.f ? 0.0 : end + x;
+      if (a.ws_dgsum) sum += y;
+      else a.dg[tok * a.Hv + h] = static_cast<float>(y);
+    }
+    end += read_lane64(x, C - 1);
+  }
+  if (a.ws_dgsum) {
+    sum = wave_incl_scan64(sum);
+    if (lane == WAVE - 1) a.ws_dgsum[unit] = sum;
+  }
+}
+// A decay per head: dg is the sum over all tokens, segments in their order.
+__global__ void __launch_bounds__(WAVE) lin_dgsum_kernel(LinearArgs a) {
+  const int h = blockIdx.x, lane = __lane_id();
+  double s = 0.0;
+  for (int slot = lane; slot < a.slots; slot += WAVE) s += a.ws_dgsum[(int64_t)slot * a.Hv + h];
+  s = wave_incl_scan64(s);
+  if (lane == WAVE - 1) a.dg[h] = static_cast<float>(s);
+}
+
+// The sum over the value heads that share a query and key head.
+template <class T>
+__global__ void __launch_bounds__(kThreads) lin_group_kernel(LinearArgs a, int64_t vecs) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= vecs) return;
+  const int G = a.Hv / a.Hqk, per = a.Hqk * a.Dk / 4;
+  const int64_t tok = i / per;
+  // tokens of no sequence keep what they had
+  if (a.cu_seqlens && (tok < a.cu_seqlens[0] || tok >= a.cu_seqlens[a.N])) return;
+  const int at = (int)(i - tok * per) * 4, hk = at / a.Dk, d = at - hk * a.Dk;
+  const int64_t src = (tok * a.Hv + (int64_t)hk * G) * a.Dk + d;
+  f32x4 s = zero4(), t = zero4();
+  for (int u = 0; u < G; ++u) {
+    s += *reinterpret_cast<const f32x4*>(a.ws_dq + src + (int64_t)u * a.Dk);
+    t += *reinterpret_cast<const f32x4*>(a.ws_dk + src + (int64_t)u * a.Dk);
+  }
+  Lin<T>::put4(static_cast<T*>(a.dq) + tok * a.Hqk * a.Dk + at, s);
+  Lin<T>::put4(static_cast<T*>(a.dk) + tok * a.Hqk * a.Dk + at, t);
+}
+
+template <class T, int DC, int CW, int ROLE>
+hipError_t walk(const LinearArgs& a, int width, hipStream_t s) {
+  using W = WalkLds<T, DC, CW, ROLE>;
+  const int slabs = width / (64 * CW);
+  const int64_t blocks = (int64_t)a.slots * a.Hv * slabs;
+  if (blocks == 0) return hipSuccess;
+  if (W::BYTES > 65536) {
+    static thread_local int done = -1;
+    int dev = 0;
+    if (hipGetDevice(&dev) == hipSuccess && dev != done) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&lin_walk_kernel<T, DC, CW, ROLE>),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, W::BYTES);
+      if (e != hipSuccess) return e;
+      done = dev;
+    }
+  }
+  lin_walk_kernel<T, DC, CW, ROLE><<<dim3((unsigned)blocks), kThreads, W::BYTES, s>>>(a, slabs);
+  return hipGetLastError();
+}
+
+// A role over the sizes. dc: the contraction, width: the output's columns.
+template <class T, int ROLE>
+hipError_t walk_dims(const LinearArgs& a, int dc, int width, hipStream_t s) {
+  if (width == 64) {
+    if (dc == 64) return walk<T, 64, 1, ROLE>(a, width, s);
+    if (dc == 128) return walk<T, 128, 1, ROLE>(a, width, s);
+    if constexpr (ROLE == kDq || ROLE == kDk) return walk<T, 256, 1, ROLE>(a, width, s);
+  } else {
+    if (dc == 64) return walk<T, 64, 2, ROLE>(a, width, s);
+    if (dc == 128) return walk<T, 128, 2, ROLE>(a, width, s);
+    if constexpr (ROLE == kDq || ROLE == kDk) return walk<T, 256, 2, ROLE>(a, width, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <int C, bool REV>
+hipError_t fold(const LinearArgs& a, hipStream_t s) {
+  const int blocks = (a.Dk * a.Dv / 4 + kThreads - 1) / kThreads;
+  if (a.N == 0) return hipSuccess;
+  lin_fold_kernel<C, REV><<<dim3((unsigned)(a.N * a.Hv * blocks)), kThreads, 0, s>>>(a, blocks);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t linear_fwd(const LinearArgs& a, hipStream_t s) {
+  hipError_t e;
+  if (a.ws_state) {
+    if ((e = walk_dims<T, kStateFwd>(a, a.Dk, a.Dv, s)) != hipSuccess) return e;
+    if ((e = fold<Lin<T>::C, false>(a, s)) != hipSuccess) return e;
+  }
+  return walk_dims<T, kFwd>(a, a.Dk, a.Dv, s);
+}
+
+template <class T>
+hipError_t linear_bwd(const LinearArgs& a, hipStream_t s) {
+  constexpr int C = Lin<T>::C;
+  hipError_t e;
+  if (a.ws_state) {
+    if ((e = walk_dims<T, kStateFwd>(a, a.Dk, a.Dv, s)) != hipSuccess) return e;
+    if ((e = walk_dims<T, kStateRev>(a, a.Dk, a.Dv, s)) != hipSuccess) return e;
+    if ((e = fold<C, false>(a, s)) != hipSuccess) return e;
+    if ((e = fold<C, true>(a, s)) != hipSuccess) return e;
+  }
+  if ((e = walk_dims<T, kDq>(a, a.Dv, a.Dk, s)) != hipSuccess) return e;
+  if ((e = walk_dims<T, kDk>(a, a.Dv, a.Dk, s)) != hipSuccess) return e;
+  if ((e = walk_dims<T, kDv>(a, a.Dk, a.Dv, s)) != hipSuccess) return e;
+  const int units = a.slots * a.Hv;
+  if (units > 0) {
+    lin_dg_kernel<C><<<dim3((unsigned)((units + kWaves - 1) / kWaves)), kThreads, 0, s>>>(a, units);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.ws_dgsum) {
+    lin_dgsum_kernel<<<dim3((unsigned)a.Hv), WAVE, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.ws_dq && a.tokens > 0) {
+    const int64_t vecs = (int64_t)a.tokens * a.Hqk * a.Dk / 4;
+    lin_group_kernel<T><<<dim3((unsigned)((vecs + kThreads - 1) / kThreads)), kThreads, 0, s>>>(a, vecs);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dv, bool f32, bool bwd) {
+  const int C = f32 ? Lin<float>::C : Lin<bf16>::C;
+  const int slabs = Dv <= 128 ? 1 : 2;
+  const int64_t chunks = packed ? tokens / C + N : (int64_t)N * ((T + C - 1) / C);
+  const int64_t most = packed ? tokens / C + 1 : std::max(1, (T + C - 1) / C);      // of one sequence
+  const int64_t target = 2 * 256 / (bwd ? 2 : 1);
+  const int64_t want = std::max<int64_t>(1, (target + Hv * slabs - 1) / (Hv * slabs));
+  LinearPlan p{};
+  p.seg = (int)std::min<int64_t>(most, std::max<int64_t>(4, (chunks + want - 1) / want));
+  p.segmented = p.seg < most;
+  const int64_t m = (int64_t)p.seg * C;
+  p.slots = packed ? N + tokens / m : N * std::max<int64_t>(1, (T + m - 1) / m);
+  p.chunk_slots = packed ? N + tokens / C : chunks;
+  p.chunk = C;
+  return p;
+}
+
+hipError_t launch_linear_fwd(const LinearArgs& a, bool f32, hipStream_t s) {
+  return f32 ? linear_fwd<float>(a, s) : linear_fwd<bf16>(a, s);
+}
+hipError_t launch_linear_bwd(const LinearArgs& a, bool f32, hipStream_t s) {
+  return f32 ? linear_bwd<float>(a, s) : linear_bwd<bf16>(a, s);
+}
+
+}  // namespace gdn

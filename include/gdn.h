@@ -527,6 +527,70 @@ typedef struct {
 size_t gdn_beam_workspace_bytes(const gdn_beam_args* a);   /* 0 on error */
 gdn_status gdn_beam_select(const gdn_beam_args* a, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay per head: the recurrence above without the
+ * delta rule's read before the write. Per sequence and value head, from h0:
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T;   o_t = scale S_t^T q_t
+ * g is a log-decay per token and value head, or one per head for every token.
+ * -inf is a reset (the state before the token does not reach it); a gate above
+ * 0 lets the state grow and is computed as it stands, as long as exp of its sum
+ * over 64 tokens stays in range. ht is the state after the last token; a
+ * sequence without tokens hands h0 through. Value head h reads query/key head
+ * h / (Hv / Hqk). Tokens that no sequence holds (before cu_seqlens[0] or from
+ * cu_seqlens[N] on) are neither read nor written; offsets outside the
+ * buffer are cut to it.
+ * Arithmetic: products on the matrix cores with FP32 sums. States, decays and dg
+ * keep FP32 (bf16 factors of states are taken in two parts, 2^-17); the pairs'
+ * weights of a chunk, and states that only o is read from, are rounded to the input
+ * type. The results do not depend on what else runs, and repeat bit for bit.
+ * Sizes: Dk in {64, 128}, Dv in {64, 128, 256}, Hv % Hqk == 0, either io_dtype. */
+typedef struct {
+  int32_t B, T, Hqk, Hv, Dk, Dv;
+  int32_t num_seqs;            /* N (must equal B without cu_seqlens)         */
+  int32_t io_dtype;            /* gdn_dtype of q, k, v and o                  */
+  int32_t g_per_head;          /* 0: g [B, T, Hv]; 1: g [Hv]                  */
+  float scale;
+  int64_t q_stride, k_stride, v_stride; /* elements between consecutive tokens
+                                  of q, k, v (of all B * T, batch-major); 0:
+                                  contiguous. Rows start 16-byte aligned; at most
+                                  2^24 - 1 elements                           */
+  const void* q;               /* [B, T, Hqk, Dk]                             */
+  const void* k;               /* [B, T, Hqk, Dk]                             */
+  const void* v;               /* [B, T, Hv, Dv]                              */
+  const float* g;              /* aligned to an element only                  */
+  const float* h0;             /* [N, Hv, Dk, Dv], or NULL (= 0)              */
+  const int32_t* cu_seqlens;   /* [N + 1] offsets (device), or NULL           */
+  void* o;                     /* out [B, T, Hv, Dv]                          */
+  float* ht;                   /* out [N, Hv, Dk, Dv], or NULL                */
+  void* workspace;             /* gdn_linear_fwd_workspace_bytes() bytes: a state
+                                  per segment, where sequences are cut into
+                                  segments to fill the device; contents
+                                  undefined before and after, calls that may
+                                  overlap need one each                       */
+  size_t workspace_bytes;
+} gdn_linear_args;
+size_t gdn_linear_fwd_workspace_bytes(const gdn_linear_args* a);   /* 0 also on error */
+gdn_status gdn_linear_fwd(const gdn_linear_args* a, void* stream);
+
+/* Its gradients, from the inputs alone (nothing is saved by the forward). dg is
+ * the gradient of the log-decay: [B, T, Hv], or [Hv] (summed over all tokens) with
+ * g_per_head; 0 where exp(g) is below FP32's normal range (g < -88). */
+typedef struct {
+  gdn_linear_args fwd;         /* as the forward call; o, ht and the workspace
+                                  are not read                                */
+  const void* do_;             /* [B, T, Hv, Dv] io_dtype, contiguous         */
+  const float* dht;            /* [N, Hv, Dk, Dv] or NULL (= 0)               */
+  void* dq;                    /* out [B, T, Hqk, Dk] io_dtype (summed over the group) */
+  void* dk;                    /* out [B, T, Hqk, Dk]                         */
+  void* dv;                    /* out [B, T, Hv, Dv]                          */
+  float* dg;                   /* out, see above                              */
+  float* dh0;                  /* out [N, Hv, Dk, Dv], or NULL                */
+  void* workspace;             /* gdn_linear_bwd_workspace_bytes() bytes      */
+  size_t workspace_bytes;
+} gdn_linear_bwd_args;
+size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_bwd_args* a);   /* 0 on error */
+gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* a, void* stream);
+
 const char* gdn_last_error(void);
 int32_t gdn_abi_version(void);
 

@@ -1,0 +1,54 @@
+"""Oracle: linear attention with a decay per head (float64, torch on the CPU).
+
+TEST INFRASTRUCTURE ONLY: imported by tests/, never by the product path.
+
+Per sequence and value head, from S = h0 (or 0):
+
+    S   <- exp(g_t) * S + k_t v_t^T
+    o_t  = scale * S^T q_t
+    ht   = S after the last token
+
+g is [B, T, Hv], or [Hv] for one decay per head. Grouped heads: value head h
+reads query/key head h // (Hv // Hqk). Packed sequences (cu_seqlens) are
+independent. Token by token; the gradients are autograd's.
+"""
+import torch
+
+
+def _bounds(B, T, cu_seqlens):
+    if cu_seqlens is None:
+        return [(b * T, (b + 1) * T) for b in range(B)]
+    cu = [int(x) for x in cu_seqlens]
+    return list(zip(cu[:-1], cu[1:]))
+
+
+def linear_fwd(q, k, v, g, scale, h0=None, cu_seqlens=None):
+    """Returns (o [B, T, Hv, Dv], ht [N, Hv, Dk, Dv]); tokens of no sequence are zero."""
+    B, T, Hqk, Dk = q.shape
+    Hv, Dv = v.shape[2:]
+    G = Hv // Hqk
+    q, k = (x.reshape(B * T, Hqk, Dk).repeat_interleave(G, 1) for x in (q, k))
+    v = v.reshape(B * T, Hv, Dv)
+    a = torch.exp(g).expand(B * T, Hv) if g.dim() == 1 else torch.exp(g.reshape(B * T, Hv))
+    rows, ends = [torch.zeros(Hv, Dv, dtype=v.dtype)] * (B * T), []
+    for n, (lo, hi) in enumerate(_bounds(B, T, cu_seqlens)):
+        S = torch.zeros(Hv, Dk, Dv, dtype=v.dtype) if h0 is None else h0[n]
+        for t in range(lo, hi):
+            S = a[t][:, None, None] * S + k[t][:, :, None] * v[t][:, None, :]
+            rows[t] = scale * (S * q[t][:, :, None]).sum(1)
+        ends.append(S)
+    o = torch.stack(rows).reshape(B, T, Hv, Dv) if rows else torch.zeros(B, T, Hv, Dv, dtype=v.dtype)
+    ht = torch.stack(ends) if ends else torch.zeros(0, Hv, Dk, Dv, dtype=v.dtype)
+    return o, ht
+
+
+def linear_bwd(q, k, v, g, scale, do, dht=None, h0=None, cu_seqlens=None):
+    """Returns dict dq, dk, dv, dg, and dh0 when h0 is given."""
+    wrt = dict(q=q, k=k, v=v, g=g) | ({} if h0 is None else {'h0': h0})
+    wrt = {n: x.detach().clone().requires_grad_() for n, x in wrt.items()}
+    o, ht = linear_fwd(wrt['q'], wrt['k'], wrt['v'], wrt['g'], scale, wrt.get('h0'), cu_seqlens)
+    loss = (o * do).sum() + (0 if dht is None else (ht * dht).sum())
+    if not loss.requires_grad:
+        return {'d' + n: torch.zeros_like(x) for n, x in wrt.items()}
+    got = torch.autograd.grad(loss, list(wrt.values()), allow_unused=True)
+    return {'d' + n: torch.zeros_like(x) if y is None else y for (n, x), y in zip(wrt.items(), got)}

@@ -1,0 +1,145 @@
+"""Linear attention with a decay per head on the GPU against the float64 oracle.
+
+Bounds. U = 2^-8 is half a bf16 step. Each value of o is a sum of products; the
+kernel rounds the pair weights and the state it is read from to bf16 (once each) and
+the result once, so |error| <= U A + U |o|, with A the same sum over the
+absolute values of every factor (which the oracle computes from |q|, |k|, |v|,
+|h0|); FP32 sums and exponentials add less than 2^-14 A at these lengths (under
+900 sums of 2^-24 each, exponents to 2^-21). dq, dk, dv: the same form. States and
+dh0: factors in two bf16 parts, U^2 = 2^-16 A, and the FP32 part. With FP32 inputs
+there is the FP32 part alone. dg: its sums run over q . dq and k . dk of one segment
+(under 900 tokens here), each with 2^-15 of its absolute value at most (two split factors),
+so 2^-15 times the suffix sum of their absolute values, plus the same share of dg's own."""
+import math
+
+import pytest
+import torch
+
+import gateddeltanet_chunked_recurrence_amd as G
+from oracle.linear import linear_bwd, linear_fwd
+from parity_util import rel, say
+
+pytestmark = pytest.mark.gpu
+
+U, FP32 = 2.0 ** -8, 2.0 ** -14
+
+
+def make(io, B, T, lens, Hqk, Hv, Dk, Dv, gate='token', h0=True, view=False, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=gen)                      # noqa: E731
+    dt = torch.bfloat16 if io == 'bf16' else torch.float32
+    cu = None
+    if lens is not None:
+        cu = [0]
+        for n in lens:
+            cu.append(cu[-1] + n)
+        B, T = 1, max(T, cu[-1])
+    q, k, v, do = rnd(B, T, Hqk, Dk), rnd(B, T, Hqk, Dk), rnd(B, T, Hv, Dv), rnd(B, T, Hv, Dv)
+    if gate == 'head':
+        g = torch.log(0.8 + 0.199 * torch.rand(Hv, generator=gen))
+    else:
+        g = -torch.nn.functional.softplus(rnd(B, T, Hv) - 1.0)
+        if gate == 'reset':                                             # resets, and gates that keep all or nothing
+            pick = torch.rand(B, T, Hv, generator=gen)
+            g = torch.where(pick < 0.05, -math.inf, torch.where(pick < 0.1, -95.0, torch.where(pick < 0.2, 0.0, g)))
+    N = len(lens) if lens is not None else B
+    x = dict(q=q.to(dt), k=k.to(dt), v=v.to(dt), g=g, do=do.to(dt),
+             h0=rnd(N, Hv, Dk, Dv) if h0 else None, dht=rnd(N, Hv, Dk, Dv) if h0 else None)
+    d = {n: None if t is None else t.cuda() for n, t in x.items()}
+    if view:                                                            # one projection's output
+        y = torch.cat([x['q'].flatten(2), x['k'].flatten(2), x['v'].flatten(2), x['v'].flatten(2)[..., :64]], 2).cuda()
+        s = [Hqk * Dk, Hqk * Dk, Hv * Dv, 64]
+        a, b, c, _ = y.split(s, 2)
+        d['q'], d['k'], d['v'] = a.unflatten(2, (Hqk, Dk)), b.unflatten(2, (Hqk, Dk)), c.unflatten(2, (Hv, Dv))
+    d['cu'] = None if cu is None else torch.tensor(cu, dtype=torch.int32, device='cuda')
+    return {n: None if t is None else t.double() for n, t in x.items()}, d, cu
+
+
+def within(name, got, want, bound):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), name
+    off = (got - want).abs()
+    worst = float((off / bound.clamp_min(1e-300)).max()) if off.numel() else 0.0
+    say(f'  {name}: rel {rel(got, want):.2e}, {worst:.3f} of its bound')
+    assert (off <= bound).all(), (name, worst)
+
+
+def positive(x):
+    return {n: None if t is None else t if n == 'g' else t.abs() for n, t in x.items()}
+
+
+def check_fwd(x, d, cu, io, out=None):
+    scale = x['q'].shape[-1] ** -0.5
+    o, ht = G.gdn_linear_fwd(d['q'], d['k'], d['v'], d['g'], h0=d['h0'], cu_seqlens=d['cu'], out=out)
+    torch.cuda.synchronize()
+    p = positive(x)
+    wo, wh = linear_fwd(x['q'], x['k'], x['v'], x['g'], scale, x['h0'], cu)
+    ao, ah = linear_fwd(p['q'], p['k'], p['v'], x['g'], scale, p['h0'], cu)
+    b = io == 'bf16'
+    used = slice(None) if cu is None else slice(0, cu[-1])
+    within('o', o[:, used], wo[:, used], (ao * (U * b + FP32) + wo.abs() * U * b)[:, used])
+    within('ht', ht, wh, ah * (U * U * b + FP32))
+    return o
+
+
+def check_bwd(x, d, cu, io, out=None):
+    scale = x['q'].shape[-1] ** -0.5
+    got = G.gdn_linear_bwd(d['q'], d['k'], d['v'], d['g'], d['do'], dht=d['dht'], h0=d['h0'], cu_seqlens=d['cu'], out=out)
+    torch.cuda.synchronize()
+    p = positive(x)
+    want = linear_bwd(x['q'], x['k'], x['v'], x['g'], scale, x['do'], x['dht'], x['h0'], cu)
+    top = linear_bwd(p['q'], p['k'], p['v'], x['g'], scale, p['do'], p['dht'], p['h0'], cu)
+    b = io == 'bf16'
+    used = slice(None) if cu is None else slice(0, cu[-1])
+    for n in ('dq', 'dk', 'dv'):
+        within(n, got[n][:, used], want[n][:, used], (top[n] * (U * b + FP32) + want[n].abs() * U * b)[:, used])
+    if x['h0'] is not None:
+        within('dh0', got['dh0'], want['dh0'], top['dh0'] * (U * U * b + FP32))
+    Hv = x['v'].shape[2]
+    rep = Hv // x['q'].shape[2]
+    # a head's share of q . dq is at most its group's
+    dots = sum((p[a] * top['d' + a]).sum(-1) for a in ('q', 'k')).repeat_interleave(rep, 2)
+    sums = torch.zeros_like(dots).flatten(0, 1)
+    flat = dots.flatten(0, 1)
+    for lo, hi in zip(cu[:-1], cu[1:]) if cu else [(i * x['q'].shape[1], (i + 1) * x['q'].shape[1]) for i in range(x['q'].shape[0])]:
+        sums[lo:hi] = flat[lo:hi].flip(0).cumsum(0).flip(0)
+    sums = sums.reshape(dots.shape)
+    if x['g'].dim() == 1:
+        sums = sums.sum((0, 1))
+        within('dg', got['dg'], want['dg'], (sums + top['dg']) * 2.0 ** -15 + 1e-30)
+    else:
+        within('dg', got['dg'][:, used], want['dg'][:, used], ((sums + top['dg']) * 2.0 ** -15 + 1e-30)[:, used])
+    if x['q'].shape[1]:
+        assert rel(got['dg'] if x['g'].dim() == 1 else got['dg'][:, used], want['dg'] if x['g'].dim() == 1 else want['dg'][:, used]) < 2.0 ** -13
+    return got
+
+
+CASES = [
+    # io, B, T, lens, Hqk, Hv, Dk, Dv, gate, h0, view
+    ('bf16', 1, 1, None, 1, 1, 64, 64, 'token', True, False),
+    ('bf16', 2, 64, None, 1, 2, 64, 64, 'token', False, False),
+    ('bf16', 1, 65, None, 2, 2, 128, 128, 'token', True, False),
+    ('bf16', 2, 150, None, 1, 3, 128, 64, 'head', True, True),
+    ('bf16', 1, 203, None, 1, 1, 64, 256, 'token', True, False),
+    ('bf16', 1, 700, None, 1, 2, 128, 256, 'token', True, False),
+    ('bf16', 1, 515, None, 1, 1, 64, 128, 'reset', True, False),
+    ('bf16', 1, 0, [1, 63, 0, 130, 300, 2], 2, 4, 128, 128, 'token', True, True),
+    ('bf16', 1, 900, [257, 64, 500], 1, 1, 64, 64, 'head', False, False),
+    ('f32', 1, 1, None, 1, 1, 64, 64, 'token', True, False),
+    ('f32', 2, 33, None, 1, 2, 128, 64, 'token', False, True),
+    ('f32', 1, 300, None, 1, 2, 64, 128, 'reset', True, False),
+    ('f32', 1, 300, None, 1, 1, 128, 256, 'head', True, False),
+    ('f32', 1, 0, [0, 31, 130, 1, 200], 1, 3, 128, 128, 'token', True, False),
+]
+
+
+@pytest.mark.parametrize('case', CASES, ids=lambda c: '-'.join(map(str, c)).replace(' ', ''))
+def test_forward(case):
+    say(f'linear forward {case}')
+    check_fwd(*make(*case, seed=1), case[0])
+
+
+@pytest.mark.parametrize('case', CASES, ids=lambda c: '-'.join(map(str, c)).replace(' ', ''))
+def test_backward(case):
+    say(f'linear backward {case}')
+    check_bwd(*make(*case, seed=2), case[0])
