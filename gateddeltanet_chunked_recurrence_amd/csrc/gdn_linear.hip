@@ -107,22 +107,33 @@ template <> struct Lin<bf16> {
     const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(const_cast<bf16*>(p + 4 * ld))));
     return Frag{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
   }
-  // two accumulator tiles as one operand (paired rows), rounded; and what the rounding left
-  template <bool SPLIT>
-  static __device__ __forceinline__ void pack(const f32x4& t0, const f32x4& t1, Frag& hi, Frag& lo) {
-    if constexpr (SPLIT) pack_pair_split(t0, t1, hi, lo);
-    else hi = pack_pair(t0, t1);
+  // Two accumulator tiles (paired rows) as one operand: the sum of N bf16 parts,
+  // of which three hold all 24 bits of an FP32 value. A part is rounded by cutting
+  // the lower half of the pattern off, which the next part makes up for; the
+  // last is rounded to nearest.
+  template <int N>
+  static __device__ __forceinline__ void parts(f32x4 t0, f32x4 t1, Frag (&f)[N]) {
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      if (m + 1 == N) {
+        f[m] = pack_pair(t0, t1);
+      } else {
+        // whole vectors: __builtin_bit_cast of one element of a vector takes its first
+        const u32x4 a = __builtin_bit_cast(u32x4, t0), b = __builtin_bit_cast(u32x4, t1);
+        const u32x4 w{__builtin_amdgcn_perm(a[1], a[0], 0x07060302u), __builtin_amdgcn_perm(a[3], a[2], 0x07060302u),
+                      __builtin_amdgcn_perm(b[1], b[0], 0x07060302u), __builtin_amdgcn_perm(b[3], b[2], 0x07060302u)};
+        t0 -= __builtin_bit_cast(f32x4, a & 0xFFFF0000u);
+        t1 -= __builtin_bit_cast(f32x4, b & 0xFFFF0000u);
+        f[m] = __builtin_bit_cast(Frag, w);
+      }
+    }
   }
-  // elements times b, as a sum of two operands (2^-17 of each)
-  template <bool SPLIT>
-  static __device__ __forceinline__ void scaled(const Frag& x, const f32x4& b0, const f32x4& b1, Frag& hi, Frag& lo) {
-    f32x4 t0, t1;
+  static __device__ __forceinline__ void times(const Frag& x, const f32x4& b0, const f32x4& b1, f32x4& t0, f32x4& t1) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       t0[e] = from_bf16(x[e]) * b0[e];
       t1[e] = from_bf16(x[e + 4]) * b1[e];
     }
-    pack<SPLIT>(t0, t1, hi, lo);
   }
   static __device__ __forceinline__ void put4(bf16* p, const f32x4& x) {
     *reinterpret_cast<bf16x4*>(p) = bf16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
@@ -155,19 +166,27 @@ template <> struct Lin<float> {
     }
     return f;
   }
-  template <bool SPLIT>
-  static __device__ __forceinline__ void pack(const f32x4& t0, const f32x4& t1, Frag& hi, Frag&) {
-    hi = Frag{t0, t1};
+  template <int N>
+  static __device__ __forceinline__ void parts(const f32x4& t0, const f32x4& t1, Frag (&f)[N]) {
+    static_assert(N == 1, "FP32 operands are whole");
+    f[0] = Frag{t0, t1};
   }
-  template <bool SPLIT>
-  static __device__ __forceinline__ void scaled(const Frag& x, const f32x4& b0, const f32x4& b1, Frag& hi, Frag&) {
-    hi = Frag{x.a * b0, x.b * b1};
+  static __device__ __forceinline__ void times(const Frag& x, const f32x4& b0, const f32x4& b1, f32x4& t0, f32x4& t1) {
+    t0 = x.a * b0;
+    t1 = x.b * b1;
   }
   static __device__ __forceinline__ void put4(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
   static __device__ __forceinline__ f32x4 get4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 };
 
 constexpr int kThreads = 256, kWaves = 4;
+
+// n rows of `bytes` bytes, `stride` apart, as a buffer: loads beyond them give
+// zeros, stores beyond them do nothing. The chunk's rows span less than 2^32 bytes.
+__device__ __forceinline__ auto rows_rsrc(const void* base, uint32_t stride, int n, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)((uint32_t)(n - 1) * stride + (uint32_t)bytes),
+                                           0x00020000);
+}
 
 // C rows of D elements on their way from memory to LDS, 16 bytes per thread
 // and pass; rows from n on are zeros.
@@ -178,13 +197,12 @@ struct Rows {
   static_assert(RPP * NP == C, "whole passes");
   static constexpr int BYTES = C * LD * (int)sizeof(T);
   u32x4 r[NP];
-  __device__ __forceinline__ void load(const char* base, int stride, int n) {
-    const int row = threadIdx.x / VPR, at = (threadIdx.x % VPR) * 16;
+  __device__ __forceinline__ void load(const char* base, uint32_t stride, int n) {
+    const uint32_t row = threadIdx.x / VPR, at = (threadIdx.x % VPR) * 16;
+    const auto rsrc = rows_rsrc(base, stride, n, D * (int)sizeof(T));
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int t = row + p * RPP;
-      r[p] = t < n ? *reinterpret_cast<const u32x4*>(base + (t * stride + at)) : u32x4{0, 0, 0, 0};
-    }
+    for (int p = 0; p < NP; ++p)
+      r[p] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (row + p * RPP) * stride + at, 0, 0);
   }
   __device__ __forceinline__ void store(T* lds) const {
     const int row = threadIdx.x / VPR, at = (threadIdx.x % VPR) * (16 / (int)sizeof(T));
@@ -280,12 +298,16 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   constexpr int C = L::C, DO = 64 * CW, ES = sizeof(T), NQ = C / 16, NT = NQ * NQ / kWaves;
   constexpr bool REV = ROLE == kDk || ROLE == kDv || ROLE == kStateRev, STATE = W::STATE;
   constexpr bool TURNED = ROLE == kDq || ROLE == kDk;      // the state is held transposed
-  constexpr bool SPLIT_IN = TURNED, SPLIT_ADD = ROLE != kDv;
-  constexpr bool B16 = sizeof(T) == 2;
+  // bf16 parts of the state where an output reads it, and of what it takes up
+  constexpr int NIN = ES == 2 && TURNED ? 3 : 1, NADD = ES == 2 && ROLE != kDv ? 3 : 1;
   constexpr int LDX = Rows<T, DC>::LD, LDZ = Rows<T, DO>::LD, STEP = 4 * CW;
 
   Segment seg;
   if (!lin_segment<C>(a, slot, seg)) return;
+  // what the last segment adds is read by none
+  if constexpr (STATE) {
+    if (REV ? seg.s == 0 : (seg.first + seg.count) * C >= seg.len) return;
+  }
   const int lane = __lane_id(), r16 = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = h / (a.Hv / a.Hqk), col0 = slab * DO;
@@ -312,21 +334,24 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   // ---- the state before the first chunk
   const int64_t elems = (int64_t)a.Dk * a.Dv;
   const int colw = col0 + 16 * CW * wave;
-  // element r of tile (mt, ct)
-  auto dc_of = [&](int mt) { return 32 * (mt >> 1) + 8 * grp + 4 * (mt & 1); };
-  auto col_of = [&](int ct) { return colw + STEP * (r16 >> 2) + 4 * ct + (r16 & 3); };
-  auto get_state = [&](const float* p, int mt, int ct) {
-    if constexpr (TURNED) return *reinterpret_cast<const f32x4*>(p + (int64_t)col_of(ct) * a.Dv + dc_of(mt));
-    f32x4 s;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) s[r] = p[(int64_t)(dc_of(mt) + r) * a.Dv + col_of(ct)];
-    return s;
+  // Four rows of tile (mt, ct) of a state, by lane l: made anew at the walk's end
+  // (fresh_lane), or the offsets would stay in registers all the way there.
+  auto state_at = [&](int l, int mt, int ct) {
+    const int dc = 32 * (mt >> 1) + 8 * (l >> 4) + 4 * (mt & 1);
+    const int col = colw + STEP * ((l & 15) >> 2) + 4 * ct + (l & 3);
+    return TURNED ? col * a.Dv + dc : dc * a.Dv + col;
   };
-  auto put_state = [&](float* p, int mt, int ct, const f32x4& s) {
-    if constexpr (TURNED) *reinterpret_cast<f32x4*>(p + (int64_t)col_of(ct) * a.Dv + dc_of(mt)) = s;
+  auto get_state = [&](const float* p, int l, int mt, int ct) {
+    p += state_at(l, mt, ct);
+    if constexpr (TURNED) return *reinterpret_cast<const f32x4*>(p);
+    return f32x4{p[0], p[a.Dv], p[2 * a.Dv], p[3 * a.Dv]};
+  };
+  auto put_state = [&](float* p, int l, int mt, int ct, const f32x4& s) {
+    p += state_at(l, mt, ct);
+    if constexpr (TURNED) *reinterpret_cast<f32x4*>(p) = s;
     else
 #pragma unroll
-      for (int r = 0; r < 4; ++r) p[(int64_t)(dc_of(mt) + r) * a.Dv + col_of(ct)] = s[r];
+      for (int r = 0; r < 4; ++r) p[r * a.Dv] = s[r];
   };
   f32x4 S[DC / 16][CW];
   const int64_t seq_head = (int64_t)seg.n * a.Hv + h, slot_head = (int64_t)slot * a.Hv + h;
@@ -338,7 +363,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
   for (int mt = 0; mt < DC / 16; ++mt)
 #pragma unroll
-    for (int ct = 0; ct < CW; ++ct) S[mt][ct] = start ? get_state(start, mt, ct) : zero4();
+    for (int ct = 0; ct < CW; ++ct) S[mt][ct] = start ? get_state(start, lane, mt, ct) : zero4();
 
   // ---- chunks on their way to LDS
   Rows<T, STATE ? 64 : DC> rx;
@@ -349,10 +374,10 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     const int t0 = c * C, n = min(C, seg.len - t0);
     const int64_t tok = seg.bos + t0;
     if (lane < C) gate = lane < n ? a.g[(tok + lane) * a.gs + h] : 0.f;
-    if constexpr (!STATE) rx.load(x.p + tok * x.stride, (int)x.stride, n);
-    ry.load(y.p + tok * y.stride, (int)y.stride, n);
-    rz.load(z.p + tok * z.stride, (int)z.stride, n);
-    if constexpr (ROLE == kDk) rk.load(w.p + tok * w.stride, (int)w.stride, n);
+    if constexpr (!STATE) rx.load(x.p + tok * x.stride, (uint32_t)x.stride, n);
+    ry.load(y.p + tok * y.stride, (uint32_t)y.stride, n);
+    rz.load(z.p + tok * z.stride, (uint32_t)z.stride, n);
+    if constexpr (ROLE == kDk) rk.load(w.p + tok * w.stride, (uint32_t)w.stride, n);
   };
   auto chunk_of = [&](int i) { return seg.first + (REV ? seg.count - 1 - i : i); };
   double log_decay = 0.0;                                 // STATE: over the segment
@@ -441,6 +466,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
           if (grp == 0) sums[(kWaves + wave) * C + 16 * qt + r16] = csum;
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
       // ---- the state's part: out = factor x S
 #pragma unroll
       for (int ct = 0; ct < CW; ++ct)
@@ -448,17 +474,16 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
         for (int t = 0; t < NQ; ++t) O[ct][t] = zero4();
 #pragma unroll
       for (int kb = 0; kb < DC / 32; ++kb) {
-        Frag hi[CW], lo[CW];
+        Frag sf[CW][NIN];
 #pragma unroll
-        for (int ct = 0; ct < CW; ++ct) L::template pack<SPLIT_IN>(S[2 * kb][ct], S[2 * kb + 1][ct], hi[ct], lo[ct]);
+        for (int ct = 0; ct < CW; ++ct) L::template parts<NIN>(S[2 * kb][ct], S[2 * kb + 1][ct], sf[ct]);
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
           const Frag xf = L::row(sX + (16 * t + r16) * LDX + 32 * kb + 8 * grp);
 #pragma unroll
-          for (int ct = 0; ct < CW; ++ct) {
-            O[ct][t] = L::mma(hi[ct], xf, O[ct][t]);
-            if constexpr (SPLIT_IN && B16) O[ct][t] = L::mma(lo[ct], xf, O[ct][t]);
-          }
+          for (int ct = 0; ct < CW; ++ct)
+#pragma unroll
+            for (int m = 0; m < NIN; ++m) O[ct][t] = L::mma(sf[ct][m], xf, O[ct][t]);
         }
       }
 #pragma unroll
@@ -484,6 +509,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
         }
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
     // ---- Z as an operand over tokens
     Frag zf[C / 32][CW];
 #pragma unroll
@@ -517,17 +543,25 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
                     : static_cast<char*>(ROLE == kDq ? a.dq : a.dk) + (int64_t)hk * a.Dk * ES;
         stride = parts ? (int64_t)a.Hv * a.Dk * 4 : (int64_t)a.Hqk * a.Dk * ES;
       }
-      const int at = 16 * CW * wave + STEP * grp + col0;
+      const auto rsrc = rows_rsrc(dst + tok * stride, (uint32_t)stride, n, parts ? a.Dk * 4 : (TURNED ? a.Dk : a.Dv) * ES);
+      const uint32_t at = 16 * CW * wave + STEP * grp + col0;
 #pragma unroll
       for (int t = 0; t < NQ; ++t) {
-        const int row = 16 * t + r16;
-        if (row >= n) continue;
-        char* p = dst + (tok + row) * stride;
+        const uint32_t row = (16 * t + r16) * (uint32_t)stride;
+        if (ES == 4 || parts) {
 #pragma unroll
-        for (int ct = 0; ct < CW; ++ct) {
-          const f32x4 o = O[ct][t] * out_scale;
-          if (parts) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + at + 4 * ct) = o;
-          else L::put4(reinterpret_cast<T*>(p) + at + 4 * ct, o);
+          for (int ct = 0; ct < CW; ++ct)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[ct][t] * out_scale), rsrc,
+                                                   row + (at + 4 * ct) * 4, 0, 0);
+        } else if constexpr (CW == 2) {
+          __builtin_amdgcn_raw_buffer_store_b128(
+              __builtin_bit_cast(u32x4, pack_pair(O[0][t] * out_scale, O[1][t] * out_scale)), rsrc, row + at * 2, 0, 0);
+        } else {
+          typedef unsigned int u32x2v __attribute__((ext_vector_type(2)));
+          const f32x4 o = O[0][t] * out_scale;
+          __builtin_amdgcn_raw_buffer_store_b64(
+              __builtin_bit_cast(u32x2v, bf16x4{to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])}), rsrc,
+              row + at * 2, 0, 0);
         }
       }
       if constexpr (TURNED) {
@@ -551,6 +585,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
         }
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
     // ---- the state after the chunk
     const float decay = G.decay;
 #pragma unroll
@@ -561,23 +596,27 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     for (int tb = 0; tb < C / 32; ++tb) {
       const f32x4 b0 = *reinterpret_cast<const f32x4*>(&G.key[32 * tb + 8 * grp]);
       const f32x4 b1 = *reinterpret_cast<const f32x4*>(&G.key[32 * tb + 8 * grp + 4]);
-      Frag hi[CW], lo[CW];
+      Frag zs[CW][NADD];
 #pragma unroll
-      for (int ct = 0; ct < CW; ++ct) L::template scaled<SPLIT_ADD>(zf[tb][ct], b0, b1, hi[ct], lo[ct]);
+      for (int ct = 0; ct < CW; ++ct) {
+        f32x4 t0, t1;
+        L::times(zf[tb][ct], b0, b1, t0, t1);
+        L::template parts<NADD>(t0, t1, zs[ct]);
+      }
 #pragma unroll
       for (int mt = 0; mt < DC / 16; ++mt) {
         const Frag yf = L::col(sY, LDX, 32 * tb, 32 * (mt >> 1) + 4 * (mt & 1), 8, r16, grp);
 #pragma unroll
-        for (int ct = 0; ct < CW; ++ct) {
-          S[mt][ct] = L::mma(yf, hi[ct], S[mt][ct]);
-          if constexpr (SPLIT_ADD && B16) S[mt][ct] = L::mma(yf, lo[ct], S[mt][ct]);
-        }
+        for (int ct = 0; ct < CW; ++ct)
+#pragma unroll
+          for (int m = 0; m < NADD; ++m) S[mt][ct] = L::mma(yf, zs[ct][m], S[mt][ct]);
       }
     }
     if (wave == 0 && i + 1 < seg.count) lin_gates<C, REV>(*gates[(i + 1) & 1], gate, a.scale);
   }
 
   // ---- the state after the last chunk
+  const int last_lane = fresh_lane();
   float* end = nullptr;
   if constexpr (STATE) end = (ROLE == kStateFwd ? a.ws_state : a.ws_dstate) + slot_head * elems;
   else if constexpr (ROLE == kFwd) {
@@ -589,7 +628,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
     for (int mt = 0; mt < DC / 16; ++mt)
 #pragma unroll
-      for (int ct = 0; ct < CW; ++ct) put_state(end, mt, ct, S[mt][ct]);
+      for (int ct = 0; ct < CW; ++ct) put_state(end, last_lane, mt, ct, S[mt][ct]);
   }
   if constexpr (STATE) {
     if (threadIdx.x == 0 && slab == 0) a.ws_decay[slot_head] = static_cast<float>(exp(log_decay));
@@ -603,7 +642,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
       for (int mt = 0; mt < DC / 16; ++mt)
 #pragma unroll
         for (int ct = 0; ct < CW; ++ct) {
-          const f32x4 o = get_state(other, mt, ct);
+          const f32x4 o = get_state(other, last_lane, mt, ct);
 #pragma unroll
           for (int r = 0; r < 4; ++r) dot = fmaf(S[mt][ct][r], o[r], dot);
         }
@@ -617,7 +656,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 }
 
 template <class T, int DC, int CW, int ROLE>
-__global__ void __launch_bounds__(kThreads) lin_walk_kernel(LinearArgs a, int slabs) {
+__global__ void __launch_bounds__(kThreads, (DC <= 128 ? 2 : 1)) lin_walk_kernel(LinearArgs a, int slabs) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int unit = blockIdx.x, per = a.Hv * slabs;
   const int slot = unit / per, rest = unit - slot * per;
@@ -641,10 +680,9 @@ __global__ void __launch_bounds__(kThreads) lin_fold_kernel(LinearArgs a, int bl
   for (int i = 0; i < segs; ++i) {
     const int64_t sh = (slot0 + (REV ? segs - 1 - i : i)) * a.Hv + h;
     f32x4* p = reinterpret_cast<f32x4*>(buf + sh * elems + at);
-    const f32x4 add = *p;
-    const float decay = a.ws_decay[sh];
-    *p = S;
-    S = S * decay + add;
+    const f32x4 was = S;
+    if (i + 1 < segs) S = S * a.ws_decay[sh] + *p;
+    *p = was;
   }
 }
 
