@@ -91,20 +91,41 @@ __device__ __forceinline__ int lin_slot(const LinearArgs& a, int n, int s, int b
 }
 
 // ------------------------------------------------------------- operand access
+// Rows of D elements in LDS, without padding: the 16-byte pieces of a row are
+// exchanged by an XOR with bits of the row's number, so that the 16 rows of an
+// operand read along rows lie in 16 different places of the 64 banks, and so do the
+// 4 rows by 4 pieces that a lane group reads along columns.
+template <class T, int D>
+struct Tile {
+  static constexpr int ES = sizeof(T), RB = D * ES;
+  static_assert(RB % 128 == 0, "rows of whole half bank lines");
+  static __device__ __forceinline__ int flip(int row) {
+    return RB == 128 ? ((row & 2) << 1) | ((row >> 2) & 3) : ((row & 3) << 2) | ((row >> 2) & 3);
+  }
+  static __device__ __forceinline__ T* at(T* m, int row, int col) {
+    const int piece = col * ES / 16, rest = col * ES % 16;
+    return reinterpret_cast<T*>(reinterpret_cast<char*>(m) + row * RB + ((piece ^ flip(row)) * 16 + rest));
+  }
+};
+
 template <class T> struct Lin;
 template <> struct Lin<bf16> {
-  static constexpr int C = 64, PAD = 8;
+  static constexpr int C = 64;
   using Frag = bf16x8;
   static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) { return mfma(a, b, c); }
-  // 8 consecutive elements
-  static __device__ __forceinline__ Frag row(const bf16* p) { return *reinterpret_cast<const Frag*>(p); }
+  // elements col .. col + 7 of a row (col a multiple of 8)
+  template <int D>
+  static __device__ __forceinline__ Frag row(bf16* m, int r, int col) {
+    return *reinterpret_cast<const Frag*>(Tile<bf16, D>::at(m, r, col));
+  }
   // rows r0 + 8 g + e (e = 0..7) of the lane's column c0 + step (r16 >> 2) + (r16 & 3)
-  static __device__ __forceinline__ Frag col(const bf16* m, int ld, int r0, int c0, int step, int r16, int g) {
+  template <int D>
+  static __device__ __forceinline__ Frag col(bf16* m, int r0, int c0, int step, int r16, int g) {
     typedef short s16x4v __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4v* lds_s16x4;
-    const bf16* p = m + (r0 + 8 * g + (r16 >> 2)) * ld + c0 + step * (r16 & 3);
-    const bf16x4 x = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(const_cast<bf16*>(p))));
-    const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(const_cast<bf16*>(p + 4 * ld))));
+    const int r = r0 + 8 * g + (r16 >> 2), c = c0 + step * (r16 & 3);
+    const bf16x4 x = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(Tile<bf16, D>::at(m, r, c))));
+    const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(Tile<bf16, D>::at(m, r + 4, c))));
     return Frag{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
   }
   // Two accumulator tiles (paired rows) as one operand: the sum of N bf16 parts,
@@ -138,13 +159,18 @@ template <> struct Lin<bf16> {
   static __device__ __forceinline__ void put4(bf16* p, const f32x4& x) {
     *reinterpret_cast<bf16x4*>(p) = bf16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
   }
-  static __device__ __forceinline__ f32x4 get4(const bf16* p) {
-    const bf16x4 v = *reinterpret_cast<const bf16x4*>(p);
+  using Four = bf16x4;
+  static __device__ __forceinline__ f32x4 wide(const Four& v) {
     return f32x4{from_bf16(v[0]), from_bf16(v[1]), from_bf16(v[2]), from_bf16(v[3])};
+  }
+  static __device__ __forceinline__ f32x4 get4(const bf16* p) { return wide(*reinterpret_cast<const Four*>(p)); }
+  template <class R>
+  static __device__ __forceinline__ Four load4(const R& rsrc, uint32_t off) {
+    return __builtin_bit_cast(Four, __builtin_amdgcn_raw_buffer_load_b64(rsrc, off, 0, 0));
   }
 };
 template <> struct Lin<float> {
-  static constexpr int C = 32, PAD = 4;
+  static constexpr int C = 32;
   struct Frag { f32x4 a, b; };
   static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
 #pragma unroll
@@ -153,16 +179,19 @@ template <> struct Lin<float> {
     for (int e = 0; e < 4; ++e) c = mfma_f32(a.b[e], b.b[e], c);
     return c;
   }
-  static __device__ __forceinline__ Frag row(const float* p) {
-    return Frag{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)};
+  template <int D>
+  static __device__ __forceinline__ Frag row(float* m, int r, int col) {
+    return Frag{*reinterpret_cast<const f32x4*>(Tile<float, D>::at(m, r, col)),
+                *reinterpret_cast<const f32x4*>(Tile<float, D>::at(m, r, col + 4))};
   }
-  static __device__ __forceinline__ Frag col(const float* m, int ld, int r0, int c0, int step, int r16, int g) {
-    const float* p = m + (r0 + 8 * g) * ld + c0 + step * (r16 >> 2) + (r16 & 3);
+  template <int D>
+  static __device__ __forceinline__ Frag col(float* m, int r0, int c0, int step, int r16, int g) {
+    const int r = r0 + 8 * g, c = c0 + step * (r16 >> 2) + (r16 & 3);
     Frag f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      f.a[e] = p[e * ld];
-      f.b[e] = p[(e + 4) * ld];
+      f.a[e] = *Tile<float, D>::at(m, r + e, c);
+      f.b[e] = *Tile<float, D>::at(m, r + 4 + e, c);
     }
     return f;
   }
@@ -176,7 +205,13 @@ template <> struct Lin<float> {
     t1 = x.b * b1;
   }
   static __device__ __forceinline__ void put4(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
+  using Four = f32x4;
+  static __device__ __forceinline__ f32x4 wide(const Four& v) { return v; }
   static __device__ __forceinline__ f32x4 get4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+  template <class R>
+  static __device__ __forceinline__ Four load4(const R& rsrc, uint32_t off) {
+    return __builtin_bit_cast(Four, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
+  }
 };
 
 constexpr int kThreads = 256, kWaves = 4;
@@ -192,10 +227,10 @@ __device__ __forceinline__ auto rows_rsrc(const void* base, uint32_t stride, int
 // and pass; rows from n on are zeros.
 template <class T, int D>
 struct Rows {
-  static constexpr int C = Lin<T>::C, LD = D + Lin<T>::PAD;
+  static constexpr int C = Lin<T>::C;
   static constexpr int VPR = D * (int)sizeof(T) / 16, RPP = kThreads / VPR, NP = C / RPP;
   static_assert(RPP * NP == C, "whole passes");
-  static constexpr int BYTES = C * LD * (int)sizeof(T);
+  static constexpr int BYTES = C * D * (int)sizeof(T);
   u32x4 r[NP];
   __device__ __forceinline__ void load(const char* base, uint32_t stride, int n) {
     const uint32_t row = threadIdx.x / VPR, at = (threadIdx.x % VPR) * 16;
@@ -207,7 +242,7 @@ struct Rows {
   __device__ __forceinline__ void store(T* lds) const {
     const int row = threadIdx.x / VPR, at = (threadIdx.x % VPR) * (16 / (int)sizeof(T));
 #pragma unroll
-    for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4*>(lds + (row + p * RPP) * LD + at) = r[p];
+    for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4*>(Tile<T, D>::at(lds, row + p * RPP, at)) = r[p];
   }
 };
 
@@ -246,30 +281,102 @@ __device__ __forceinline__ double read_lane64(double x, int l) {
 // remainder, so that differences of far-decayed tokens keep 2^-24: a log-decay of
 // -inf (a reset) counts -128, whose exponential is zero in FP32 and whose sum
 // over a chunk leaves its neighbours' digits in place.
+// The registers hold the state in units of `unit`, which takes the decays
+// instead of every element; only where it leaves 2^+-40 are they multiplied.
 template <int C>
 struct Gates {
   float hi[C], lo[C];                    // gam
   float query[C];                        // factor of the state's part of an output
   float key[C];                          // factor of a token's addition to the state
-  float decay;                           // of the state over the chunk
+  float renorm;                          // of the state's elements before the additions
+  float unit;                            // after the chunk
 };
 constexpr float kResetGate = -128.f;
 
 template <int C, bool REV>
-__device__ __forceinline__ void lin_gates(Gates<C>& s, float g, float in_scale) {
+__device__ __forceinline__ void lin_gates(Gates<C>& s, float g, float scale, float& unit) {
   const int t = __lane_id();
   double x = g < kResetGate ? kResetGate : g;
   x = wave_incl_scan64(x * 1.4426950408889634074);
   const double total = read_lane64(x, C - 1);
+  const float decay = fexp2(static_cast<float>(total));
+  const float was = unit, next = unit * decay;
+  const bool keep = next > 0x1p-40f && next < 0x1p40f;
+  unit = keep ? next : 1.f;
   if (t < C) {
     const float hi = static_cast<float>(x);
     s.hi[t] = hi;
     s.lo[t] = static_cast<float>(x - static_cast<double>(hi));
-    const float grow = fexp2(hi), left = fexp2(static_cast<float>(total - x));
-    s.query[t] = REV ? left : grow;
-    s.key[t] = REV ? in_scale * grow : left;
-    if (t == 0) s.decay = fexp2(static_cast<float>(total));
+    const float grow = fexp2(hi), left = fexp2(static_cast<float>(total - x)), per = 1.0f / unit;
+    s.query[t] = was * (REV ? left : scale * grow);
+    s.key[t] = per * (REV ? scale * grow : left);
+    if (t == 0) {
+      s.renorm = keep ? 1.f : next;
+      s.unit = unit;
+    }
   }
+}
+
+// The additions to a state over a whole segment, without decays between its
+// chunks: `far` is the log of what the chunks between here and the segment's end
+// (REV: its start) leave.
+template <int C, bool REV>
+__device__ __forceinline__ void lin_gates_far(Gates<C>& s, float g, float scale, double& far) {
+  const int t = __lane_id();
+  double x = g < kResetGate ? kResetGate : g;
+  x = wave_incl_scan64(x * 1.4426950408889634074);
+  const double total = read_lane64(x, C - 1);
+  if (t < C) s.key[t] = REV ? scale * fexp2(static_cast<float>(far + x)) : fexp2(static_cast<float>(far + (total - x)));
+  far += total;
+}
+
+// How many of a segment's chunks, from its end (BACK) or its start, add anything to
+// a state there: beyond them every factor is below 2^-150, zero in FP32. And the log
+// (base 2) of the decay over the whole segment. Looks at the gates alone. All
+// threads; uses LDS at `lds` (2,048 chunks' totals) and leaves it to the next
+// barrier.
+template <int C, bool BACK>
+__device__ __forceinline__ int lin_reach(const LinearArgs& a, const Segment& seg, int h, char* lds, double& total) {
+  constexpr int MOST = 1024, AHEAD = 8;
+  double* const sum = reinterpret_cast<double*>(lds);     // [MOST] by distance
+  float* const top = reinterpret_cast<float*>(sum + MOST);
+  const int lane = __lane_id(), wave = threadIdx.x >> 6;
+  int count = 0;
+  double far = 0.0;
+  for (int i0 = 0; i0 < seg.count; i0 += MOST) {
+    const int most = min(MOST, seg.count - i0);
+    if (i0) lds_barrier();
+    for (int j0 = wave * AHEAD; j0 < most; j0 += kWaves * AHEAD) {
+      float g[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + j0 + u, c = seg.first + (BACK ? seg.count - 1 - i : i), t = c * C + lane;
+        g[u] = j0 + u < most && lane < C && t < seg.len ? a.g[(seg.bos + t) * a.gs + h] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        double x = g[u] < kResetGate ? kResetGate : g[u];
+        x = wave_incl_scan64(x * 1.4426950408889634074);
+        const double all = read_lane64(x, WAVE - 1);
+        const float m = wave_max(static_cast<float>(BACK ? all - x : x));
+        if (lane == 0 && j0 + u < most) {
+          sum[j0 + u] = all;
+          top[j0 + u] = m;
+        }
+      }
+    }
+    lds_barrier();
+    for (int j0 = 0; j0 < most; j0 += WAVE) {
+      const int j = j0 + lane;
+      const double x = j < most ? sum[j] : 0.0, y = wave_incl_scan64(x);
+      // not (below): a NaN counts as there
+      const uint64_t there = __ballot(j < most && !(far + (y - x) + top[min(j, MOST - 1)] < -150.0));
+      if (there) count = i0 + j0 + 64 - __builtin_clzll(there);
+      far += read_lane64(y, WAVE - 1);
+    }
+  }
+  total = far;
+  return count;
 }
 
 template <class T, int DC, int CW, int ROLE>
@@ -277,10 +384,9 @@ struct WalkLds {
   using L = Lin<T>;
   static constexpr int C = L::C, DO = 64 * CW;
   static constexpr bool STATE = ROLE == kStateFwd || ROLE == kStateRev;
-  static constexpr int PLD = C + L::PAD;
   static constexpr int X = 0, Y = X + (STATE ? 0 : Rows<T, DC>::BYTES), Z = Y + Rows<T, DC>::BYTES;
   static constexpr int K = Z + Rows<T, DO>::BYTES, P = K + (ROLE == kDk ? Rows<T, DO>::BYTES : 0);
-  static constexpr int G = P + (STATE ? 0 : C * PLD * (int)sizeof(T));
+  static constexpr int G = P + (STATE ? 0 : C * C * (int)sizeof(T));
   static constexpr int SUMS = G + 2 * (int)((sizeof(Gates<C>) + 15) / 16 * 16);
   static constexpr int BYTES = SUMS + (ROLE == kDk ? 3 : ROLE == kDq ? 1 : 0) * kWaves * C * 4;
 };
@@ -295,12 +401,13 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   using L = Lin<T>;
   using W = WalkLds<T, DC, CW, ROLE>;
   using Frag = typename L::Frag;
+  using Four = typename L::Four;
   constexpr int C = L::C, DO = 64 * CW, ES = sizeof(T), NQ = C / 16, NT = NQ * NQ / kWaves;
   constexpr bool REV = ROLE == kDk || ROLE == kDv || ROLE == kStateRev, STATE = W::STATE;
   constexpr bool TURNED = ROLE == kDq || ROLE == kDk;      // the state is held transposed
   // bf16 parts of the state where an output reads it, and of what it takes up
   constexpr int NIN = ES == 2 && TURNED ? 3 : 1, NADD = ES == 2 && ROLE != kDv ? 3 : 1;
-  constexpr int LDX = Rows<T, DC>::LD, LDZ = Rows<T, DO>::LD, STEP = 4 * CW;
+  constexpr int STEP = 4 * CW;
 
   Segment seg;
   if (!lin_segment<C>(a, slot, seg)) return;
@@ -365,6 +472,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
     for (int ct = 0; ct < CW; ++ct) S[mt][ct] = start ? get_state(start, lane, mt, ct) : zero4();
 
+  double far_total = 0.0;                                 // STATE: log of the segment's decay
   // ---- chunks on their way to LDS
   Rows<T, STATE ? 64 : DC> rx;
   Rows<T, DC> ry;
@@ -379,13 +487,22 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     rz.load(z.p + tok * z.stride, (uint32_t)z.stride, n);
     if constexpr (ROLE == kDk) rk.load(w.p + tok * w.stride, (uint32_t)w.stride, n);
   };
-  auto chunk_of = [&](int i) { return seg.first + (REV ? seg.count - 1 - i : i); };
-  double log_decay = 0.0;                                 // STATE: over the segment
-  if (seg.count > 0) {
+  // additions alone are gathered from the end where they weigh most
+  constexpr bool BACK = STATE ? !REV : REV;
+  auto chunk_of = [&](int i) { return seg.first + (BACK ? seg.count - 1 - i : i); };
+  float unit = 1.f;
+  double far = 0.0;                                       // STATE: log of the decay over the chunks done
+  auto put_gates = [&](int i) {
+    if constexpr (STATE) lin_gates_far<C, REV>(*gates[i & 1], gate, a.scale, far);
+    else lin_gates<C, REV>(*gates[i & 1], gate, a.scale, unit);
+  };
+  int count = seg.count;
+  if constexpr (STATE) count = lin_reach<C, BACK>(a, seg, h, lds + W::Y, far_total);
+  if (count > 0) {
     fetch(chunk_of(0));
-    if (wave == 0) lin_gates<C, REV>(*gates[0], gate, a.scale);
+    if (wave == 0) put_gates(0);
   }
-  for (int i = 0; i < seg.count; ++i) {
+  for (int i = 0; i < count; ++i) {
     const int c = chunk_of(i), t0 = c * C, n = min(C, seg.len - t0);
     const int64_t tok = seg.bos + t0;
     lds_barrier();                                        // the last chunk's reads are done
@@ -393,22 +510,32 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     ry.store(sY);
     rz.store(sZ);
     if constexpr (ROLE == kDk) rk.store(sK);
-    if constexpr (STATE) {
-      double x0 = gate < kResetGate ? kResetGate : gate;
-      log_decay += read_lane64(wave_incl_scan64(x0), C - 1);
-    }
     lds_barrier();
     const Gates<C>& G = *gates[i & 1];
-    if (i + 1 < seg.count) fetch(chunk_of(i + 1));
+    // the rows that q . dq needs, ahead of the next chunk's
+    Four rows[NQ][CW];
+    if constexpr (ROLE == kDq) {
+      const int l = fresh_lane();
+      const auto rsrc = rows_rsrc(w.p + tok * w.stride, (uint32_t)w.stride, n, a.Dk * ES);
+#pragma unroll
+      for (int t = 0; t < NQ; ++t)
+#pragma unroll
+        for (int ct = 0; ct < CW; ++ct)
+          rows[t][ct] = L::load4(rsrc, (16 * t + (l & 15)) * (uint32_t)w.stride +
+                                           (uint32_t)(16 * CW * wave + STEP * (l >> 4) + 4 * ct) * ES);
+    }
+    if (i + 1 < count) fetch(chunk_of(i + 1));
 
     f32x4 O[CW][NQ];
     if constexpr (!STATE) {
       // ---- P = (X Y^T) * weights, rows are queries
+      // lane numbers anew in each phase, or the phases' addresses stay in registers
       const int qt = wave % NQ, kt0 = wave / NQ * NT;
       {
+        const int l = fresh_lane(), r16 = l & 15, grp = l >> 4;
         Frag xf[DC / 32];
 #pragma unroll
-        for (int kb = 0; kb < DC / 32; ++kb) xf[kb] = L::row(sX + (16 * qt + r16) * LDX + 32 * kb + 8 * grp);
+        for (int kb = 0; kb < DC / 32; ++kb) xf[kb] = L::template row<DC>(sX, 16 * qt + r16, 32 * kb + 8 * grp);
         const float qhi = G.hi[16 * qt + r16], qlo = G.lo[16 * qt + r16];
         float csum = 0.f;
 #pragma unroll
@@ -420,26 +547,23 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
           if (need) {
 #pragma unroll
             for (int kb = 0; kb < DC / 32; ++kb)
-              p = L::mma(L::row(sY + (16 * kt + r16) * LDX + 32 * kb + 8 * grp), xf[kb], p);
+              p = L::mma(L::template row<DC>(sY, 16 * kt + r16, 32 * kb + 8 * grp), xf[kb], p);
             const f32x4 khi = *reinterpret_cast<const f32x4*>(&G.hi[16 * kt + 4 * grp]);
             const f32x4 klo = *reinterpret_cast<const f32x4*>(&G.lo[16 * kt + 4 * grp]);
-            f32x4 wt;
+            // the tile on the diagonal is cut; its other half may have overflowed
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int key = 16 * kt + 4 * grp + r, qry = 16 * qt + r16;
               const float diff = (qhi - khi[r]) + (qlo - klo[r]);
-              const float e = fexp2(REV ? -diff : diff);
-              wt[r] = (REV ? key >= qry : key <= qry) ? (REV ? a.scale * e : e) : 0.f;
-              // not a product where the weight is not taken: it may have overflowed there
-              p[r] = (REV ? key >= qry : key <= qry) ? p[r] * wt[r] : 0.f;
+              p[r] *= a.scale * fexp2(REV ? -diff : diff);
+              if (kt == qt && (REV ? 4 * grp + r < r16 : 4 * grp + r > r16)) p[r] = 0.f;
             }
             if constexpr (ROLE == kDk) {
               // the other product of the pair, q_i . k_j
               f32x4 m = zero4();
 #pragma unroll
               for (int kb = 0; kb < DO / 32; ++kb)
-                m = L::mma(L::row(sZ + (16 * kt + r16) * LDZ + 32 * kb + 8 * grp),
-                           L::row(sK + (16 * qt + r16) * LDZ + 32 * kb + 8 * grp), m);
+                m = L::mma(L::template row<DO>(sZ, 16 * kt + r16, 32 * kb + 8 * grp),
+                           L::template row<DO>(sK, 16 * qt + r16, 32 * kb + 8 * grp), m);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const float mm = p[r] * m[r];
@@ -454,7 +578,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
             }
           }
           // a block of 32 keys is read whole: its masked half holds zeros
-          if (REV ? (kt | 1) >= qt : (kt & ~1) <= qt) L::put4(sP + (16 * qt + r16) * W::PLD + 16 * kt + 4 * grp, p);
+          if (REV ? (kt | 1) >= qt : (kt & ~1) <= qt) L::put4(Tile<T, C>::at(sP, 16 * qt + r16, 16 * kt + 4 * grp), p);
           if constexpr (ROLE == kDk) {
             if (r16 == 0)
               *reinterpret_cast<f32x4*>(sums + wave * C + 16 * kt + 4 * grp) = f32x4{rsum[0], rsum[1], rsum[2], rsum[3]};
@@ -472,6 +596,8 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
       for (int ct = 0; ct < CW; ++ct)
 #pragma unroll
         for (int t = 0; t < NQ; ++t) O[ct][t] = zero4();
+      {
+      const int l = fresh_lane(), r16 = l & 15, grp = l >> 4;
 #pragma unroll
       for (int kb = 0; kb < DC / 32; ++kb) {
         Frag sf[CW][NIN];
@@ -479,7 +605,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
         for (int ct = 0; ct < CW; ++ct) L::template parts<NIN>(S[2 * kb][ct], S[2 * kb + 1][ct], sf[ct]);
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
-          const Frag xf = L::row(sX + (16 * t + r16) * LDX + 32 * kb + 8 * grp);
+          const Frag xf = L::template row<DC>(sX, 16 * t + r16, 32 * kb + 8 * grp);
 #pragma unroll
           for (int ct = 0; ct < CW; ++ct)
 #pragma unroll
@@ -498,8 +624,8 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
           for (int ct = 0; ct < CW; ++ct) {
             f32x4 m;
-            if constexpr (ROLE == kDk) m = L::get4(sK + row * LDZ + at + 4 * ct);
-            else m = row < n ? L::get4(reinterpret_cast<const T*>(w.p + (tok + row) * w.stride) + at + 4 * ct) : zero4();
+            if constexpr (ROLE == kDk) m = L::get4(Tile<T, DO>::at(sK, row, at + 4 * ct));
+            else m = L::wide(rows[t][ct]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) dot = fmaf(O[ct][t][r], m[r], dot);
           }
@@ -508,15 +634,17 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
           if (grp == 0) sums[((ROLE == kDk ? 2 * kWaves : 0) + wave) * C + row] = dot;
         }
       }
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     // ---- Z as an operand over tokens
     Frag zf[C / 32][CW];
+    const int l = fresh_lane(), r16 = l & 15, grp = l >> 4;
 #pragma unroll
     for (int tb = 0; tb < C / 32; ++tb)
 #pragma unroll
       for (int ct = 0; ct < CW; ++ct)
-        zf[tb][ct] = L::col(sZ, LDZ, 32 * tb, 16 * CW * wave + 4 * ct, STEP, r16, grp);
+        zf[tb][ct] = L::template col<DO>(sZ, 32 * tb, 16 * CW * wave + 4 * ct, STEP, r16, grp);
     if constexpr (!STATE) {
       lds_barrier();                                      // P and the sums are there
 #pragma unroll
@@ -524,12 +652,11 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
         for (int tb = 0; tb < C / 32; ++tb) {
           if (REV ? 2 * tb + 1 < t : 2 * tb > t) continue;
-          const Frag pf = L::row(sP + (16 * t + r16) * W::PLD + 32 * tb + 8 * grp);
+          const Frag pf = L::template row<C>(sP, 16 * t + r16, 32 * tb + 8 * grp);
 #pragma unroll
           for (int ct = 0; ct < CW; ++ct) O[ct][t] = L::mma(zf[tb][ct], pf, O[ct][t]);
         }
       // ---- the outputs
-      const float out_scale = REV ? 1.f : a.scale;
       char* dst;
       int64_t stride;
       bool parts = false;
@@ -551,14 +678,14 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
         if (ES == 4 || parts) {
 #pragma unroll
           for (int ct = 0; ct < CW; ++ct)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[ct][t] * out_scale), rsrc,
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[ct][t]), rsrc,
                                                    row + (at + 4 * ct) * 4, 0, 0);
         } else if constexpr (CW == 2) {
           __builtin_amdgcn_raw_buffer_store_b128(
-              __builtin_bit_cast(u32x4, pack_pair(O[0][t] * out_scale, O[1][t] * out_scale)), rsrc, row + at * 2, 0, 0);
+              __builtin_bit_cast(u32x4, pack_pair(O[0][t], O[1][t])), rsrc, row + at * 2, 0, 0);
         } else {
           typedef unsigned int u32x2v __attribute__((ext_vector_type(2)));
-          const f32x4 o = O[0][t] * out_scale;
+          const f32x4 o = O[0][t];
           __builtin_amdgcn_raw_buffer_store_b64(
               __builtin_bit_cast(u32x2v, bf16x4{to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])}), rsrc,
               row + at * 2, 0, 0);
@@ -578,8 +705,6 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
             for (int u = 0; u < kWaves / NQ; ++u) cols += sums[(kWaves + u * NQ + tile) * C + t];
             s = (rows - cols) - s;
-          } else {
-            s *= out_scale;
           }
           (ROLE == kDk ? a.ws_kdk : a.ws_qdq)[((int64_t)(seg.cslot + c) * a.Hv + h) * C + t] = s;
         }
@@ -587,13 +712,18 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     }
     __builtin_amdgcn_sched_barrier(0);
     // ---- the state after the chunk
-    const float decay = G.decay;
+    if constexpr (!STATE) {
+      const float renorm = G.renorm;
+      if (renorm != 1.f) {
 #pragma unroll
-    for (int mt = 0; mt < DC / 16; ++mt)
+        for (int mt = 0; mt < DC / 16; ++mt)
 #pragma unroll
-      for (int ct = 0; ct < CW; ++ct) S[mt][ct] *= decay;
+          for (int ct = 0; ct < CW; ++ct) S[mt][ct] *= renorm;
+      }
+    }
 #pragma unroll
     for (int tb = 0; tb < C / 32; ++tb) {
+      const int l = fresh_lane(), r16 = l & 15, grp = l >> 4;
       const f32x4 b0 = *reinterpret_cast<const f32x4*>(&G.key[32 * tb + 8 * grp]);
       const f32x4 b1 = *reinterpret_cast<const f32x4*>(&G.key[32 * tb + 8 * grp + 4]);
       Frag zs[CW][NADD];
@@ -605,18 +735,27 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
       }
 #pragma unroll
       for (int mt = 0; mt < DC / 16; ++mt) {
-        const Frag yf = L::col(sY, LDX, 32 * tb, 32 * (mt >> 1) + 4 * (mt & 1), 8, r16, grp);
+        const Frag yf = L::template col<DC>(sY, 32 * tb, 32 * (mt >> 1) + 4 * (mt & 1), 8, r16, grp);
 #pragma unroll
         for (int ct = 0; ct < CW; ++ct)
 #pragma unroll
           for (int m = 0; m < NADD; ++m) S[mt][ct] = L::mma(yf, zs[ct][m], S[mt][ct]);
       }
     }
-    if (wave == 0 && i + 1 < seg.count) lin_gates<C, REV>(*gates[(i + 1) & 1], gate, a.scale);
+    if (wave == 0 && i + 1 < count) put_gates(i + 1);
   }
 
   // ---- the state after the last chunk
   const int last_lane = fresh_lane();
+  if constexpr (!STATE) {
+    if (seg.count > 0) {
+      const float u = gates[(seg.count - 1) & 1]->unit;
+#pragma unroll
+      for (int mt = 0; mt < DC / 16; ++mt)
+#pragma unroll
+        for (int ct = 0; ct < CW; ++ct) S[mt][ct] *= u;
+    }
+  }
   float* end = nullptr;
   if constexpr (STATE) end = (ROLE == kStateFwd ? a.ws_state : a.ws_dstate) + slot_head * elems;
   else if constexpr (ROLE == kFwd) {
@@ -631,7 +770,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
       for (int ct = 0; ct < CW; ++ct) put_state(end, last_lane, mt, ct, S[mt][ct]);
   }
   if constexpr (STATE) {
-    if (threadIdx.x == 0 && slab == 0) a.ws_decay[slot_head] = static_cast<float>(exp(log_decay));
+    if (threadIdx.x == 0 && slab == 0) a.ws_decay[slot_head] = fexp2(static_cast<float>(far_total));
   }
   if constexpr (ROLE == kDq) {
     // <dS, S> at the segment's end
@@ -658,8 +797,10 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 template <class T, int DC, int CW, int ROLE>
 __global__ void __launch_bounds__(kThreads, (DC <= 128 ? 2 : 1)) lin_walk_kernel(LinearArgs a, int slabs) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int unit = blockIdx.x, per = a.Hv * slabs;
+  // consecutive units, which share q and k, on one XCD (workgroups go round the eight)
+  const int unit = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3), per = a.Hv * slabs;
   const int slot = unit / per, rest = unit - slot * per;
+  if (slot >= a.slots) return;
   lin_walk<T, DC, CW, ROLE>(a, slot, rest / slabs, rest % slabs, lds);
 }
 
@@ -677,12 +818,24 @@ __global__ void __launch_bounds__(kThreads) lin_fold_kernel(LinearArgs a, int bl
   float* buf = REV ? a.ws_dstate : a.ws_state;
   f32x4 S = init ? *reinterpret_cast<const f32x4*>(init + ((int64_t)n * a.Hv + h) * elems + at) : zero4();
   const int64_t slot0 = lin_slot<C>(a, n, 0, bos);
-  for (int i = 0; i < segs; ++i) {
-    const int64_t sh = (slot0 + (REV ? segs - 1 - i : i)) * a.Hv + h;
-    f32x4* p = reinterpret_cast<f32x4*>(buf + sh * elems + at);
-    const f32x4 was = S;
-    if (i + 1 < segs) S = S * a.ws_decay[sh] + *p;
-    *p = was;
+  auto sh = [&](int i) { return (slot0 + (REV ? segs - 1 - i : i)) * a.Hv + h; };
+  // the segments' additions load eight ahead of the chain
+  constexpr int AHEAD = 8;
+  f32x4 add[AHEAD];
+  float decay[AHEAD];
+  for (int i0 = 0; i0 < segs; i0 += AHEAD) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (i0 + u + 1 < segs) {
+        add[u] = *reinterpret_cast<const f32x4*>(buf + sh(i0 + u) * elems + at);
+        decay[u] = a.ws_decay[sh(i0 + u)];
+      }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (i0 + u < segs) {
+        *reinterpret_cast<f32x4*>(buf + sh(i0 + u) * elems + at) = S;
+        if (i0 + u + 1 < segs) S = S * decay[u] + add[u];
+      }
   }
 }
 
@@ -766,7 +919,7 @@ hipError_t walk(const LinearArgs& a, int width, hipStream_t s) {
       done = dev;
     }
   }
-  lin_walk_kernel<T, DC, CW, ROLE><<<dim3((unsigned)blocks), kThreads, W::BYTES, s>>>(a, slabs);
+  lin_walk_kernel<T, DC, CW, ROLE><<<dim3((unsigned)((blocks + 7) / 8 * 8)), kThreads, W::BYTES, s>>>(a, slabs);
   return hipGetLastError();
 }
 
