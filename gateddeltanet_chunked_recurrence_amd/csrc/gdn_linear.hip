@@ -423,8 +423,8 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   T* const sZ = reinterpret_cast<T*>(lds + W::Z);
   T* const sK = reinterpret_cast<T*>(lds + W::K);
   T* const sP = reinterpret_cast<T*>(lds + W::P);
-  Gates<C>* const gates[2] = {reinterpret_cast<Gates<C>*>(lds + W::G),
-                              reinterpret_cast<Gates<C>*>(lds + W::G + (W::SUMS - W::G) / 2)};
+  // not an array of two pointers: loads through one would be flat, and wait for every load in flight
+  auto gates = [&](int i) -> Gates<C>& { return *reinterpret_cast<Gates<C>*>(lds + W::G + (i & 1) * ((W::SUMS - W::G) / 2)); };
   float* const sums = reinterpret_cast<float*>(lds + W::SUMS);
 
   const Operand q{static_cast<const char*>(a.q) + (int64_t)hk * a.Dk * ES, a.qs * ES};
@@ -493,8 +493,8 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   float unit = 1.f;
   double far = 0.0;                                       // STATE: log of the decay over the chunks done
   auto put_gates = [&](int i) {
-    if constexpr (STATE) lin_gates_far<C, REV>(*gates[i & 1], gate, a.scale, far);
-    else lin_gates<C, REV>(*gates[i & 1], gate, a.scale, unit);
+    if constexpr (STATE) lin_gates_far<C, REV>(gates(i), gate, a.scale, far);
+    else lin_gates<C, REV>(gates(i), gate, a.scale, unit);
   };
   int count = seg.count;
   if constexpr (STATE) count = lin_reach<C, BACK>(a, seg, h, lds + W::Y, far_total);
@@ -511,7 +511,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     rz.store(sZ);
     if constexpr (ROLE == kDk) rk.store(sK);
     lds_barrier();
-    const Gates<C>& G = *gates[i & 1];
+    const Gates<C>& G = gates(i);
     // the rows that q . dq needs, ahead of the next chunk's
     Four rows[NQ][CW];
     if constexpr (ROLE == kDq) {
@@ -749,7 +749,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   const int last_lane = fresh_lane();
   if constexpr (!STATE) {
     if (seg.count > 0) {
-      const float u = gates[(seg.count - 1) & 1]->unit;
+      const float u = gates(seg.count - 1).unit;
 #pragma unroll
       for (int mt = 0; mt < DC / 16; ++mt)
 #pragma unroll
