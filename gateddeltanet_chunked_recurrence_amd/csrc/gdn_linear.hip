@@ -25,6 +25,12 @@
 // segment adds to the state, a second folds these along the sequence, and the
 // walks start at every segment.
 #include <algorithm>
+#ifndef LINC
+#define LINC 32
+#endif
+#ifndef LINOCC
+#define LINOCC 3
+#endif
 
 #include "gdn_device.h"
 #include "gdn_launch.h"
@@ -98,40 +104,47 @@ __device__ __forceinline__ int lin_slot(const LinearArgs& a, int n, int s, int b
 template <class T, int D>
 struct Tile {
   static constexpr int ES = sizeof(T), RB = D * ES;
-  static_assert(RB % 128 == 0, "rows of whole half bank lines");
+  static_assert(RB == 64 || RB % 128 == 0, "rows of whole parts of a bank line");
   static __device__ __forceinline__ int flip(int row) {
-    return RB == 128 ? ((row & 2) << 1) | ((row >> 2) & 3) : ((row & 3) << 2) | ((row >> 2) & 3);
+    return RB == 64 ? (row >> 2) & 3 : RB == 128 ? ((row & 2) << 1) | ((row >> 2) & 3) : ((row & 3) << 2) | ((row >> 2) & 3);
   }
-  static __device__ __forceinline__ T* at(T* m, int row, int col) {
-    const int piece = col * ES / 16, rest = col * ES % 16;
-    return reinterpret_cast<T*>(reinterpret_cast<char*>(m) + row * RB + ((piece ^ flip(row)) * 16 + rest));
+  // Byte offset of (row, col). Offsets of a lane's elements differ by constants
+  // that are XORed in (columns) or added (rows, by 16 or more), as the flip depends on
+  // row & 15 alone: so a base per lane serves a whole operand.
+  static __device__ __forceinline__ int at(int row, int col) {
+    return row * RB + (((col * ES / 16) ^ flip(row)) * 16 + col * ES % 16);
   }
 };
 
 template <class T> struct Lin;
 template <> struct Lin<bf16> {
-  static constexpr int C = 64;
+  static constexpr int C = LINC;
   using Frag = bf16x8;
   static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) { return mfma(a, b, c); }
-  // elements col .. col + 7 of a row (col a multiple of 8)
+  // elements 32 kb + 8 g .. + 7 of row 16 t + r16; `base`: Tile::at(r16, 8 g)
   template <int D>
-  static __device__ __forceinline__ Frag row(bf16* m, int r, int col) {
-    return *reinterpret_cast<const Frag*>(Tile<bf16, D>::at(m, r, col));
+  static __device__ __forceinline__ Frag row(const char* m, int base, int t, int kb) {
+    return *reinterpret_cast<const Frag*>(m + 16 * t * Tile<bf16, D>::RB + (base ^ (64 * kb)));
   }
-  // rows r0 + 8 g + e (e = 0..7) of the lane's column c0 + step (r16 >> 2) + (r16 & 3)
+  // rows 32 tb + 8 g + e (e = 0..7) of the lane's column c + step (r16 >> 2) + (r16 & 3), c a
+  // multiple of 4; `base`: colbase(step, r16, g)
   template <int D>
-  static __device__ __forceinline__ Frag col(bf16* m, int r0, int c0, int step, int r16, int g) {
+  static __device__ __forceinline__ int colbase(int step, int r16, int g) {
+    return Tile<bf16, D>::at(8 * g + (r16 >> 2), step * (r16 & 3));
+  }
+  template <int D>
+  static __device__ __forceinline__ Frag col(const char* m, int base, int tb, int c) {
     typedef short s16x4v __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4v* lds_s16x4;
-    const int r = r0 + 8 * g + (r16 >> 2), c = c0 + step * (r16 & 3);
-    const bf16x4 x = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(Tile<bf16, D>::at(m, r, c))));
-    const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(Tile<bf16, D>::at(m, r + 4, c))));
+    constexpr int RB = Tile<bf16, D>::RB;
+    const char* p = m + 32 * tb * RB + c % 8 * 2;
+    const int b0 = base ^ (c / 8 * 16), b1 = b0 ^ 16;      // 4 rows on: the flip's lowest bit
+    const bf16x4 x = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(const_cast<char*>(p + b0))));
+    const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(const_cast<char*>(p + 4 * RB + b1))));
     return Frag{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
   }
   // Two accumulator tiles (paired rows) as one operand: the sum of N bf16 parts,
-  // of which three hold all 24 bits of an FP32 value. A part is rounded by cutting
-  // the lower half of the pattern off, which the next part makes up for; the
-  // last is rounded to nearest.
+  // of which three hold all 24 bits of an FP32 value, each rounded to nearest.
   template <int N>
   static __device__ __forceinline__ void parts(f32x4 t0, f32x4 t1, Frag (&f)[N]) {
 #pragma unroll
@@ -139,13 +152,23 @@ template <> struct Lin<bf16> {
       if (m + 1 == N) {
         f[m] = pack_pair(t0, t1);
       } else {
-        // whole vectors: __builtin_bit_cast of one element of a vector takes its first
-        const u32x4 a = __builtin_bit_cast(u32x4, t0), b = __builtin_bit_cast(u32x4, t1);
-        const u32x4 w{__builtin_amdgcn_perm(a[1], a[0], 0x07060302u), __builtin_amdgcn_perm(a[3], a[2], 0x07060302u),
-                      __builtin_amdgcn_perm(b[1], b[0], 0x07060302u), __builtin_amdgcn_perm(b[3], b[2], 0x07060302u)};
-        t0 -= __builtin_bit_cast(f32x4, a & 0xFFFF0000u);
-        t1 -= __builtin_bit_cast(f32x4, b & 0xFFFF0000u);
-        f[m] = __builtin_bit_cast(Frag, w);
+        // What a part leaves is a sum of products with -1 and 0: v_dot2_f32_bf16
+        // takes the part as it lies in its register, exactly.
+        f[m] = pack_pair(t0, t1);
+        typedef bf16 bf16x2v __attribute__((ext_vector_type(2)));
+        // (-1, 0) and (0, -1) by way of registers: as an inline constant of the
+        // instruction, -1.0 is not the pair that the compiler takes it for
+        uint32_t w1 = 0xBF80u, w2 = 0xBF800000u;
+        asm("" : "+s"(w1), "+s"(w2));
+        const bf16x2v one = __builtin_bit_cast(bf16x2v, w1), two = __builtin_bit_cast(bf16x2v, w2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bf16x2v a{f[m][2 * e], f[m][2 * e + 1]}, b{f[m][2 * e + 4], f[m][2 * e + 5]};
+          t0[2 * e] = __builtin_amdgcn_fdot2_f32_bf16(a, one, t0[2 * e], false);
+          t0[2 * e + 1] = __builtin_amdgcn_fdot2_f32_bf16(a, two, t0[2 * e + 1], false);
+          t1[2 * e] = __builtin_amdgcn_fdot2_f32_bf16(b, one, t1[2 * e], false);
+          t1[2 * e + 1] = __builtin_amdgcn_fdot2_f32_bf16(b, two, t1[2 * e + 1], false);
+        }
       }
     }
   }
@@ -180,18 +203,25 @@ template <> struct Lin<float> {
     return c;
   }
   template <int D>
-  static __device__ __forceinline__ Frag row(float* m, int r, int col) {
-    return Frag{*reinterpret_cast<const f32x4*>(Tile<float, D>::at(m, r, col)),
-                *reinterpret_cast<const f32x4*>(Tile<float, D>::at(m, r, col + 4))};
+  static __device__ __forceinline__ Frag row(const char* m, int base, int t, int kb) {
+    const char* p = m + 16 * t * Tile<float, D>::RB;
+    const int b = base ^ (128 * kb);
+    return Frag{*reinterpret_cast<const f32x4*>(p + b), *reinterpret_cast<const f32x4*>(p + (b ^ 16))};
   }
   template <int D>
-  static __device__ __forceinline__ Frag col(float* m, int r0, int c0, int step, int r16, int g) {
-    const int r = r0 + 8 * g, c = c0 + step * (r16 >> 2) + (r16 & 3);
+  static __device__ __forceinline__ int colbase(int step, int r16, int g) {
+    return Tile<float, D>::at(8 * g, step * (r16 >> 2) + (r16 & 3));
+  }
+  template <int D>
+  static __device__ __forceinline__ Frag col(const char* m, int base, int tb, int c) {
+    constexpr int RB = Tile<float, D>::RB;
+    static_assert(RB >= 256, "the flip's four bits");
     Frag f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f.a[e] = *Tile<float, D>::at(m, r + e, c);
-      f.b[e] = *Tile<float, D>::at(m, r + 4 + e, c);
+    for (int e = 0; e < 8; ++e) {
+      const float x = *reinterpret_cast<const float*>(m + (32 * tb + e) * RB + (base ^ (c * 4) ^ (((e & 3) << 2 | e >> 2) << 4)));
+      if (e < 4) f.a[e] = x;
+      else f.b[e - 4] = x;
     }
     return f;
   }
@@ -239,10 +269,12 @@ struct Rows {
     for (int p = 0; p < NP; ++p)
       r[p] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (row + p * RPP) * stride + at, 0, 0);
   }
-  __device__ __forceinline__ void store(T* lds) const {
+  __device__ __forceinline__ void store(char* lds) const {
     const int row = threadIdx.x / VPR, at = (threadIdx.x % VPR) * (16 / (int)sizeof(T));
 #pragma unroll
-    for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4*>(Tile<T, D>::at(lds, row + p * RPP, at)) = r[p];
+    for (int p = 0; p < NP; ++p)
+      *reinterpret_cast<u32x4*>(lds + (RPP % 16 == 0 ? p * RPP * Tile<T, D>::RB + Tile<T, D>::at(row, at)
+                                                     : Tile<T, D>::at(row + p * RPP, at))) = r[p];
   }
 };
 
@@ -294,15 +326,15 @@ struct Gates {
 constexpr float kResetGate = -128.f;
 
 template <int C, bool REV>
-__device__ __forceinline__ void lin_gates(Gates<C>& s, float g, float scale, float& unit) {
+__device__ __forceinline__ void lin_gates(Gates<C>& s, float g, float scale, float was) {
   const int t = __lane_id();
   double x = g < kResetGate ? kResetGate : g;
   x = wave_incl_scan64(x * 1.4426950408889634074);
   const double total = read_lane64(x, C - 1);
   const float decay = fexp2(static_cast<float>(total));
-  const float was = unit, next = unit * decay;
+  const float next = was * decay;
   const bool keep = next > 0x1p-40f && next < 0x1p40f;
-  unit = keep ? next : 1.f;
+  const float unit = keep ? next : 1.f;
   if (t < C) {
     const float hi = static_cast<float>(x);
     s.hi[t] = hi;
@@ -418,14 +450,19 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   const int lane = __lane_id(), r16 = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = h / (a.Hv / a.Hqk), col0 = slab * DO;
-  T* const sX = reinterpret_cast<T*>(lds + W::X);
-  T* const sY = reinterpret_cast<T*>(lds + W::Y);
-  T* const sZ = reinterpret_cast<T*>(lds + W::Z);
-  T* const sK = reinterpret_cast<T*>(lds + W::K);
-  T* const sP = reinterpret_cast<T*>(lds + W::P);
+  char* const sX = lds + W::X;
+  char* const sY = lds + W::Y;
+  char* const sZ = lds + W::Z;
+  char* const sK = lds + W::K;
+  char* const sP = lds + W::P;
   // not an array of two pointers: loads through one would be flat, and wait for every load in flight
   auto gates = [&](int i) -> Gates<C>& { return *reinterpret_cast<Gates<C>*>(lds + W::G + (i & 1) * ((W::SUMS - W::G) / 2)); };
   float* const sums = reinterpret_cast<float*>(lds + W::SUMS);
+  // this lane's places in the tiles
+  const int xrow = Tile<T, DC>::at(r16, 8 * grp), ycol = L::template colbase<DC>(8, r16, grp);
+  const int zrow = Tile<T, DO>::at(r16, 8 * grp);
+  const int zcol = L::template colbase<DO>(4 * CW, r16, grp) ^ (16 * CW * wave * (int)sizeof(T));
+  const int prow = Tile<T, C>::at(r16, 8 * grp), pput = Tile<T, C>::at(r16, 4 * grp);
 
   const Operand q{static_cast<const char*>(a.q) + (int64_t)hk * a.Dk * ES, a.qs * ES};
   const Operand k{static_cast<const char*>(a.k) + (int64_t)hk * a.Dk * ES, a.ks * ES};
@@ -490,11 +527,10 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   // additions alone are gathered from the end where they weigh most
   constexpr bool BACK = STATE ? !REV : REV;
   auto chunk_of = [&](int i) { return seg.first + (BACK ? seg.count - 1 - i : i); };
-  float unit = 1.f;
   double far = 0.0;                                       // STATE: log of the decay over the chunks done
   auto put_gates = [&](int i) {
     if constexpr (STATE) lin_gates_far<C, REV>(gates(i), gate, a.scale, far);
-    else lin_gates<C, REV>(gates(i), gate, a.scale, unit);
+    else lin_gates<C, REV>(gates(i), gate, a.scale, i ? gates(i + 1).unit : 1.f);
   };
   int count = seg.count;
   if constexpr (STATE) count = lin_reach<C, BACK>(a, seg, h, lds + W::Y, far_total);
@@ -529,13 +565,11 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     f32x4 O[CW][NQ];
     if constexpr (!STATE) {
       // ---- P = (X Y^T) * weights, rows are queries
-      // lane numbers anew in each phase, or the phases' addresses stay in registers
       const int qt = wave % NQ, kt0 = wave / NQ * NT;
       {
-        const int l = fresh_lane(), r16 = l & 15, grp = l >> 4;
         Frag xf[DC / 32];
 #pragma unroll
-        for (int kb = 0; kb < DC / 32; ++kb) xf[kb] = L::template row<DC>(sX, 16 * qt + r16, 32 * kb + 8 * grp);
+        for (int kb = 0; kb < DC / 32; ++kb) xf[kb] = L::template row<DC>(sX, xrow, qt, kb);
         const float qhi = G.hi[16 * qt + r16], qlo = G.lo[16 * qt + r16];
         float csum = 0.f;
 #pragma unroll
@@ -547,23 +581,23 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
           if (need) {
 #pragma unroll
             for (int kb = 0; kb < DC / 32; ++kb)
-              p = L::mma(L::template row<DC>(sY, 16 * kt + r16, 32 * kb + 8 * grp), xf[kb], p);
+              p = L::mma(L::template row<DC>(sY, xrow, kt, kb), xf[kb], p);
             const f32x4 khi = *reinterpret_cast<const f32x4*>(&G.hi[16 * kt + 4 * grp]);
             const f32x4 klo = *reinterpret_cast<const f32x4*>(&G.lo[16 * kt + 4 * grp]);
-            // the tile on the diagonal is cut; its other half may have overflowed
+            // the tile on the diagonal is cut: weight 0 where the exponent is -inf
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float diff = (qhi - khi[r]) + (qlo - klo[r]);
-              p[r] *= a.scale * fexp2(REV ? -diff : diff);
-              if (kt == qt && (REV ? 4 * grp + r < r16 : 4 * grp + r > r16)) p[r] = 0.f;
+              const bool cut = kt == qt && (REV ? 4 * grp + r < r16 : 4 * grp + r > r16);
+              p[r] *= a.scale * fexp2(cut ? -__builtin_inff() : REV ? -diff : diff);
             }
             if constexpr (ROLE == kDk) {
               // the other product of the pair, q_i . k_j
               f32x4 m = zero4();
 #pragma unroll
               for (int kb = 0; kb < DO / 32; ++kb)
-                m = L::mma(L::template row<DO>(sZ, 16 * kt + r16, 32 * kb + 8 * grp),
-                           L::template row<DO>(sK, 16 * qt + r16, 32 * kb + 8 * grp), m);
+                m = L::mma(L::template row<DO>(sZ, zrow, kt, kb),
+                           L::template row<DO>(sK, zrow, qt, kb), m);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const float mm = p[r] * m[r];
@@ -578,7 +612,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
             }
           }
           // a block of 32 keys is read whole: its masked half holds zeros
-          if (REV ? (kt | 1) >= qt : (kt & ~1) <= qt) L::put4(Tile<T, C>::at(sP, 16 * qt + r16, 16 * kt + 4 * grp), p);
+          if (REV ? (kt | 1) >= qt : (kt & ~1) <= qt) L::put4(reinterpret_cast<T*>(sP + 16 * qt * Tile<T, C>::RB + (pput ^ (16 * kt * ES))), p);
           if constexpr (ROLE == kDk) {
             if (r16 == 0)
               *reinterpret_cast<f32x4*>(sums + wave * C + 16 * kt + 4 * grp) = f32x4{rsum[0], rsum[1], rsum[2], rsum[3]};
@@ -597,7 +631,6 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
         for (int t = 0; t < NQ; ++t) O[ct][t] = zero4();
       {
-      const int l = fresh_lane(), r16 = l & 15, grp = l >> 4;
 #pragma unroll
       for (int kb = 0; kb < DC / 32; ++kb) {
         Frag sf[CW][NIN];
@@ -605,7 +638,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
         for (int ct = 0; ct < CW; ++ct) L::template parts<NIN>(S[2 * kb][ct], S[2 * kb + 1][ct], sf[ct]);
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
-          const Frag xf = L::template row<DC>(sX, 16 * t + r16, 32 * kb + 8 * grp);
+          const Frag xf = L::template row<DC>(sX, xrow, t, kb);
 #pragma unroll
           for (int ct = 0; ct < CW; ++ct)
 #pragma unroll
@@ -624,7 +657,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
           for (int ct = 0; ct < CW; ++ct) {
             f32x4 m;
-            if constexpr (ROLE == kDk) m = L::get4(Tile<T, DO>::at(sK, row, at + 4 * ct));
+            if constexpr (ROLE == kDk) m = L::get4(reinterpret_cast<const T*>(sK + Tile<T, DO>::at(row, at + 4 * ct)));
             else m = L::wide(rows[t][ct]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) dot = fmaf(O[ct][t][r], m[r], dot);
@@ -639,12 +672,11 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     __builtin_amdgcn_sched_barrier(0);
     // ---- Z as an operand over tokens
     Frag zf[C / 32][CW];
-    const int l = fresh_lane(), r16 = l & 15, grp = l >> 4;
 #pragma unroll
     for (int tb = 0; tb < C / 32; ++tb)
 #pragma unroll
       for (int ct = 0; ct < CW; ++ct)
-        zf[tb][ct] = L::template col<DO>(sZ, 32 * tb, 16 * CW * wave + 4 * ct, STEP, r16, grp);
+        zf[tb][ct] = L::template col<DO>(sZ, zcol, tb, 4 * ct);
     if constexpr (!STATE) {
       lds_barrier();                                      // P and the sums are there
 #pragma unroll
@@ -652,7 +684,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
         for (int tb = 0; tb < C / 32; ++tb) {
           if (REV ? 2 * tb + 1 < t : 2 * tb > t) continue;
-          const Frag pf = L::template row<C>(sP, 16 * t + r16, 32 * tb + 8 * grp);
+          const Frag pf = L::template row<C>(sP, prow, t, tb);
 #pragma unroll
           for (int ct = 0; ct < CW; ++ct) O[ct][t] = L::mma(zf[tb][ct], pf, O[ct][t]);
         }
@@ -723,7 +755,6 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     }
 #pragma unroll
     for (int tb = 0; tb < C / 32; ++tb) {
-      const int l = fresh_lane(), r16 = l & 15, grp = l >> 4;
       const f32x4 b0 = *reinterpret_cast<const f32x4*>(&G.key[32 * tb + 8 * grp]);
       const f32x4 b1 = *reinterpret_cast<const f32x4*>(&G.key[32 * tb + 8 * grp + 4]);
       Frag zs[CW][NADD];
@@ -735,14 +766,15 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
       }
 #pragma unroll
       for (int mt = 0; mt < DC / 16; ++mt) {
-        const Frag yf = L::template col<DC>(sY, 32 * tb, 32 * (mt >> 1) + 4 * (mt & 1), 8, r16, grp);
+        const Frag yf = L::template col<DC>(sY, ycol, tb, 32 * (mt >> 1) + 4 * (mt & 1));
 #pragma unroll
         for (int ct = 0; ct < CW; ++ct)
 #pragma unroll
           for (int m = 0; m < NADD; ++m) S[mt][ct] = L::mma(yf, zs[ct][m], S[mt][ct]);
       }
     }
-    if (wave == 0 && i + 1 < count) put_gates(i + 1);
+    // the waves take turns
+    if (wave == (STATE ? 0 : (i + 1) % kWaves) && i + 1 < count) put_gates(i + 1);
   }
 
   // ---- the state after the last chunk
@@ -795,7 +827,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 }
 
 template <class T, int DC, int CW, int ROLE>
-__global__ void __launch_bounds__(kThreads, (DC <= 128 ? 2 : 1)) lin_walk_kernel(LinearArgs a, int slabs) {
+__global__ void __launch_bounds__(kThreads, (DC > 128 ? 1 : ROLE == kDq || ROLE == kDk ? 2 : 3)) lin_walk_kernel(LinearArgs a, int slabs) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   // consecutive units, which share q and k, on one XCD (workgroups go round the eight)
   const int unit = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3), per = a.Hv * slabs;
@@ -993,10 +1025,10 @@ LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dv
   const int slabs = Dv <= 128 ? 1 : 2;
   const int64_t chunks = packed ? tokens / C + N : (int64_t)N * ((T + C - 1) / C);
   const int64_t most = packed ? tokens / C + 1 : std::max(1, (T + C - 1) / C);      // of one sequence
-  const int64_t target = 2 * 256 / (bwd ? 2 : 1);
+  const int64_t target = (LINC == 32 ? 3 : 2) * 256 / (bwd ? 2 : 1);
   const int64_t want = std::max<int64_t>(1, (target + Hv * slabs - 1) / (Hv * slabs));
   LinearPlan p{};
-  p.seg = (int)std::min<int64_t>(most, std::max<int64_t>(4, (chunks + want - 1) / want));
+  p.seg = (int)std::min<int64_t>(most, std::max<int64_t>(256 / C, (chunks + want - 1) / want));
   p.segmented = p.seg < most;
   const int64_t m = (int64_t)p.seg * C;
   p.slots = packed ? N + tokens / m : N * std::max<int64_t>(1, (T + m - 1) / m);
