@@ -826,20 +826,52 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   }
 }
 
-template <class T, int DC, int CW, int ROLE>
-__global__ void __launch_bounds__(kThreads, (DC > 128 ? 1 : ROLE == kDq || ROLE == kDk ? 2 : 3)) lin_walk_kernel(LinearArgs a, int slabs) {
+// Slabs of columns of a role's output, and the role over the head's sizes.
+template <int DK, int DV, int ROLE>
+struct RoleDims {
+  static constexpr bool TURNED = ROLE == kDq || ROLE == kDk;
+  static constexpr int DC = TURNED ? DV : DK, DO = TURNED ? DK : DV;
+  static constexpr int CW = DO == 64 ? 1 : 2, SLABS = DO / (64 * CW);
+};
+template <class T, int DK, int DV, int ROLE>
+constexpr int role_lds() {
+  using R = RoleDims<DK, DV, ROLE>;
+  return WalkLds<T, R::DC, R::CW, ROLE>::BYTES;
+}
+template <class T, int DK, int DV, int ROLE>
+__device__ __forceinline__ void lin_role(const LinearArgs& a, int unit, char* lds) {
+  using R = RoleDims<DK, DV, ROLE>;
+  const int per = a.Hv * R::SLABS, slot = unit / per, rest = unit - slot * per;
+  if (slot < a.slots) lin_walk<T, R::DC, R::CW, ROLE>(a, slot, rest / R::SLABS, rest % R::SLABS, lds);
+}
+// Consecutive units, which share q and k, on one XCD (workgroups go round the eight).
+__device__ __forceinline__ int lin_unit() { return (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3); }
+
+template <class T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 3) lin_fwd_kernel(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  // consecutive units, which share q and k, on one XCD (workgroups go round the eight)
-  const int unit = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3), per = a.Hv * slabs;
-  const int slot = unit / per, rest = unit - slot * per;
-  if (slot >= a.slots) return;
-  lin_walk<T, DC, CW, ROLE>(a, slot, rest / slabs, rest % slabs, lds);
+  lin_role<T, DK, DV, kFwd>(a, lin_unit(), lds);
+}
+// blockIdx.y: what segments add to the state, or to its gradient.
+template <class T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 3) lin_states_kernel(LinearArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  if (blockIdx.y == 0) lin_role<T, DK, DV, kStateFwd>(a, lin_unit(), lds);
+  else lin_role<T, DK, DV, kStateRev>(a, lin_unit(), lds);
+}
+// blockIdx.y: the walks of dk, dq and dv, the longest first.
+template <class T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads, DV == 256 ? 1 : 2) lin_bwd_kernel(LinearArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  if (blockIdx.y == 0) lin_role<T, DK, DV, kDk>(a, lin_unit(), lds);
+  else if (blockIdx.y == 1) lin_role<T, DK, DV, kDq>(a, lin_unit(), lds);
+  else lin_role<T, DK, DV, kDv>(a, lin_unit(), lds);
 }
 
 // Folds what each segment adds into the state before it (REV: the gradient of
 // the state after it): buf[slot] is replaced along each sequence.
 template <int C, bool REV>
-__global__ void __launch_bounds__(kThreads) lin_fold_kernel(LinearArgs a, int blocks) {
+__device__ __forceinline__ void lin_fold(const LinearArgs& a, int blocks) {
   const int unit = blockIdx.x / blocks, n = unit / a.Hv, h = unit - n * a.Hv;
   const int64_t elems = (int64_t)a.Dk * a.Dv, at = ((int64_t)(blockIdx.x % blocks) * kThreads + threadIdx.x) * 4;
   if (at >= elems) return;
@@ -871,6 +903,12 @@ __global__ void __launch_bounds__(kThreads) lin_fold_kernel(LinearArgs a, int bl
   }
 }
 
+template <int C>
+__global__ void __launch_bounds__(kThreads) lin_fold_kernel(LinearArgs a, int blocks) {
+  if (blockIdx.y == 0) lin_fold<C, false>(a, blocks);
+  else lin_fold<C, true>(a, blocks);
+}
+
 // dg of a segment's tokens, a wave per (segment, head): suffix sums over each
 // chunk on top of <dS, S> at its end.
 template <int C>
@@ -883,23 +921,34 @@ __global__ void __launch_bounds__(kThreads) lin_dg_kernel(LinearArgs a, int unit
     if (a.ws_dgsum && lane == 0) a.ws_dgsum[unit] = 0.0;
     return;
   }
+  // Tokens backwards, 64 at a time, lane 63 the first of them: a prefix sum over
+  // lanes is a suffix sum over tokens. Chunks need no care of their own: pairs
+  // within one add up to nothing before it.
+  constexpr int AHEAD = 4;
+  const int lo = seg.first * C, hi = min(lo + seg.count * C, seg.len);
   double end = a.ws_end[unit], sum = 0.0;
-  for (int c = seg.first + seg.count - 1; c >= seg.first; --c) {
-    const int n = min(C, seg.len - c * C);
-    // lanes backwards: a prefix sum over lanes is a suffix sum over tokens
-    const int t = C - 1 - lane;
-    const int64_t at = ((int64_t)(seg.cslot + c) * a.Hv + h) * C + t;
-    double x = 0.0;
-    if (t >= 0 && t < n) x = static_cast<double>(a.ws_qdq[at]) + static_cast<double>(a.ws_kdk[at]);
-    x = wave_incl_scan64(x);
-    if (t >= 0 && t < n) {
-      const int64_t tok = seg.bos + c * C + t;
-      // where exp(g) is zero in FP32 nothing reaches over the token
-      const double y = a.g[tok * a.gs + h] < -88.f ? 0.0 : end + x;
-      if (a.ws_dgsum) sum += y;
-      else a.dg[tok * a.Hv + h] = static_cast<float>(y);
+  for (int t0 = hi - 1; t0 >= lo; t0 -= AHEAD * WAVE) {
+    float x[AHEAD], y[AHEAD], g[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int t = t0 - u * WAVE - lane;
+      const int64_t at = ((int64_t)(seg.cslot + t / C) * a.Hv + h) * C + t % C;
+      x[u] = t >= lo ? a.ws_qdq[at] : 0.f;
+      y[u] = t >= lo ? a.ws_kdk[at] : 0.f;
+      g[u] = t >= lo ? a.g[(int64_t)(seg.bos + t) * a.gs + h] : 0.f;
     }
-    end += read_lane64(x, C - 1);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int t = t0 - u * WAVE - lane;
+      const double s = wave_incl_scan64(static_cast<double>(x[u]) + static_cast<double>(y[u]));
+      // where exp(g) is zero in FP32 nothing reaches over the token
+      const double d = g[u] < -88.f ? 0.0 : end + s;
+      if (t >= lo) {
+        if (a.ws_dgsum) sum += d;
+        else a.dg[(int64_t)(seg.bos + t) * a.Hv + h] = static_cast<float>(d);
+      }
+      end += read_lane64(s, WAVE - 1);
+    }
   }
   if (a.ws_dgsum) {
     sum = wave_incl_scan64(sum);
@@ -935,72 +984,52 @@ __global__ void __launch_bounds__(kThreads) lin_group_kernel(LinearArgs a, int64
   Lin<T>::put4(static_cast<T*>(a.dk) + tok * a.Hqk * a.Dk + at, t);
 }
 
-template <class T, int DC, int CW, int ROLE>
-hipError_t walk(const LinearArgs& a, int width, hipStream_t s) {
-  using W = WalkLds<T, DC, CW, ROLE>;
-  const int slabs = width / (64 * CW);
-  const int64_t blocks = (int64_t)a.slots * a.Hv * slabs;
-  if (blocks == 0) return hipSuccess;
-  if (W::BYTES > 65536) {
-    static thread_local int done = -1;
-    int dev = 0;
-    if (hipGetDevice(&dev) == hipSuccess && dev != done) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&lin_walk_kernel<T, DC, CW, ROLE>),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, W::BYTES);
-      if (e != hipSuccess) return e;
-      done = dev;
-    }
-  }
-  lin_walk_kernel<T, DC, CW, ROLE><<<dim3((unsigned)((blocks + 7) / 8 * 8)), kThreads, W::BYTES, s>>>(a, slabs);
+// A kernel's grid: units, rounded up to eight, by y.
+template <class K>
+hipError_t launch(K* kernel, const LinearArgs& a, int64_t units, int y, int lds, hipStream_t s) {
+  if (units == 0) return hipSuccess;
+  kernel<<<dim3((unsigned)((units + 7) / 8 * 8), (unsigned)y), kThreads, lds, s>>>(a);
   return hipGetLastError();
 }
-
-// A role over the sizes. dc: the contraction, width: the output's columns.
-template <class T, int ROLE>
-hipError_t walk_dims(const LinearArgs& a, int dc, int width, hipStream_t s) {
-  if (width == 64) {
-    if (dc == 64) return walk<T, 64, 1, ROLE>(a, width, s);
-    if (dc == 128) return walk<T, 128, 1, ROLE>(a, width, s);
-    if constexpr (ROLE == kDq || ROLE == kDk) return walk<T, 256, 1, ROLE>(a, width, s);
-  } else {
-    if (dc == 64) return walk<T, 64, 2, ROLE>(a, width, s);
-    if (dc == 128) return walk<T, 128, 2, ROLE>(a, width, s);
-    if constexpr (ROLE == kDq || ROLE == kDk) return walk<T, 256, 2, ROLE>(a, width, s);
-  }
-  return hipErrorInvalidValue;
-}
-
-template <int C, bool REV>
-hipError_t fold(const LinearArgs& a, hipStream_t s) {
-  const int blocks = (a.Dk * a.Dv / 4 + kThreads - 1) / kThreads;
-  if (a.N == 0) return hipSuccess;
-  lin_fold_kernel<C, REV><<<dim3((unsigned)(a.N * a.Hv * blocks)), kThreads, 0, s>>>(a, blocks);
+template <class T, int DK, int DV>
+hipError_t launch_states(const LinearArgs& a, int y, hipStream_t s) {
+  constexpr int C = Lin<T>::C;
+  const hipError_t e = launch(lin_states_kernel<T, DK, DV>, a, (int64_t)a.slots * a.Hv * RoleDims<DK, DV, kStateFwd>::SLABS,
+                              y, role_lds<T, DK, DV, kStateFwd>(), s);
+  if (e != hipSuccess || a.N == 0) return e;
+  const int blocks = (DK * DV / 4 + kThreads - 1) / kThreads;
+  lin_fold_kernel<C><<<dim3((unsigned)(a.N * a.Hv * blocks), (unsigned)y), kThreads, 0, s>>>(a, blocks);
   return hipGetLastError();
 }
-
-template <class T>
-hipError_t linear_fwd(const LinearArgs& a, hipStream_t s) {
-  hipError_t e;
+template <class T, int DK, int DV>
+hipError_t launch_fwd(const LinearArgs& a, hipStream_t s) {
   if (a.ws_state) {
-    if ((e = walk_dims<T, kStateFwd>(a, a.Dk, a.Dv, s)) != hipSuccess) return e;
-    if ((e = fold<Lin<T>::C, false>(a, s)) != hipSuccess) return e;
+    const hipError_t e = launch_states<T, DK, DV>(a, 1, s);
+    if (e != hipSuccess) return e;
   }
-  return walk_dims<T, kFwd>(a, a.Dk, a.Dv, s);
+  return launch(lin_fwd_kernel<T, DK, DV>, a, (int64_t)a.slots * a.Hv * RoleDims<DK, DV, kFwd>::SLABS, 1,
+                role_lds<T, DK, DV, kFwd>(), s);
 }
+template <class T, int DK, int DV>
+hipError_t launch_walks(const LinearArgs& a, hipStream_t s) {
+  if (a.ws_state) {
+    const hipError_t e = launch_states<T, DK, DV>(a, 2, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch(lin_bwd_kernel<T, DK, DV>, a, (int64_t)a.slots * a.Hv * RoleDims<DK, DV, kDv>::SLABS, 3,
+                std::max(role_lds<T, DK, DV, kDk>(), role_lds<T, DK, DV, kDv>()), s);
+}
+
+// f<T, Dk, Dv> for the sizes at hand.
+#define GDN_LINEAR_DIMS(f, T)                                                                        \
+  (a.Dk == 64 ? (a.Dv == 64 ? f<T, 64, 64>(a, s) : a.Dv == 128 ? f<T, 64, 128>(a, s) : f<T, 64, 256>(a, s)) \
+              : (a.Dv == 64 ? f<T, 128, 64>(a, s) : a.Dv == 128 ? f<T, 128, 128>(a, s) : f<T, 128, 256>(a, s)))
 
 template <class T>
 hipError_t linear_bwd(const LinearArgs& a, hipStream_t s) {
   constexpr int C = Lin<T>::C;
-  hipError_t e;
-  if (a.ws_state) {
-    if ((e = walk_dims<T, kStateFwd>(a, a.Dk, a.Dv, s)) != hipSuccess) return e;
-    if ((e = walk_dims<T, kStateRev>(a, a.Dk, a.Dv, s)) != hipSuccess) return e;
-    if ((e = fold<C, false>(a, s)) != hipSuccess) return e;
-    if ((e = fold<C, true>(a, s)) != hipSuccess) return e;
-  }
-  if ((e = walk_dims<T, kDq>(a, a.Dv, a.Dk, s)) != hipSuccess) return e;
-  if ((e = walk_dims<T, kDk>(a, a.Dv, a.Dk, s)) != hipSuccess) return e;
-  if ((e = walk_dims<T, kDv>(a, a.Dk, a.Dv, s)) != hipSuccess) return e;
+  hipError_t e = GDN_LINEAR_DIMS(launch_walks, T);
+  if (e != hipSuccess) return e;
   const int units = a.slots * a.Hv;
   if (units > 0) {
     lin_dg_kernel<C><<<dim3((unsigned)((units + kWaves - 1) / kWaves)), kThreads, 0, s>>>(a, units);
@@ -1038,7 +1067,7 @@ LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dv
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& a, bool f32, hipStream_t s) {
-  return f32 ? linear_fwd<float>(a, s) : linear_fwd<bf16>(a, s);
+  return f32 ? GDN_LINEAR_DIMS(launch_fwd, float) : GDN_LINEAR_DIMS(launch_fwd, bf16);
 }
 hipError_t launch_linear_bwd(const LinearArgs& a, bool f32, hipStream_t s) {
   return f32 ? linear_bwd<float>(a, s) : linear_bwd<bf16>(a, s);
