@@ -65,6 +65,10 @@ class PoolStepArgs(ctypes.Structure):
                 ('k', c_vp), ('v', c_vp), ('g', c_vp), ('beta', c_vp), ('o', c_vp)]
 
 
+class PoolLinearStepArgs(ctypes.Structure):
+    _fields_ = [('step', PoolStepArgs), ('g_per_head', c_i32)]
+
+
 class BeamArgs(ctypes.Structure):
     _fields_ = [('B', c_i32), ('W', c_i32), ('V', c_i32), ('K', c_i32), ('io_dtype', c_i32),
                 ('pad_token', c_i32), ('row_stride', c_i64), ('logits', c_vp), ('scores', c_vp),
@@ -128,6 +132,8 @@ def load_library():
                                              c_vp]),
                        ('gdn_pool_step', [ctypes.POINTER(PoolStruct), ctypes.POINTER(PoolStepArgs),
                                           c_vp]),
+                       ('gdn_pool_linear_step', [ctypes.POINTER(PoolStruct),
+                                                 ctypes.POINTER(PoolLinearStepArgs), c_vp]),
                        ('gdn_beam_select', [ctypes.POINTER(BeamArgs), c_vp]),
                        ('gdn_linear_fwd', [ctypes.POINTER(LinearArgs), c_vp]),
                        ('gdn_linear_bwd', [ctypes.POINTER(LinearBwdArgs), c_vp])):
@@ -709,6 +715,13 @@ def gdn_pool_step(pool, layer, slots, q, k, v, g, beta, scale=None, slots_out=No
     named by another sequence that has tokens or copies its state). Returns o
     [B, T, Hv, Dv] in q's type; rows past lens and of absent sequences are not
     written (zero in a new o)."""
+    a, ref, out, keep = _step_args(pool, layer, slots, q, k, v, g, scale, slots_out, lens, readout, out, beta)
+    _launch(load_library().gdn_pool_step, pool.device, pool._ref, ref)
+    return out
+
+
+def _step_args(pool, layer, slots, q, k, v, g, scale, slots_out, lens, readout, out, beta=None, linear=False):
+    """The arguments of a step from checked tensors: (struct, reference, out, tensors to keep)."""
     dev, shape = pool.device, q.shape
     if len(shape) != 4:
         raise ValueError(f'q: [B, T, Hqk, Dk]; got {list(shape)}')
@@ -722,11 +735,14 @@ def gdn_pool_step(pool, layer, slots, q, k, v, g, beta, scale=None, slots_out=No
     a.q_stride = _token_stride(q, 'q', shape_qk, dt, dev)
     a.k_stride = _token_stride(k, 'k', shape_qk, dt, dev)
     a.v_stride = _token_stride(v, 'v', shape_v, dt, dev)
-    _need(g, 'g', torch.float32, shape_g, dev)
-    _need(beta, 'beta', torch.float32, shape_g, dev)
+    per_head = linear and g.dim() == 1
+    _need(g, 'g', torch.float32, (Hv,) if per_head else shape_g, dev)
     _need(slots, 'slots', torch.int32, (B,), dev)
     a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    a.g, a.beta, a.slots = g.data_ptr(), beta.data_ptr(), slots.data_ptr()
+    a.g, a.slots = g.data_ptr(), slots.data_ptr()
+    if not linear:
+        _need(beta, 'beta', torch.float32, shape_g, dev)
+        a.beta = beta.data_ptr()
     if slots_out is not None:
         _need(slots_out, 'slots_out', torch.int32, (B,), dev)
         a.slots_out = slots_out.data_ptr()
@@ -739,7 +755,18 @@ def gdn_pool_step(pool, layer, slots, q, k, v, g, beta, scale=None, slots_out=No
     else:
         _need(out, 'out', dt, shape_v, dev)
     a.o = out.data_ptr()
-    _launch(load_library().gdn_pool_step, dev, pool._ref, ctypes.byref(a))
+    if linear:
+        a = PoolLinearStepArgs(a, per_head)
+    return a, ctypes.byref(a), out, lens
+
+
+def gdn_pool_linear_step(pool, layer, slots, q, k, v, g, scale=None, slots_out=None, lens=None,
+                         readout=READOUT_BEFORE_WRITE, out=None):
+    """Steps of linear attention on the pages of a pool: S <- exp(g) S + k v^T and
+    o = scale S^T q for tokens 0 .. lens[b] - 1 of each sequence; g FP32, [B, T, Hv]
+    or one log-decay per head [Hv]. Everything else as gdn_pool_step."""
+    a, ref, out, keep = _step_args(pool, layer, slots, q, k, v, g, scale, slots_out, lens, readout, out, linear=True)
+    _launch(load_library().gdn_pool_linear_step, pool.device, pool._ref, ref)
     return out
 
 
@@ -872,6 +899,17 @@ def gdn_linear_fwd(q, k, v, g, scale=None, h0=None, cu_seqlens=None, output_fina
         a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
     _launch(lib.gdn_linear_fwd, dev, ref)
     return out, ht
+
+
+def gdn_pool_linear_prefill(pool, layer, slots, q, k, v, g, scale=None, cu_seqlens=None, resume=True):
+    """Prefill of the sequences in `slots` (int32 [N]) by linear attention:
+    gdn_linear_fwd from the states of their pages (resume=False: from zero states,
+    the pages are not read), its final states written to the pages through the pool's
+    quantizer, once. Returns o."""
+    h0 = gdn_pool_read(pool, layer, slots) if resume else None
+    o, ht = gdn_linear_fwd(q, k, v, g, scale, h0, cu_seqlens)
+    gdn_pool_write(pool, layer, slots, ht)
+    return o
 
 
 def gdn_linear_bwd(q, k, v, g, do, dht=None, scale=None, h0=None, cu_seqlens=None, out=None):

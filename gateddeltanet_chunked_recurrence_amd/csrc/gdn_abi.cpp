@@ -984,6 +984,71 @@ gdn_status check_linear_ptrs(const char* what, const LinearPtr* e, int n, const 
   return GDN_OK;
 }
 
+// gdn_pool_step, or (linear) gdn_pool_linear_step: g one per head or per token, no beta.
+gdn_status pool_step(const char* what, const gdn_pool* pool, const gdn_pool_step_args* a, bool linear, bool per_head,
+                     void* stream) {
+  gdn_status s = check_pool(pool, what);
+  if (s != GDN_OK) return s;
+  if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
+  if ((s = check_layer(what, pool, a->layer)) != GDN_OK) return s;
+  if (a->T < 0 || a->Hqk <= 0) return fail(GDN_E_INVALID, "%s: bad sizes T=%d Hqk=%d", what, a->T, a->Hqk);
+  if (pool->Hv % a->Hqk != 0)
+    return fail(GDN_E_INVALID, "%s: Hv (%d) must be a multiple of Hqk (%d)", what, pool->Hv, a->Hqk);
+  if (a->io_dtype != GDN_BF16 && a->io_dtype != GDN_F32)
+    return fail(GDN_E_INVALID, "io_dtype %d: use 0 bf16 or 1 f32", a->io_dtype);
+  if (a->readout != GDN_READOUT_BEFORE_WRITE && a->readout != GDN_READOUT_AFTER_WRITE)
+    return fail(GDN_E_INVALID, "%s: readout %d: use 0 before or 1 after the write", what, a->readout);
+  if (!std::isfinite(a->scale)) return fail(GDN_E_INVALID, "scale is not finite");
+  if ((s = check_entries(what, a->B, a->slots, "slots")) != GDN_OK) return s;
+  const bool any = a->B > 0 && a->T > 0;
+  const struct { const void* p; const char* name; bool required; } ptrs[] = {
+      {a->q, "q", any}, {a->k, "k", any}, {a->v, "v", any}, {a->g, "g", any}, {linear ? nullptr : a->beta, "beta", any && !linear},
+      {a->o, "o", any}, {a->slots_out, "slots_out", false}, {a->lens, "lens", false}};
+  for (const auto& e : ptrs) {
+    if (e.required && !e.p) return fail(GDN_E_INVALID, "%s: %s is NULL", what, e.name);
+    // the gates are read one by one, so they may start at any token of a longer block
+    const uintptr_t align = e.p == a->g || e.p == a->beta ? 4 : 16;
+    if (reinterpret_cast<uintptr_t>(e.p) % align)
+      return fail(GDN_E_INVALID, "%s: %s is not %d-byte aligned", what, e.name, (int)align);
+  }
+  const int64_t es = a->io_dtype == GDN_F32 ? 4 : 2;
+  const int64_t row_qk = (int64_t)a->Hqk * pool->Dk, row_v = (int64_t)pool->Hv * pool->Dv;
+  const struct { int64_t stride, row; const char* name; } strides[] = {
+      {a->q_stride, row_qk, "q"}, {a->k_stride, row_qk, "k"}, {a->v_stride, row_v, "v"}};
+  for (const auto& e : strides)
+    if (e.stride != 0 && (e.stride < e.row || e.stride * es % 16 != 0))
+      return fail(GDN_E_INVALID, "%s: %s_stride %lld: at least %lld and a multiple of 16 bytes", what, e.name,
+                  (long long)e.stride, (long long)e.row);
+  if ((int64_t)a->B * pool->Hv * (pool->Dv / 16) > INT32_MAX - 64)
+    return fail(GDN_E_UNSUPPORTED, "%s: B * Hv * Dv exceeds 2^35", what);
+  if (a->B == 0) return GDN_OK;
+  gdn::PoolStepArgs k{};
+  k.pool = pool_ref(pool);
+  if (!k.pool.err) return no_err_word();
+  k.slots = a->slots;
+  k.slots_out = a->slots_out;
+  k.lens = a->lens;
+  k.q = a->q;
+  k.k = a->k;
+  k.v = a->v;
+  k.g = a->g;
+  k.beta = a->beta;
+  k.o = a->o;
+  k.qs = a->q_stride ? a->q_stride : row_qk;
+  k.ks = a->k_stride ? a->k_stride : row_qk;
+  k.vs = a->v_stride ? a->v_stride : row_v;
+  k.layer_page = (int64_t)a->layer * pool->slots;
+  k.B = a->B;
+  k.T = a->T;
+  k.Hqk = a->Hqk;
+  k.readout = a->readout;
+  k.f32_io = a->io_dtype == GDN_F32;
+  k.scale = a->scale;
+  k.linear = linear;
+  k.gs = per_head ? 0 : pool->Hv;
+  return hip_status(gdn::launch_pool_step(k, static_cast<hipStream_t>(stream)), what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1289,65 +1354,14 @@ gdn_status gdn_pool_reorder(const gdn_pool* pool, const int32_t* slots, const in
 }
 
 gdn_status gdn_pool_step(const gdn_pool* pool, const gdn_pool_step_args* a, void* stream) {
-  const char* what = "gdn_pool_step";
-  gdn_status s = check_pool(pool, what);
-  if (s != GDN_OK) return s;
-  if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
-  if ((s = check_layer(what, pool, a->layer)) != GDN_OK) return s;
-  if (a->T < 0 || a->Hqk <= 0) return fail(GDN_E_INVALID, "%s: bad sizes T=%d Hqk=%d", what, a->T, a->Hqk);
-  if (pool->Hv % a->Hqk != 0)
-    return fail(GDN_E_INVALID, "%s: Hv (%d) must be a multiple of Hqk (%d)", what, pool->Hv, a->Hqk);
-  if (a->io_dtype != GDN_BF16 && a->io_dtype != GDN_F32)
-    return fail(GDN_E_INVALID, "io_dtype %d: use 0 bf16 or 1 f32", a->io_dtype);
-  if (a->readout != GDN_READOUT_BEFORE_WRITE && a->readout != GDN_READOUT_AFTER_WRITE)
-    return fail(GDN_E_INVALID, "%s: readout %d: use 0 before or 1 after the write", what, a->readout);
-  if (!std::isfinite(a->scale)) return fail(GDN_E_INVALID, "scale is not finite");
-  if ((s = check_entries(what, a->B, a->slots, "slots")) != GDN_OK) return s;
-  const bool any = a->B > 0 && a->T > 0;
-  const struct { const void* p; const char* name; bool required; } ptrs[] = {
-      {a->q, "q", any}, {a->k, "k", any}, {a->v, "v", any}, {a->g, "g", any}, {a->beta, "beta", any},
-      {a->o, "o", any}, {a->slots_out, "slots_out", false}, {a->lens, "lens", false}};
-  for (const auto& e : ptrs) {
-    if (e.required && !e.p) return fail(GDN_E_INVALID, "%s: %s is NULL", what, e.name);
-    // the gates are read one by one, so they may start at any token of a longer block
-    const uintptr_t align = e.p == a->g || e.p == a->beta ? 4 : 16;
-    if (reinterpret_cast<uintptr_t>(e.p) % align)
-      return fail(GDN_E_INVALID, "%s: %s is not %d-byte aligned", what, e.name, (int)align);
-  }
-  const int64_t es = a->io_dtype == GDN_F32 ? 4 : 2;
-  const int64_t row_qk = (int64_t)a->Hqk * pool->Dk, row_v = (int64_t)pool->Hv * pool->Dv;
-  const struct { int64_t stride, row; const char* name; } strides[] = {
-      {a->q_stride, row_qk, "q"}, {a->k_stride, row_qk, "k"}, {a->v_stride, row_v, "v"}};
-  for (const auto& e : strides)
-    if (e.stride != 0 && (e.stride < e.row || e.stride * es % 16 != 0))
-      return fail(GDN_E_INVALID, "%s: %s_stride %lld: at least %lld and a multiple of 16 bytes", what, e.name,
-                  (long long)e.stride, (long long)e.row);
-  if ((int64_t)a->B * pool->Hv * (pool->Dv / 16) > INT32_MAX - 64)
-    return fail(GDN_E_UNSUPPORTED, "%s: B * Hv * Dv exceeds 2^35", what);
-  if (a->B == 0) return GDN_OK;
-  gdn::PoolStepArgs k{};
-  k.pool = pool_ref(pool);
-  if (!k.pool.err) return no_err_word();
-  k.slots = a->slots;
-  k.slots_out = a->slots_out;
-  k.lens = a->lens;
-  k.q = a->q;
-  k.k = a->k;
-  k.v = a->v;
-  k.g = a->g;
-  k.beta = a->beta;
-  k.o = a->o;
-  k.qs = a->q_stride ? a->q_stride : row_qk;
-  k.ks = a->k_stride ? a->k_stride : row_qk;
-  k.vs = a->v_stride ? a->v_stride : row_v;
-  k.layer_page = (int64_t)a->layer * pool->slots;
-  k.B = a->B;
-  k.T = a->T;
-  k.Hqk = a->Hqk;
-  k.readout = a->readout;
-  k.f32_io = a->io_dtype == GDN_F32;
-  k.scale = a->scale;
-  return hip_status(gdn::launch_pool_step(k, static_cast<hipStream_t>(stream)), "gdn_pool_step launch");
+  return pool_step("gdn_pool_step", pool, a, false, false, stream);
+}
+
+gdn_status gdn_pool_linear_step(const gdn_pool* pool, const gdn_pool_linear_step_args* a, void* stream) {
+  const char* what = "gdn_pool_linear_step";
+  if (a && a->g_per_head != 0 && a->g_per_head != 1)
+    return fail(GDN_E_INVALID, "%s: g_per_head %d: use 0 per token or 1 per head", what, a->g_per_head);
+  return pool_step(what, pool, a ? &a->step : nullptr, true, a && a->g_per_head, stream);
 }
 
 size_t gdn_beam_workspace_bytes(const gdn_beam_args* a) {

@@ -300,6 +300,8 @@ struct PoolStepArgs {
   int64_t layer_page;         // first page of the layer
   int32_t B, T, Hqk, readout, f32_io;
   float scale;
+  int32_t linear;             // linear attention: u = v, beta is not read
+  int64_t gs;                 // linear: elements between tokens of g (0: one gate per head)
 };
 hipError_t launch_pool_step(const PoolStepArgs& a, hipStream_t s);
 

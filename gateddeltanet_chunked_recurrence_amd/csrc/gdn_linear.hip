@@ -25,12 +25,6 @@
 // segment adds to the state, a second folds these along the sequence, and the
 // walks start at every segment.
 #include <algorithm>
-#ifndef LINC
-#define LINC 32
-#endif
-#ifndef LINOCC
-#define LINOCC 3
-#endif
 
 #include "gdn_device.h"
 #include "gdn_launch.h"
@@ -118,7 +112,7 @@ struct Tile {
 
 template <class T> struct Lin;
 template <> struct Lin<bf16> {
-  static constexpr int C = LINC;
+  static constexpr int C = 32;
   using Frag = bf16x8;
   static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) { return mfma(a, b, c); }
   // elements 32 kb + 8 g .. + 7 of row 16 t + r16; `base`: Tile::at(r16, 8 g)
@@ -1054,7 +1048,11 @@ LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dv
   const int slabs = Dv <= 128 ? 1 : 2;
   const int64_t chunks = packed ? tokens / C + N : (int64_t)N * ((T + C - 1) / C);
   const int64_t most = packed ? tokens / C + 1 : std::max(1, (T + C - 1) / C);      // of one sequence
-  const int64_t target = (LINC == 32 ? 3 : 2) * 256 / (bwd ? 2 : 1);
+  // Segments for two workgroups a CU, or one and each of the gradients' three walks
+  // (4 x 4,096 tokens, 16 heads of 128 x 128, forward: 110, 116, 106 and 121 us for 256, 384,
+  // 512 and 768 workgroups; gradients of 2 x 8,192: 281, 308, 308 and 346); more of them
+  // cost states, fewer leave CUs idle.
+  const int64_t target = bwd ? 256 : 512;
   const int64_t want = std::max<int64_t>(1, (target + Hv * slabs - 1) / (Hv * slabs));
   LinearPlan p{};
   p.seg = (int)std::min<int64_t>(most, std::max<int64_t>(256 / C, (chunks + want - 1) / want));

@@ -11,7 +11,7 @@
 // a = alpha d:  p = c^T k, w = c^T q;  u = beta (v - a p);
 //   o_before = scale (a w + (k . q) u);  S' = a c + k u^T
 // so both products read the codes as they are and the output needs no pass
-// over S'.
+// over S'. Linear attention (LIN) is the same step with u = v.
 //
 // Bound: a token moves Dk Dv bytes in and out per head for 6 Dk Dv FLOP, so
 // at many sequences this is a copy (bound by HBM). The page is value-major
@@ -81,6 +81,13 @@ template <bool F32>
 __device__ __forceinline__ void store4(void* p, f32x4 x) {
   if constexpr (F32) *reinterpret_cast<f32x4*>(p) = x;
   else *reinterpret_cast<bf16x4*>(p) = bf16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
+}
+
+// A token's log-decay. The delta rule's gates are one per token and head; linear
+// attention's may be one per head.
+template <bool LIN>
+__device__ __forceinline__ float step_gate(const PoolStepArgs& a, int64_t token, int h) {
+  return a.g[(LIN ? token * a.gs : token * a.pool.Hv) + h];
 }
 
 // What every wave of a call does first: its sequence, head and rows, whether
@@ -218,7 +225,7 @@ __device__ __forceinline__ float head_kq(const char* hb, int r, int g) {
 // .. + 15 (one 16-byte piece per s). In: codes `raw`, a = exp(g) d. Out: the new
 // codes in `raw`, the tile's scale d and the outputs o. `join` makes the
 // tile's amax of a wave's; `decoded` is called when the codes are in bf16.
-template <int DK, int FMT, bool F32, int NT, typename Decoded, typename Join>
+template <int DK, int FMT, bool F32, int NT, bool LIN, typename Decoded, typename Join>
 __device__ __forceinline__ void step_tile(const PoolRef& P, const char* hb, u32x4 (&raw)[NT][DK / 64],
                                           float alpha, float beta, float kq, float scale,
                                           const float (&v)[NT], float (&o)[NT], float& d, bool after,
@@ -295,7 +302,7 @@ __device__ __forceinline__ void step_tile(const PoolRef& P, const char* hb, u32x
   float m = 0.f;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const float u = beta * fmaf(-alpha, p[j], v[j]);
+    const float u = LIN ? v[j] : beta * fmaf(-alpha, p[j], v[j]);
     o[j] = scale * fmaf(kq, u, alpha * q[j]);
     const float uu = u * ru;
     bf16x8 ub{};
@@ -361,7 +368,7 @@ __device__ __forceinline__ void load_share(const PoolStepArgs& a, int64_t token,
 
 // Several tokens, or lengths: one wave per 16 NT rows, the state stays in
 // registers as codes between tokens.
-template <int DK, int FMT, bool F32, int NT, int WPT>
+template <int DK, int FMT, bool F32, int NT, int WPT, bool LIN>
 __global__ void __launch_bounds__((WPT == 1 ? 4 : WPT) * WAVE)
 pool_step_many_kernel(PoolStepArgs a, int waves) {
   using H = HeadLds<DK, F32>;
@@ -400,8 +407,8 @@ pool_step_many_kernel(PoolStepArgs a, int waves) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       v[j] = F32 ? reinterpret_cast<const float*>(vp)[16 * j] : from_bf16(reinterpret_cast<const bf16*>(vp)[16 * j]);
-    gate = a.g[(tok0 + t) * Hv + w.h];
-    beta = a.beta[(tok0 + t) * Hv + w.h];
+    gate = step_gate<LIN>(a, tok0 + t, w.h);
+    if constexpr (!LIN) beta = a.beta[(tok0 + t) * Hv + w.h];
   };
   if (w.T > 0) load_token(0);
   char* op = static_cast<char*>(a.o) + (tok0 * o_tok + (int64_t)w.h * Dv + w.row + r) * ES;
@@ -430,7 +437,7 @@ pool_step_many_kernel(PoolStepArgs a, int waves) {
     float vt[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) vt[j] = v[j];
-    step_tile<DK, FMT, F32, NT>(
+    step_tile<DK, FMT, F32, NT, LIN>(
         P, hb, raw, alpha, bt, kq, a.scale, vt, o, d, a.readout != 0,
         [&]() {
           if (t + 1 < w.T) load_token(t + 1);
@@ -463,7 +470,7 @@ pool_step_many_kernel(PoolStepArgs a, int waves) {
 // tiles of it) and load the next tile's codes and the next head's inputs
 // before they compute the current ones. A wave that is launched per tile
 // waits for its slot, then for its codes, with nothing else in flight.
-template <int DK, int FMT, bool F32, int NT, int WPT, bool AFTER>
+template <int DK, int FMT, bool F32, int NT, int WPT, bool AFTER, bool LIN>
 __global__ void __launch_bounds__((WPT == 1 ? 4 : WPT) * WAVE, 3)
 pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk) {
   using H = HeadLds<DK, F32>;
@@ -506,8 +513,8 @@ pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk
   float gn = 0.f, bn = 0.f;
   auto load_head = [&](const Place& x) {
     load_share<DK, F32>(a, x.n, x.h / (Hv / a.Hqk), share);
-    gn = a.g[(int64_t)x.n * Hv + x.h];
-    bn = a.beta[(int64_t)x.n * Hv + x.h];
+    gn = step_gate<LIN>(a, x.n, x.h);
+    if constexpr (!LIN) bn = a.beta[(int64_t)x.n * Hv + x.h];
   };
   u32x4 rawn[NT][NS];
   float dn = 1.f;
@@ -597,7 +604,7 @@ pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk
         for (int s = 0; s < NS; ++s) raw[j][s] = rawn[j][s];
       }
       const float alpha = decay * dn;
-      step_tile<DK, FMT, F32, NT>(
+      step_tile<DK, FMT, F32, NT, LIN>(
           P, hb, raw, alpha, beta, kq, a.scale, v, o, d, AFTER,
           [&]() {
             if (t + 1 < span) load_tile(cur, t + 1);
@@ -638,7 +645,7 @@ pool_step_one_kernel(PoolStepArgs a, int lspan, int lparts, int elems, int chunk
 // sequences of up to 5 tokens, 6 heads of 64 x 64 (9 MB in, 9 out): 7.5 us, 8.2
 // without the next token's loads ahead; bound by latency (four waves per CU).
 constexpr int kRows32 = 32;
-template <int DK, bool F32>
+template <int DK, bool F32, bool LIN>
 __global__ void __launch_bounds__(4 * WAVE) pool_step_f32_kernel(PoolStepArgs a, int waves) {
   constexpr int NV = DK / 32, ES = F32 ? 4 : 2, NR = kRows32 / 8;
   static_assert(NR == 4, "one vector of v and o per lane");
@@ -673,8 +680,8 @@ __global__ void __launch_bounds__(4 * WAVE) pool_step_f32_kernel(PoolStepArgs a,
       q[i] = load4<F32>(qp + 32 * i * ES);
     }
     v = load4<F32>(static_cast<const char*>(a.v) + ((tok0 + t) * a.vs + (int64_t)w.h * Dv + row0) * ES);
-    gate = a.g[(tok0 + t) * Hv + w.h];
-    beta = a.beta[(tok0 + t) * Hv + w.h];
+    gate = step_gate<LIN>(a, tok0 + t, w.h);
+    if constexpr (!LIN) beta = a.beta[(tok0 + t) * Hv + w.h];
   };
   if (w.T > 0) load_token(0);
   char* op = static_cast<char*>(a.o) + (tok0 * o_tok + (int64_t)w.h * Dv + row0) * ES;
@@ -707,12 +714,12 @@ __global__ void __launch_bounds__(4 * WAVE) pool_step_f32_kernel(PoolStepArgs a,
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p = fmaf(S[j][i][e], kt[i][e], p);
+          if constexpr (!LIN) p = fmaf(S[j][i][e], kt[i][e], p);
           x = fmaf(S[j][i][e], qt[i][e], x);
         }
-      p = sum_row(p);
+      if constexpr (!LIN) p = sum_row(p);
       x = sum_row(x);
-      const float u = bt * fmaf(-alpha, p, vt[j]);
+      const float u = LIN ? vt[j] : bt * fmaf(-alpha, p, vt[j]);
       o[j] = a.scale * fmaf(kq, u, alpha * x);       // both readouts: nothing is rounded on the way
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -738,7 +745,7 @@ inline int ilog2(int x) {
   return l;
 }
 
-template <int DK, int FMT, bool F32, int NT, int WPT>
+template <int DK, int FMT, bool F32, int NT, int WPT, bool LIN>
 void launch_codes_wpt(const PoolStepArgs& a, hipStream_t s) {
   constexpr int NW = WPT == 1 ? 4 : WPT;
   if (a.T == 1 && !a.lens) {
@@ -751,14 +758,14 @@ void launch_codes_wpt(const PoolStepArgs& a, hipStream_t s) {
     const int elems = heads * (tph / span), chunk = std::min(2, (elems + room - 1) / room);
     const int blocks = ((elems + chunk - 1) / chunk + gpb - 1) / gpb;
     if (a.readout)
-      pool_step_one_kernel<DK, FMT, F32, NT, WPT, true><<<dim3(blocks), NW * WAVE, 0, s>>>(
+      pool_step_one_kernel<DK, FMT, F32, NT, WPT, true, LIN><<<dim3(blocks), NW * WAVE, 0, s>>>(
           a, ilog2(span), ilog2(tph / span), elems, chunk);
     else
-      pool_step_one_kernel<DK, FMT, F32, NT, WPT, false><<<dim3(blocks), NW * WAVE, 0, s>>>(
+      pool_step_one_kernel<DK, FMT, F32, NT, WPT, false, LIN><<<dim3(blocks), NW * WAVE, 0, s>>>(
           a, ilog2(span), ilog2(tph / span), elems, chunk);
   } else {
     const int waves = a.B * a.pool.Hv * (a.pool.Dv / (16 * NT));
-    pool_step_many_kernel<DK, FMT, F32, NT, WPT><<<dim3((waves + NW - 1) / NW), NW * WAVE, 0, s>>>(a, waves);
+    pool_step_many_kernel<DK, FMT, F32, NT, WPT, LIN><<<dim3((waves + NW - 1) / NW), NW * WAVE, 0, s>>>(a, waves);
   }
 }
 
@@ -768,31 +775,36 @@ void launch_codes_wpt(const PoolStepArgs& a, hipStream_t s) {
 // E4M3 27.5, 28, 34 and 71 with one, 25.4, 25.4, 30 and 65.5 with two). A tile of 16
 // is one. INT8 tiles of 256 at 128 keys are 16 waves, which caps them at 128
 // registers: they spill 25 to 51.
-template <int DK, int FMT, bool F32>
+template <int DK, int FMT, bool F32, bool LIN>
 void launch_codes(const PoolStepArgs& a, hipStream_t s) {
   constexpr int NT = FMT == 2 && DK == 128 ? 1 : 2;
   switch (a.pool.block_v) {
-    case 16: return launch_codes_wpt<DK, FMT, F32, 1, 1>(a, s);
-    case 32: return launch_codes_wpt<DK, FMT, F32, NT, 2 / NT>(a, s);
-    case 64: return launch_codes_wpt<DK, FMT, F32, NT, 4 / NT>(a, s);
-    case 128: return launch_codes_wpt<DK, FMT, F32, NT, 8 / NT>(a, s);
-    default: return launch_codes_wpt<DK, FMT, F32, NT, 16 / NT>(a, s);
+    case 16: return launch_codes_wpt<DK, FMT, F32, 1, 1, LIN>(a, s);
+    case 32: return launch_codes_wpt<DK, FMT, F32, NT, 2 / NT, LIN>(a, s);
+    case 64: return launch_codes_wpt<DK, FMT, F32, NT, 4 / NT, LIN>(a, s);
+    case 128: return launch_codes_wpt<DK, FMT, F32, NT, 8 / NT, LIN>(a, s);
+    default: return launch_codes_wpt<DK, FMT, F32, NT, 16 / NT, LIN>(a, s);
   }
 }
 
-template <int DK, bool F32>
+template <int DK, bool F32, bool LIN>
 void launch_dk(const PoolStepArgs& a, hipStream_t s) {
-  if (a.pool.fmt == 1) return launch_codes<DK, 1, F32>(a, s);
-  if (a.pool.fmt == 2) return launch_codes<DK, 2, F32>(a, s);
+  if (a.pool.fmt == 1) return launch_codes<DK, 1, F32, LIN>(a, s);
+  if (a.pool.fmt == 2) return launch_codes<DK, 2, F32, LIN>(a, s);
   const int waves = a.B * a.pool.Hv * (a.pool.Dv / kRows32);
-  pool_step_f32_kernel<DK, F32><<<dim3((unsigned)((waves + 3) / 4)), 4 * WAVE, 0, s>>>(a, waves);
+  pool_step_f32_kernel<DK, F32, LIN><<<dim3((unsigned)((waves + 3) / 4)), 4 * WAVE, 0, s>>>(a, waves);
 }
 
 }  // namespace
 
 hipError_t launch_pool_step(const PoolStepArgs& a, hipStream_t s) {
-  if (a.pool.Dk == 128) a.f32_io ? launch_dk<128, true>(a, s) : launch_dk<128, false>(a, s);
-  else a.f32_io ? launch_dk<64, true>(a, s) : launch_dk<64, false>(a, s);
+  if (a.linear) {
+    if (a.pool.Dk == 128) a.f32_io ? launch_dk<128, true, true>(a, s) : launch_dk<128, false, true>(a, s);
+    else a.f32_io ? launch_dk<64, true, true>(a, s) : launch_dk<64, false, true>(a, s);
+  } else {
+    if (a.pool.Dk == 128) a.f32_io ? launch_dk<128, true, false>(a, s) : launch_dk<128, false, false>(a, s);
+    else a.f32_io ? launch_dk<64, true, false>(a, s) : launch_dk<64, false, false>(a, s);
+  }
   return hipGetLastError();
 }
 

@@ -591,6 +591,17 @@ typedef struct {
 size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_bwd_args* a);   /* 0 on error */
 gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* a, void* stream);
 
+/* Its step on the pages of a state pool (as gdn_pool_step in all else): tokens
+ * 0 .. lens[b] - 1 of each sequence from the states in `slots`,
+ *   S <- exp(g_t) S + k_t v_t^T;  o_before = scale S^T q_t;  S <- QDQ_S(S);
+ *   o_after = scale S^T q_t
+ * step.beta is not read; |v| has to stay below 2^63 with pages of codes. */
+typedef struct {
+  gdn_pool_step_args step;
+  int32_t g_per_head;          /* 0: step.g [B, T, Hv]; 1: step.g [Hv]        */
+} gdn_pool_linear_step_args;
+gdn_status gdn_pool_linear_step(const gdn_pool* pool, const gdn_pool_linear_step_args* a, void* stream);
+
 const char* gdn_last_error(void);
 int32_t gdn_abi_version(void);
 
