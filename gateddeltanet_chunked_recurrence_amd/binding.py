@@ -76,6 +76,14 @@ class BeamArgs(ctypes.Structure):
                 ('workspace', c_vp), ('workspace_bytes', c_sz)]
 
 
+class LogitsArgs(ctypes.Structure):
+    _fields_ = [('B', c_i32), ('W', c_i32), ('V', c_i32), ('io_dtype', c_i32), ('L', c_i32), ('num_bias', c_i32),
+                ('num_masks', c_i32), ('row_stride', c_i64), ('out_stride', c_i64), ('token_stride', c_i64),
+                ('logits', c_vp), ('out', c_vp), ('tokens', c_vp), ('lens', c_vp), ('prompt_lens', c_vp),
+                ('repetition', c_vp), ('presence', c_vp), ('frequency', c_vp), ('bias_ids', c_vp),
+                ('bias_vals', c_vp), ('mask', c_vp), ('mask_rows', c_vp)]
+
+
 class LinearArgs(ctypes.Structure):
     _fields_ = [('B', c_i32), ('T', c_i32), ('Hqk', c_i32), ('Hv', c_i32), ('Dk', c_i32), ('Dv', c_i32),
                 ('num_seqs', c_i32), ('io_dtype', c_i32), ('g_per_head', c_i32), ('scale', c_f32),
@@ -135,6 +143,7 @@ def load_library():
                        ('gdn_pool_linear_step', [ctypes.POINTER(PoolStruct),
                                                  ctypes.POINTER(PoolLinearStepArgs), c_vp]),
                        ('gdn_beam_select', [ctypes.POINTER(BeamArgs), c_vp]),
+                       ('gdn_logits_adjust', [ctypes.POINTER(LogitsArgs), c_vp]),
                        ('gdn_linear_fwd', [ctypes.POINTER(LinearArgs), c_vp]),
                        ('gdn_linear_bwd', [ctypes.POINTER(LinearBwdArgs), c_vp])):
         f = getattr(lib, name)
@@ -176,7 +185,7 @@ def _check(status):
 
 
 DEVERR_LDS_WAIT, DEVERR_FLAG_WAIT, DEVERR_SAVED_STAMP, DEVERR_P_RANGE = 1, 2, 4, 8
-DEVERR_POOL_SLOT = 16
+DEVERR_POOL_SLOT, DEVERR_RULE_ROW = 16, 32
 
 
 def fwd_schedule(args, cus=0):
@@ -787,6 +796,80 @@ def gdn_pool_prefill(pool, layer, slots, q, k, v, g, beta, scale=None, cu_seqlen
     return o
 
 
+def _logit_rows(t, name):
+    """(B, W, V, elements between rows or 0) of logits [B, W, V] with evenly spaced rows."""
+    if t.dim() != 3:
+        raise ValueError(f'{name}: [B, W, V]; got {list(t.shape)}')
+    B, W, V = t.shape
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise ValueError(f'{name}: bfloat16 or float32, not {t.dtype}')
+    sb, sw, sv = t.stride()
+    rs = sw if W > 1 else sb
+    if t.numel() and ((sv != 1 and V > 1) or (W > 1 and B > 1 and sb != W * sw) or
+                      (B * W > 1 and rs < V)):
+        raise ValueError(f'{name}: rows must be contiguous and evenly spaced; got strides '
+                         f'{t.stride()}')
+    return B, W, V, rs if B * W > 1 else 0
+
+
+def gdn_logits_adjust(logits, tokens=None, lens=None, prompt_lens=None, repetition=None, presence=None,
+                      frequency=None, bias=None, mask=None, mask_rows=None, out=None):
+    """Penalties of repeated tokens, biases and grammar masks on the logits
+    [B, W, V] (bf16 or FP32, rows evenly spaced) of B requests of W beams; see
+    gdn_logits_adjust in include/gdn.h for the rules and their order.
+
+    tokens int32 [B, W, L]: each beam's history, of which lens [B, W] (default L)
+    count, the first prompt_lens [B] (default none) as the prompt. repetition
+    (above 0, prompt and generation), presence and frequency (generation): FP32 [B]
+    or None. bias: (ids int32, values FP32) [B, n] each, n up to 1024, id -1 for
+    none. mask int32 [M, ceil(V / 32)], bit t of a row: t is allowed; mask_rows int32
+    [B, W] picks a row for each beam (-1: none; default: row b W + w). Returns a new
+    tensor, or out, which may be logits."""
+    B, W, V, rs = _logit_rows(logits, 'logits')
+    dev = logits.device
+    if out is None:
+        out = torch.empty(B, W, V, dtype=logits.dtype, device=dev)
+    elif out.shape != logits.shape or out.dtype is not logits.dtype or out.device != dev:
+        raise ValueError(f'out: {str(logits.dtype)[6:]} {list(logits.shape)} on {dev}; got '
+                         f'{str(out.dtype)[6:]} {list(out.shape)} on {out.device}')
+    a = LogitsArgs(B=B, W=W, V=V, io_dtype=GDN_BF16 if logits.dtype is torch.bfloat16 else GDN_F32,
+                   row_stride=rs, out_stride=_logit_rows(out, 'out')[3], logits=logits.data_ptr(),
+                   out=out.data_ptr())
+    if tokens is not None:
+        L = tokens.shape[-1] if tokens.dim() else 0
+        _need(tokens, 'tokens', torch.int32, (B, W, L), dev)
+        a.L, a.tokens = L, tokens.data_ptr()
+        if lens is not None:
+            _need(lens, 'lens', torch.int32, (B, W), dev)
+            a.lens = lens.data_ptr()
+        if prompt_lens is not None:
+            _need(prompt_lens, 'prompt_lens', torch.int32, (B,), dev)
+            a.prompt_lens = prompt_lens.data_ptr()
+        for name, t in (('repetition', repetition), ('presence', presence), ('frequency', frequency)):
+            if t is not None:
+                _need(t, name, torch.float32, (B,), dev)
+                setattr(a, name, t.data_ptr())
+    elif not (lens is prompt_lens is repetition is presence is frequency is None):
+        raise ValueError('penalties need tokens')
+    if bias is not None:
+        ids, vals = bias
+        n = ids.shape[-1] if ids.dim() else 0
+        _need(ids, 'bias ids', torch.int32, (B, n), dev)
+        _need(vals, 'bias values', torch.float32, (B, n), dev)
+        a.num_bias, a.bias_ids, a.bias_vals = n, ids.data_ptr(), vals.data_ptr()
+    if mask is not None:
+        M = mask.shape[0] if mask.dim() else 0
+        _need(mask, 'mask', torch.int32, (M, (V + 31) // 32), dev)
+        a.num_masks, a.mask = M, mask.data_ptr()
+        if mask_rows is not None:
+            _need(mask_rows, 'mask_rows', torch.int32, (B, W), dev)
+            a.mask_rows = mask_rows.data_ptr()
+    elif mask_rows is not None:
+        raise ValueError('mask_rows need a mask')
+    _launch(load_library().gdn_logits_adjust, dev, ctypes.byref(a))
+    return out
+
+
 def gdn_beam_select(logits, scores, num_select=None, finished=None, pad_token=0):
     """The num_select (default W, at most 64) best continuations of each of B
     requests of W beams (W up to 32): logits [B, W, V] (bf16 or FP32, rows
@@ -795,23 +878,13 @@ def gdn_beam_select(logits, scores, num_select=None, finished=None, pad_token=0)
     (scores [B, K] FP32, parents [B, K] int32, tokens [B, K] int32), best
     first, ties to the lower beam then token; see gdn_beam_select in
     include/gdn.h for masked, NaN and exhausted rows."""
-    if logits.dim() != 3:
-        raise ValueError(f'logits: [B, W, V]; got {list(logits.shape)}')
-    B, W, V = logits.shape
+    B, W, V, rs = _logit_rows(logits, 'logits')
     K = W if num_select is None else num_select
     dev, dt = logits.device, logits.dtype
-    if dt is not torch.bfloat16 and dt is not torch.float32:
-        raise ValueError(f'logits: bfloat16 or float32, not {dt}')
-    sb, sw, sv = logits.stride()
-    rs = sw if W > 1 else sb
-    if logits.numel() and ((sv != 1 and V > 1) or (W > 1 and B > 1 and sb != W * sw) or
-                           (B * W > 1 and rs < V)):
-        raise ValueError(f'logits: rows must be contiguous and evenly spaced; got strides '
-                         f'{logits.stride()}')
     _need(scores, 'scores', torch.float32, (B, W), dev)
     scores = _aligned(scores)
     a = BeamArgs(B=B, W=W, V=V, K=K, io_dtype=GDN_BF16 if dt is torch.bfloat16 else GDN_F32,
-                 pad_token=pad_token, row_stride=rs if B * W > 1 else 0, logits=logits.data_ptr(),
+                 pad_token=pad_token, row_stride=rs, logits=logits.data_ptr(),
                  scores=scores.data_ptr())
     if finished is not None:
         _need(finished, 'finished', torch.bool if finished.dtype is torch.bool else torch.uint8,
@@ -832,15 +905,18 @@ def gdn_beam_select(logits, scores, num_select=None, finished=None, pad_token=0)
     return out, parents, tokens
 
 
-def gdn_beam_advance(pool, slots, logits, scores, finished=None, pad_token=0):
+def gdn_beam_advance(pool, slots, logits, scores, finished=None, pad_token=0, rules=None):
     """One step of beam search over the states of a pool: gdn_beam_select of W
     continuations of each request, then gdn_pool_reorder of the beams' pages
-    (slots int32 [B, W]) to their parents'. Returns (scores, parents,
-    tokens) as gdn_beam_select does."""
+    (slots int32 [B, W]) to their parents'. rules: arguments of gdn_logits_adjust
+    (a dict), applied to the logits before the selection; the logits themselves are
+    left as they are. Returns (scores, parents, tokens) as gdn_beam_select does."""
     if logits.dim() != 3 or tuple(slots.shape) != tuple(logits.shape[:2]):
         raise ValueError(f'slots: [B, W] of logits [B, W, V]; got {list(slots.shape)} and '
                          f'{list(logits.shape)}')
     _need(slots, 'slots', torch.int32, slots.shape, pool.device)
+    if rules:
+        logits = gdn_logits_adjust(logits, **rules)
     out, parents, tokens = gdn_beam_select(logits, scores, None, finished, pad_token)
     gdn_pool_reorder(pool, slots, parents)
     return out, parents, tokens

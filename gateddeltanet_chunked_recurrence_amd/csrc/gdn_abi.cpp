@@ -921,7 +921,7 @@ LinearWs linear_ws(const gdn_linear_args* a, const gdn::LinearPlan& p, bool bwd)
     part(w.qdq, dots);
     part(w.kdk, dots);
     part(w.end, sh * 4);
-    if (a->g_per_head) part(w.dgsum, sh * 8);
+    if (a->g_per_head) part(w.dgsum, std::max<int64_t>(sh, 1) * 8);   // present without a sequence too: dg is 0
     if (a->Hv != a->Hqk) {
       const int64_t parts = (int64_t)a->B * a->T * a->Hv * a->Dk * 4;
       part(w.dq, parts);
@@ -1455,6 +1455,78 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* a, void* stream) {
   k.dh0 = a->dh0;
   return hip_status(gdn::launch_linear_bwd(k, f->io_dtype == GDN_F32, static_cast<hipStream_t>(stream)),
                     "gdn_linear_bwd launch");
+}
+
+gdn_status gdn_logits_adjust(const gdn_logits_args* a, void* stream) {
+  const char* what = "gdn_logits_adjust";
+  if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
+  if (a->B < 0 || a->B > 65535 || a->W < 1 || a->V < 1 || a->L < 0 || a->num_masks < 0)
+    return fail(GDN_E_INVALID, "%s: bad sizes B=%d W=%d V=%d L=%d num_masks=%d", what, a->B, a->W, a->V, a->L,
+                a->num_masks);
+  if (a->W > 65535 || a->V > (1 << 30)) return fail(GDN_E_UNSUPPORTED, "%s: W %d, V %d: too large", what, a->W, a->V);
+  if (a->L >= (1 << 20)) return fail(GDN_E_UNSUPPORTED, "%s: L %d: below 2^20", what, a->L);
+  if (a->num_bias < 0 || a->num_bias > gdn::kRulesMaxBias)
+    return fail(GDN_E_UNSUPPORTED, "%s: num_bias %d: 0 to %d", what, a->num_bias, gdn::kRulesMaxBias);
+  if (a->io_dtype != GDN_BF16 && a->io_dtype != GDN_F32)
+    return fail(GDN_E_INVALID, "io_dtype %d: use 0 bf16 or 1 f32", a->io_dtype);
+  const struct { int64_t stride, row; const char* name; } strides[] = {
+      {a->row_stride, a->V, "row"}, {a->out_stride, a->V, "out"}, {a->token_stride, a->L, "token"}};
+  for (const auto& e : strides)
+    if (e.stride != 0 && e.stride < e.row)
+      return fail(GDN_E_INVALID, "%s: %s_stride %lld below %lld", what, e.name, (long long)e.stride, (long long)e.row);
+  const bool any = a->B > 0, bias = any && a->num_bias > 0;
+  const uintptr_t es = a->io_dtype == GDN_F32 ? 4 : 2;
+  const struct { const void* p; const char* name; bool required; uintptr_t align; } ptrs[] = {
+      {a->logits, "logits", any, es},          {a->out, "out", any, es},
+      {a->tokens, "tokens", false, 4},         {a->lens, "lens", false, 4},
+      {a->prompt_lens, "prompt_lens", false, 4}, {a->repetition, "repetition", false, 4},
+      {a->presence, "presence", false, 4},     {a->frequency, "frequency", false, 4},
+      {a->bias_ids, "bias_ids", bias, 4},      {a->bias_vals, "bias_vals", bias, 4},
+      {a->mask, "mask", false, 4},             {a->mask_rows, "mask_rows", false, 4}};
+  for (const auto& e : ptrs) {
+    if (e.required && !e.p) return fail(GDN_E_INVALID, "%s: %s is NULL", what, e.name);
+    if (reinterpret_cast<uintptr_t>(e.p) % e.align)
+      return fail(GDN_E_INVALID, "%s: %s is not %d-byte aligned", what, e.name, (int)e.align);
+  }
+  if (a->mask && !a->mask_rows && (int64_t)a->num_masks < (int64_t)a->B * a->W)
+    return fail(GDN_E_INVALID, "%s: num_masks %d: one for each of the %lld rows without mask_rows", what, a->num_masks,
+                (long long)a->B * a->W);
+  if (a->mask_rows && !a->mask) return fail(GDN_E_INVALID, "%s: mask is NULL", what);
+  gdn::RulesArgs k{};
+  k.in_stride = a->row_stride ? a->row_stride : a->V;
+  k.out_stride = a->out_stride ? a->out_stride : a->V;
+  const int64_t rows = (int64_t)a->B * a->W;
+  const char *li = static_cast<const char*>(a->logits), *lo = static_cast<const char*>(a->out);
+  if (any && (li != lo || k.in_stride != k.out_stride) &&
+      li < lo + ((rows - 1) * k.out_stride + a->V) * (int64_t)es && lo < li + ((rows - 1) * k.in_stride + a->V) * (int64_t)es)
+    return fail(GDN_E_INVALID, "%s: out overlaps logits and is not logits itself", what);
+  k.logits = a->logits;
+  k.out = a->out;
+  k.tokens = a->L > 0 ? a->tokens : nullptr;
+  k.lens = a->lens;
+  k.prompt_lens = a->prompt_lens;
+  k.repetition = a->repetition;
+  k.presence = a->presence;
+  k.frequency = a->frequency;
+  k.bias_ids = a->bias_ids;
+  k.bias_vals = a->bias_vals;
+  k.mask = a->mask;
+  k.mask_rows = a->mask_rows;
+  k.tok_stride = a->token_stride ? a->token_stride : a->L;
+  k.B = a->B;
+  k.W = a->W;
+  k.V = a->V;
+  k.L = a->L;
+  k.nb = a->num_bias;
+  k.masks = a->num_masks;
+  k.words = (a->V + 31) / 32;
+  k.f32 = a->io_dtype == GDN_F32;
+  if (!any) return GDN_OK;
+  gdn::rules_plan(k);
+  if ((int64_t)k.B * k.W * k.tiles > INT32_MAX) return fail(GDN_E_UNSUPPORTED, "%s: B * W * V is too large", what);
+  k.err = err_word();
+  if (!k.err) return no_err_word();
+  return hip_status(gdn::launch_rules(k, static_cast<hipStream_t>(stream)), "gdn_logits_adjust launch");
 }
 
 }  // extern "C"

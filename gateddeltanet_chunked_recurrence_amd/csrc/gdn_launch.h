@@ -99,6 +99,7 @@ constexpr uint32_t kErrFlagWait = 2u;     // a bounded wait on another workgroup
 constexpr uint32_t kErrSavedStamp = 4u;   // saved buffer written under another policy or shape
 constexpr uint32_t kErrPRange = 8u;       // a masked Q K^T entry beyond the fp16 range
 constexpr uint32_t kErrPoolSlot = 16u;    // a pool slot out of range, or written while named twice
+constexpr uint32_t kErrRuleRow = 32u;     // rules on logits: a mask row outside the table
 
 // The policy and shape a forward wrote its saved buffer under; the backward
 // compares it with its own arguments on the device.
@@ -324,6 +325,29 @@ struct BeamArgs {
 void beam_plan(BeamArgs& a);
 int64_t beam_workspace_bytes(const BeamArgs& a);
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
+
+// Rules on logits (gdn_rules.hip).
+constexpr int kRulesMaxBias = 1024;
+struct RulesArgs {
+  const void* logits;
+  void* out;                  // may be logits
+  const int32_t* tokens;      // nullable: [B * W, L] histories
+  const int32_t* lens;        // nullable (L)
+  const int32_t* prompt_lens; // nullable (0)
+  const float* repetition;    // nullable, [B] as the next two
+  const float* presence;
+  const float* frequency;
+  const int32_t* bias_ids;    // [B, nb]
+  const float* bias_vals;
+  const uint32_t* mask;       // nullable: [masks, words]
+  const int32_t* mask_rows;   // nullable (row r of the table for row r)
+  uint32_t* err;
+  int64_t in_stride, out_stride, tok_stride;
+  int32_t B, W, V, L, nb, masks, words, f32;
+  int32_t tile, tiles;        // tokens per workgroup, workgroups per row
+};
+void rules_plan(RulesArgs& a);
+hipError_t launch_rules(const RulesArgs& a, hipStream_t s);
 
 // Linear attention with a decay per head (gdn_linear.hip).
 struct LinearArgs {

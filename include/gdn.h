@@ -527,6 +527,47 @@ typedef struct {
 size_t gdn_beam_workspace_bytes(const gdn_beam_args* a);   /* 0 on error */
 gdn_status gdn_beam_select(const gdn_beam_args* a, void* stream);
 
+/* Rules on the logits of B requests of W beams, before gdn_beam_select or any
+ * other choice. Token t of row (b, w), in FP32, rounded once to the logits' type:
+ *   x <- x > 0 ? x / repetition[b] : x * repetition[b]   if t is in the row's
+ *                                     history (prompt or generation)
+ *   x <- x - frequency[b] n_t - presence[b] [n_t > 0]    n_t: times generated
+ *   x <- x + the sum of bias_vals[b, i] with bias_ids[b, i] == t, in their order
+ *        (-inf is a ban, whatever x was)
+ *   x <- -inf                         where the row's mask has bit t 0
+ * in this order. Tokens that no rule names keep their bits, NaN and infinities
+ * too. Ids outside [0, V) are skipped (padding is -1). repetition has to be above 0.
+ * Integer counts only decide, so results repeat bit for bit. Allocates nothing,
+ * needs no workspace, may be captured. */
+typedef struct {
+  int32_t B, W, V;
+  int32_t io_dtype;            /* gdn_dtype of logits and out                 */
+  int32_t L;                   /* tokens per history row, below 2^20          */
+  int32_t num_bias;            /* entries per request, 0 to 1024              */
+  int32_t num_masks;           /* rows of mask                                */
+  int64_t row_stride;          /* elements between rows of logits; 0: V       */
+  int64_t out_stride;          /* of out; 0: V                                */
+  int64_t token_stride;        /* elements between rows of tokens; 0: L       */
+  const void* logits;          /* [B, W, V], rows aligned to an element only  */
+  void* out;                   /* out [B, W, V]; logits itself (with its stride),
+                                  or memory apart from it                     */
+  const int32_t* tokens;       /* [B, W, L] histories, or NULL (no penalties); aligned to
+                                  an element only, as the next two            */
+  const int32_t* lens;         /* [B, W] tokens of each history (cut to [0, L]), or NULL (L) */
+  const int32_t* prompt_lens;  /* [B] of them the prompt's, the first ones, or NULL (0) */
+  const float* repetition;     /* [B], or NULL (1)                            */
+  const float* presence;       /* [B], or NULL (0)                            */
+  const float* frequency;      /* [B], or NULL (0)                            */
+  const int32_t* bias_ids;     /* [B, num_bias]                               */
+  const float* bias_vals;      /* [B, num_bias]                               */
+  const uint32_t* mask;        /* [num_masks, ceil(V / 32)] words, bit t & 31 of word t / 32:
+                                  t is allowed; or NULL                       */
+  const int32_t* mask_rows;    /* [B, W] row of mask, -1: none; NULL: row b W + w. A row
+                                  outside the table makes the logits NaN and
+                                  sets GDN_DEVERR_RULE_ROW                    */
+} gdn_logits_args;
+gdn_status gdn_logits_adjust(const gdn_logits_args* a, void* stream);
+
 /* ------------------------------------------------------------------------
  * Linear attention with a decay per head: the recurrence above without the
  * delta rule's read before the write. Per sequence and value head, from h0:
@@ -624,7 +665,9 @@ int32_t gdn_abi_version(void);
  *   GDN_DEVERR_POOL_SLOT    a state pool call named a slot outside the pool,
  *                           or one that it would write twice, or write while
  *                           another of its entries reads it (that page is
- *                           left as it was).
+ *                           left as it was);
+ *   GDN_DEVERR_RULE_ROW     gdn_logits_adjust named a mask outside the table
+ *                           (that row of logits is NaN).
  * Diagnostic query: unlike every other entry point it synchronizes the
  * device, then writes the flags to *flags and clears them. */
 #define GDN_DEVERR_LDS_WAIT 1u
@@ -632,6 +675,7 @@ int32_t gdn_abi_version(void);
 #define GDN_DEVERR_SAVED_STAMP 4u
 #define GDN_DEVERR_P_RANGE 8u
 #define GDN_DEVERR_POOL_SLOT 16u
+#define GDN_DEVERR_RULE_ROW 32u
 gdn_status gdn_device_errors(uint32_t* flags);
 
 #ifdef __cplusplus

@@ -143,3 +143,143 @@ def test_forward(case):
 def test_backward(case):
     say(f'linear backward {case}')
     check_bwd(*make(*case, seed=2), case[0])
+
+
+def test_gradient_of_dg_against_differences():
+    """FP32, a few gates moved by 2^-9: (loss(g + h) - loss(g - h)) / 2h of the GPU forward, whose own FP32
+    error of 2^-22 of a loss of this size is divided by 2h; the curvature's part is h^2 / 6 of the third derivative."""
+    x, d, cu = make('f32', 1, 130, None, 1, 2, 64, 64, seed=4)
+    got = G.gdn_linear_bwd(d['q'], d['k'], d['v'], d['g'], d['do'], dht=d['dht'], h0=d['h0'])
+    h = 2.0 ** -9
+
+    def loss(g):
+        o, ht = G.gdn_linear_fwd(d['q'], d['k'], d['v'], g, h0=d['h0'])
+        a, b = o.double() * d['do'].double(), ht.double() * d['dht'].double()
+        return float(a.sum() + b.sum()), float(a.abs().sum() + b.abs().sum())
+
+    for t, hd in ((0, 0), (31, 1), (32, 0), (100, 1), (129, 0)):
+        gp, gm = d['g'].clone(), d['g'].clone()
+        gp[0, t, hd] += h
+        gm[0, t, hd] -= h
+        (lp, size), (lm, _) = loss(gp), loss(gm)
+        slope = (lp - lm) / float(gp[0, t, hd].double() - gm[0, t, hd].double())
+        say(f'  t {t}: {slope:.6f} and {float(got["dg"][0, t, hd]):.6f}')
+        assert abs(slope - float(got['dg'][0, t, hd])) <= size * (2.0 ** -22 / h + h * h)
+
+
+def test_views_write_to_given_memory_and_leave_other_tokens():
+    x, d, cu = make('bf16', 1, 400, [100, 0, 150], 2, 4, 64, 128, seed=5)                # 150 tokens behind the last
+    out = torch.full_like(d['v'].contiguous(), 7.0)
+    check_fwd(x, d, cu, 'bf16', out=out)
+    assert (out[:, 250:] == 7.0).all()
+    grads = dict(dq=torch.full_like(d['q'], 7.0), dk=torch.full_like(d['k'], 7.0), dv=torch.full_like(d['v'], 7.0),
+                 dg=torch.full_like(d['g'], 7.0))
+    got = check_bwd(x, d, cu, 'bf16', out=grads)
+    for n in grads:
+        assert got[n].data_ptr() == grads[n].data_ptr() and (got[n][:, 250:] == 7.0).all(), n
+
+
+def test_offsets_beyond_the_buffer_are_cut():
+    x, d, _ = make('bf16', 1, 300, None, 1, 2, 64, 64, h0=False, seed=6)
+    for bad, good in (([0, 50, 400], [0, 50, 300]), ([-5, 120, 2 ** 30], [0, 120, 300])):
+        for cu in (bad, good):
+            d['cu'] = torch.tensor(cu, dtype=torch.int32, device='cuda')
+            o = torch.zeros_like(d['v'])
+            _, ht = G.gdn_linear_fwd(d['q'], d['k'], d['v'], d['g'], cu_seqlens=d['cu'], out=o)
+            g = G.gdn_linear_bwd(d['q'], d['k'], d['v'], d['g'], d['do'], cu_seqlens=d['cu'])
+            if cu is bad:
+                first = o, ht, g
+        torch.cuda.synchronize()
+        assert torch.equal(first[0], o) and torch.equal(first[1], ht)
+        assert all(torch.equal(first[2][n], g[n]) for n in g)
+
+
+def test_offsets_past_32_bits():
+    stride, T = 2 ** 24 - 8, 150
+    say(f'linear attention, tokens {stride} elements apart')
+    x, d, cu = make('bf16', 1, T, None, 1, 1, 64, 64, seed=7)
+    wide = torch.empty((T - 1) * stride + 64, dtype=torch.bfloat16, device='cuda')
+    for n in ('q', 'k', 'v'):
+        view = wide.as_strided((1, T, 1, 64), (T * stride, stride, 64, 1))
+        view.copy_(d[n])
+        d[n] = view
+        if n == 'k':                                                    # one at a time is enough: 5 GB
+            check_fwd(x, d, cu, 'bf16')
+            check_bwd(x, d, cu, 'bf16')
+        d[n] = x[n].to(torch.bfloat16).cuda()
+
+
+def _bits(t):
+    return t.view(torch.int16 if t.dtype is torch.bfloat16 else torch.int32)
+
+
+def test_empty_calls():
+    q, v = torch.zeros(2, 0, 1, 64, device='cuda'), torch.zeros(2, 0, 2, 64, device='cuda')
+    h0 = torch.randn(2, 2, 64, 64, device='cuda')
+    for g in (torch.zeros(2, 0, 2, device='cuda'), torch.zeros(2, device='cuda')):
+        o, ht = G.gdn_linear_fwd(q, q, v, g, h0=h0)
+        assert o.shape == v.shape and torch.equal(ht, h0)
+        got = G.gdn_linear_bwd(q, q, v, g, v, dht=2 * h0, h0=h0)
+        assert torch.equal(got['dh0'], 2 * h0) and (got['dg'] == 0).all() and got['dg'].shape == g.shape
+        none = G.gdn_linear_bwd(q[:0], q[:0], v[:0], g[:0] if g.dim() == 3 else g, v[:0])
+        assert (none['dg'] == 0).all()
+
+
+@pytest.mark.parametrize('gate', ['token', 'head'])
+def test_streams_graphs_and_repeats(gate):
+    """Another stream, and a graph that is replayed, give the bits of a plain call, with eager work between the replays."""
+    x, d, cu = make('bf16', 1, 0, [700, 90, 3, 400], 1, 2, 128, 64, gate=gate, seed=8)
+    args = (d['q'], d['k'], d['v'], d['g'])
+
+    def both():
+        o, ht = G.gdn_linear_fwd(*args, h0=d['h0'], cu_seqlens=d['cu'])
+        g = G.gdn_linear_bwd(*args, d['do'], dht=d['dht'], h0=d['h0'], cu_seqlens=d['cu'])
+        return [o, ht] + [g[n] for n in ('dq', 'dk', 'dv', 'dg', 'dh0')]
+
+    want = [t.clone() for t in both()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = both()
+    side.synchronize()
+    assert all(torch.equal(_bits(a), _bits(b)) for a, b in zip(want, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for i in range(3):
+        new = make('bf16', 1, 0, [700, 90, 3, 400], 1, 2, 128, 64, gate=gate, seed=20 + i)[1]
+        for n in ('q', 'k', 'v', 'g', 'do', 'h0', 'dht'):
+            d[n].copy_(new[n])
+        want = both()
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(_bits(a), _bits(b)) for a, b in zip(want, held))
+
+
+def test_states_handed_on_equal_one_run():
+    """A prompt in two calls, the second from the first one's state; both within the bounds of one."""
+    x, d, _ = make('bf16', 2, 333, None, 1, 2, 128, 128, seed=9)
+    cut, scale = 190, 128 ** -0.5
+    part = lambda n, s: d[n][:, s].contiguous()                         # noqa: E731
+    o1, h1 = G.gdn_linear_fwd(*(part(n, slice(0, cut)) for n in 'qkvg'), h0=d['h0'])
+    o2, h2 = G.gdn_linear_fwd(*(part(n, slice(cut, None)) for n in 'qkvg'), h0=h1)
+    torch.cuda.synchronize()
+    p = positive(x)
+    wo, wh = linear_fwd(x['q'], x['k'], x['v'], x['g'], scale, x['h0'])
+    ao, ah = linear_fwd(p['q'], p['k'], p['v'], x['g'], scale, p['h0'])
+    within('o', torch.cat([o1, o2], 1), wo, ao * (U + FP32) + wo.abs() * U)
+    within('ht', h2, wh, ah * (2 * U * U + FP32))
+
+
+def test_growing_gates_and_long_decays():
+    """Gates above 0 grow the state; a state that decays over many chunks keeps its units."""
+    for level, T in ((0.04, 300), (-0.9, 600), (-3.0, 300)):
+        x, d, cu = make('bf16', 1, T, None, 1, 1, 64, 64, seed=10)
+        x['g'] = torch.full_like(x['g'], level)
+        d['g'] = x['g'].float().cuda()
+        x['g'] = d['g'].double().cpu()
+        say(f'gates of {level}')
+        check_fwd(x, d, cu, 'bf16')
+        check_bwd(x, d, cu, 'bf16')
