@@ -8,12 +8,13 @@
 // in FP32, rounded once. Tokens that no rule names keep their bits.
 //
 // Bound: the logits, read and written once; the rules are sparse but for the mask.
-// A workgroup takes one tile of a row's vocabulary with a word of LDS per token.
-// First the history and the biases mark the words of their tokens in the tile (a
-// count, a flag, the bias's place: integer atomics, so their order does not
-// matter). Then they are walked again: the first to set a token's bit owns it, gathers
-// its logit, and leaves the result in its word. The dense pass is a copy that looks
-// the words up: no division and no branch in it.
+// A workgroup takes one tile of a row's vocabulary with a word of LDS per token, and
+// first sends for its logits. The history and the biases mark the words of their
+// tokens in the tile (times generated, a flag, the number of biases: integer
+// atomics, so their order does not matter). Then each marked token is settled by
+// one thread: that of its bias, or the first to set the token's bit. It gathers the
+// logit and leaves the result in the word. The dense pass looks the words up: no
+// division and no branch in it.
 #include <algorithm>
 
 #include "gdn_device.h"
@@ -23,26 +24,40 @@ namespace gdn {
 
 namespace {
 
-// A word of the tile: 0, or while marked: flag "said" (31), the bias's place plus
-// one (20..30), times generated (0..19); then the result, never 0.
+// A word of the tile: 0, or while marked: flag "said" (31), biases of the token
+// (20..30), times generated (0..19); then the result, never 0.
 constexpr uint32_t kSaid = 0x80000000u;
-constexpr int kPlaceShift = 20;
-constexpr uint32_t kTimes = (1u << kPlaceShift) - 1, kPlace = 0x7FFu;
+constexpr int kBiasShift = 20;
+constexpr uint32_t kTimes = (1u << kBiasShift) - 1, kBiases = 0x7FFu;
 
 template <bool F32> struct Io;
 template <> struct Io<false> {
   using T = uint16_t;
   static constexpr int VEC = 8;
   static __device__ __forceinline__ float wide(T x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }
+  // in both halves, so that a pair's dword takes it as it is; +0 as -0, so that no
+  // result is 0
   static __device__ __forceinline__ uint32_t result(float x) {
     const bf16 b = to_bf16(x);
-    return 0x10000u | __builtin_bit_cast(uint16_t, b);
+    const uint32_t w = __builtin_bit_cast(uint16_t, b);
+    return w ? w << 16 | w : 0x80008000u;
   }
   static __device__ __forceinline__ T take(uint32_t w) { return (T)w; }
+  // a vector's dword d: elements 2 d and 2 d + 1
+  static __device__ __forceinline__ uint32_t looked_up(uint32_t x, const uint32_t* word, int d) {
+    const uint2 w = *reinterpret_cast<const uint2*>(word + 2 * d);
+    return __builtin_amdgcn_perm(w.y ? w.y : x, w.x ? w.x : x, 0x07060100u);
+  }
+  static __device__ __forceinline__ uint32_t masked(uint32_t x, uint32_t m, int d) {
+    const uint32_t lo = __builtin_amdgcn_sbfe((int)m, 2 * d, 1), hi = __builtin_amdgcn_sbfe((int)m, 2 * d + 1, 1);
+    const uint32_t keep = __builtin_amdgcn_perm(hi, lo, 0x07060100u);
+    return (x & keep) | (0xFF80FF80u & ~keep);
+  }
   static constexpr T LOWEST = 0xFF80u, NANV = 0x7FC0u;
 };
 template <> struct Io<true> {
   using T = uint32_t;
+  static constexpr T LOWEST = 0xFF800000u, NANV = 0x7FC00000u;
   static constexpr int VEC = 4;
   static __device__ __forceinline__ float wide(T x) { return __builtin_bit_cast(float, x); }
   // a NaN is made the canonical one, so that no result is 0
@@ -50,7 +65,13 @@ template <> struct Io<true> {
     return (x != x ? 0x7FC00000u : __builtin_bit_cast(uint32_t, x)) ^ 0x7FFFFFFFu;
   }
   static __device__ __forceinline__ T take(uint32_t w) { return w ^ 0x7FFFFFFFu; }
-  static constexpr T LOWEST = 0xFF800000u, NANV = 0x7FC00000u;
+  static __device__ __forceinline__ uint32_t looked_up(uint32_t x, const uint32_t* word, int d) {
+    return word[d] ? take(word[d]) : x;
+  }
+  static __device__ __forceinline__ uint32_t masked(uint32_t x, uint32_t m, int d) {
+    const uint32_t keep = __builtin_amdgcn_sbfe((int)m, d, 1);
+    return (x & keep) | (LOWEST & ~keep);
+  }
 };
 
 template <bool F32, int THREADS>
@@ -58,8 +79,7 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
   using I = Io<F32>;
   using T = typename I::T;
   constexpr int VEC = I::VEC, ES = sizeof(T);
-  typedef T Vec __attribute__((ext_vector_type(VEC)));
-  extern __shared__ __attribute__((aligned(16))) uint32_t word[];   // [tile], [tile / 32] owned, bias ids and values
+  extern __shared__ __attribute__((aligned(16))) uint32_t word[];   // [tile], [tile / 32] bits of settled tokens
   const int row = blockIdx.x / a.tiles, tile = blockIdx.x - row * a.tiles, b = row / a.W, tid = threadIdx.x;
   const T* in = static_cast<const T*>(a.logits) + (int64_t)row * a.in_stride;
   T* out = static_cast<T*>(a.out) + (int64_t)row * a.out_stride;
@@ -78,106 +98,19 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
   }
   const uint32_t low = lo - v0, high = hi - v0;
   const bool marks = a.tokens || a.nb > 0;
-  if (marks) {
-    uint32_t* const owned = word + a.tile;
-    int32_t* const ids = reinterpret_cast<int32_t*>(owned + a.tile / 32);
-    float* const add = reinterpret_cast<float*>(ids + a.nb);
-    for (int i = 4 * tid; i < a.tile + a.tile / 32; i += 4 * THREADS)
-      *reinterpret_cast<u32x4*>(word + i) = u32x4{0, 0, 0, 0};
-    for (int i = tid; i < a.nb; i += THREADS) {
-      ids[i] = a.bias_ids[(int64_t)b * a.nb + i];
-      add[i] = a.bias_vals[(int64_t)b * a.nb + i];
-    }
-    __syncthreads();
-    // the tile's tokens of the history, eight loads at a time
-    const int len = a.tokens ? min(max(a.lens ? a.lens[row] : a.L, 0), a.L) : 0;
-    const int prompt = a.prompt_lens ? a.prompt_lens[b] : 0;
-    const int32_t* tok = a.tokens + (int64_t)row * a.tok_stride;
-    auto history = [&](auto&& f) {
-      constexpr int AHEAD = 8;
-      for (int i0 = tid; i0 < len; i0 += AHEAD * THREADS) {
-        int t[AHEAD];
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) t[u] = i0 + u * THREADS < len ? tok[i0 + u * THREADS] : -1;
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const uint32_t at = (uint32_t)t[u] - (uint32_t)v0;
-          if (t[u] >= 0 && at >= low && at < high) f(i0 + u * THREADS, at);
-        }
-      }
-    };
-    history([&](int i, uint32_t at) {
-      if (i < prompt) atomicOr(&word[at], kSaid);
-      else atomicAdd(&word[at], 1u);
-    });
-    // an id's first entry takes the sum of all that name it, in their order
-    constexpr int MINE = kRulesMaxBias / THREADS;
-    float sum[MINE];
-    uint32_t first[MINE];
-#pragma unroll
-    for (int u = 0; u < MINE; ++u) {
-      const int i = tid + u * THREADS, id = i < a.nb ? ids[i] : -1;
-      const uint32_t at = (uint32_t)id - (uint32_t)v0;
-      sum[u] = 0.f;
-      first[u] = id >= 0 && at >= low && at < high;
-      if (first[u]) {
-        for (int j = 0; j < a.nb; ++j)
-          if (ids[j] == id) {
-            if (j < i) first[u] = 0;
-            sum[u] += add[j];
-          }
-        if (first[u]) atomicAdd(&word[at], (uint32_t)(i + 1) << kPlaceShift);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < MINE; ++u)
-      if (first[u]) add[tid + u * THREADS] = sum[u];
-    __syncthreads();
-    const float rho = a.repetition ? a.repetition[b] : 1.f, pres = a.presence ? a.presence[b] : 0.f;
-    const float freq = a.frequency ? a.frequency[b] : 0.f;
-    auto settle = [&](uint32_t at) {
-      const uint32_t bit = 1u << (at & 31);
-      if (atomicOr(&owned[at >> 5], bit) & bit) return;   // another's
-      const uint32_t w = word[at], times = w & kTimes, place = (w >> kPlaceShift) & kPlace;
-      float x = I::wide(in[(int)at + v0]);
-      if ((w & kSaid) || times) x = x > 0.f ? x / rho : x * rho;
-      if (times) x = (x - freq * (float)times) - pres;
-      if (place) {
-        const float y = add[place - 1];
-        x = y == -__builtin_inff() ? y : x + y;           // a ban is one, whatever the logit
-      }
-      word[at] = I::result(x);
-    };
-    history([&](int, uint32_t at) { settle(at); });
-#pragma unroll
-    for (int u = 0; u < MINE; ++u)
-      if (first[u]) settle((uint32_t)ids[tid + u * THREADS] - (uint32_t)v0);
-    __syncthreads();
-  }
-  // ---- the dense pass
   const uint32_t* bits = mrow >= 0 ? a.mask + (int64_t)mrow * a.words : nullptr;
-  auto one = [&](int v) {
-    T x = in[v];
-    if (marks) {
-      const uint32_t w = word[v - v0];
-      x = w ? I::take(w) : x;
-    }
-    if (bits && !((bits[v >> 5] >> (v & 31)) & 1)) x = I::LOWEST;
-    out[v] = x;
-  };
+  // vectors of the dense pass, a thread's first four loaded ahead of everything else
   constexpr int AHEAD = 4;
-  for (int p0 = tid * VEC; p0 < a.tile; p0 += AHEAD * THREADS * VEC) {
-    Vec x[AHEAD];
-    uint32_t m[AHEAD];
-    bool whole[AHEAD];
+  u32x4 x[AHEAD];
+  uint32_t m[AHEAD];
+  auto whole = [&](int p) { return p < a.tile && v0 + p >= 0 && v0 + p + VEC <= a.V; };
+  auto fetch = [&](int p0) {
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const int p = p0 + u * THREADS * VEC, v = v0 + p;
-      whole[u] = p < a.tile && v >= 0 && v + VEC <= a.V;
       m[u] = ~0u;
-      if (whole[u]) {
-        __builtin_memcpy(&x[u], in + v, sizeof(Vec));     // aligned to an element only
+      if (whole(p)) {
+        __builtin_memcpy(&x[u], in + v, 16);     // aligned to an element only
         if (bits) {
           const int at = v & 31;
           const uint32_t w0 = bits[v >> 5], w1 = at + VEC > 32 ? bits[(v >> 5) + 1] : 0u;
@@ -185,23 +118,159 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
         }
       }
     }
+  };
+  fetch(tid * VEC);
+  if (marks) {
+    uint32_t* const owned = word + a.tile;
+    // the history, HELD tokens a thread at a time; the first of them stay in registers
+    constexpr int HELD = 8;
+    const int len = a.tokens ? min(max(a.lens ? a.lens[row] : a.L, 0), a.L) : 0;
+    const int prompt = a.prompt_lens ? a.prompt_lens[b] : 0;
+    const int32_t* tok = a.tokens + (int64_t)row * a.tok_stride;
+    auto load = [&](int i0, uint32_t (&at)[HELD]) {       // the place in the tile, or ~0
+      int t[HELD];
+#pragma unroll
+      for (int u = 0; u < HELD; ++u) t[u] = i0 + u * THREADS < len ? tok[i0 + u * THREADS] : -1;
+#pragma unroll
+      for (int u = 0; u < HELD; ++u) {
+        at[u] = (uint32_t)t[u] - (uint32_t)v0;
+        if (t[u] < 0 || at[u] < low || at[u] >= high) at[u] = ~0u;
+      }
+    };
+    uint32_t held[HELD], more[HELD];
+    load(tid, held);
+    // the biases
+    constexpr int MINE = kRulesMaxBias / THREADS;
+    uint32_t spot[MINE];
+    float add[MINE];
+#pragma unroll
+    for (int u = 0; u < MINE; ++u) {
+      const int i = tid + u * THREADS;
+      spot[u] = ~0u;
+      add[u] = 0.f;
+      if (i < a.nb) {
+        const int id = a.bias_ids[(int64_t)b * a.nb + i];
+        const uint32_t at = (uint32_t)id - (uint32_t)v0;
+        if (id >= 0 && at >= low && at < high) spot[u] = at;
+        add[u] = a.bias_vals[(int64_t)b * a.nb + i];
+      }
+    }
+    for (int i = 4 * tid; i < a.tile + a.tile / 32; i += 4 * THREADS)
+      *reinterpret_cast<u32x4*>(word + i) = u32x4{0, 0, 0, 0};
+    __syncthreads();
+    auto mark = [&](int i0, const uint32_t (&at)[HELD]) {
+#pragma unroll
+      for (int u = 0; u < HELD; ++u)
+        if (at[u] != ~0u) {
+          if (i0 + u * THREADS < prompt) atomicOr(&word[at[u]], kSaid);
+          else atomicAdd(&word[at[u]], 1u);
+        }
+    };
+    mark(tid, held);
+    for (int i0 = tid + HELD * THREADS; i0 < len; i0 += HELD * THREADS) {
+      load(i0, more);
+      mark(i0, more);
+    }
+#pragma unroll
+    for (int u = 0; u < MINE; ++u)
+      if (spot[u] != ~0u) atomicAdd(&word[spot[u]], 1u << kBiasShift);
+    __syncthreads();
+    const float rho = a.repetition ? a.repetition[b] : 1.f, pres = a.presence ? a.presence[b] : 0.f;
+    const float freq = a.frequency ? a.frequency[b] : 0.f;
+    auto penal = [&](uint32_t w, float y) {
+      const uint32_t times = w & kTimes;
+      if ((w & kSaid) || times) y = y > 0.f ? y / rho : y * rho;
+      if (times) y = (y - freq * (float)times) - pres;
+      return y;
+    };
+    // A token with biases is settled by its first bias's thread. Where it has several
+    // (seldom), the wave looks the list through for that one and their sum, in their
+    // order.
+    float with[MINE];
+    const int lane = __lane_id();
+#pragma unroll
+    for (int u = 0; u < MINE; ++u) {
+      const uint32_t w = spot[u] == ~0u ? 0u : word[spot[u]];
+      for (uint64_t todo = __ballot(((w >> kBiasShift) & kBiases) > 1); todo; todo &= todo - 1) {
+        const int src = __builtin_ctzll(todo), id = __builtin_amdgcn_readlane((int)spot[u], src) + v0;
+        float sum = 0.f;
+        int first = -1;
+        for (int j0 = 0; j0 < a.nb; j0 += WAVE) {
+          const int j = j0 + lane;
+          const bool hit = j < a.nb && a.bias_ids[(int64_t)b * a.nb + min(j, a.nb - 1)] == id;
+          const float y = hit ? a.bias_vals[(int64_t)b * a.nb + j] : 0.f;
+          for (uint64_t hits = __ballot(hit); hits; hits &= hits - 1) {
+            const int l = __builtin_ctzll(hits);
+            sum += read_lane(y, l);
+            if (first < 0) first = j0 + l;
+          }
+        }
+        if (lane == src) {
+          add[u] = sum;
+          if (first != tid + u * THREADS) spot[u] = ~0u;
+        }
+      }
+      // a ban is one, whatever the logit
+      if (spot[u] != ~0u) with[u] = add[u] == -__builtin_inff() ? add[u] : penal(w, I::wide(in[(int)spot[u] + v0])) + add[u];
+    }
+    auto settle = [&](const uint32_t (&at)[HELD]) {
+      uint32_t w[HELD], old[HELD];
+      T y[HELD];
+#pragma unroll
+      for (int u = 0; u < HELD; ++u)
+        if (at[u] != ~0u) {
+          w[u] = word[at[u]];
+          old[u] = atomicOr(&owned[at[u] >> 5], 1u << (at[u] & 31));
+        }
+      // not one with a bias, nor one that another has taken (whose word may hold
+      // its result by now); the gathers of the rest are in flight together
+      bool mine[HELD];
+#pragma unroll
+      for (int u = 0; u < HELD; ++u) {
+        mine[u] = at[u] != ~0u && !((old[u] >> (at[u] & 31)) & 1) && !((w[u] >> kBiasShift) & kBiases);
+        if (mine[u]) y[u] = in[(int)at[u] + v0];
+      }
+#pragma unroll
+      for (int u = 0; u < HELD; ++u)
+        if (mine[u]) word[at[u]] = I::result(penal(w[u], I::wide(y[u])));
+    };
+    settle(held);
+    for (int i0 = tid + HELD * THREADS; i0 < len; i0 += HELD * THREADS) {
+      load(i0, more);
+      settle(more);
+    }
+    __syncthreads();                                      // the marks of biased tokens are read
+#pragma unroll
+    for (int u = 0; u < MINE; ++u)
+      if (spot[u] != ~0u) word[spot[u]] = I::result(with[u]);
+    __syncthreads();
+  }
+  // ---- the dense pass
+  auto one = [&](int v) {
+    T y = in[v];
+    if (marks) {
+      const uint32_t w = word[v - v0];
+      y = w ? I::take(w) : y;
+    }
+    if (bits && !((bits[v >> 5] >> (v & 31)) & 1)) y = I::LOWEST;
+    out[v] = y;
+  };
+  for (int p0 = tid * VEC; p0 < a.tile; p0 += AHEAD * THREADS * VEC) {
+    if (p0 != tid * VEC) fetch(p0);
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const int p = p0 + u * THREADS * VEC, v = v0 + p;
-      if (whole[u]) {
+      if (whole(p)) {
+        u32x4 y = x[u];
         if (marks) {
 #pragma unroll
-          for (int h = 0; h < VEC / 4; ++h) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(word + p + 4 * h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[u][4 * h + e] = w[e] ? I::take(w[e]) : x[u][4 * h + e];
-          }
+          for (int d = 0; d < 4; ++d) y[d] = I::looked_up(y[d], word + p, d);
         }
         if (bits) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) x[u][e] = (m[u] >> e) & 1 ? x[u][e] : I::LOWEST;
+          for (int d = 0; d < 4; ++d) y[d] = I::masked(y[d], m[u], d);
         }
-        *reinterpret_cast<Vec*>(out + v) = x[u];
+        *reinterpret_cast<u32x4*>(out + v) = y;
       } else if (p < a.tile) {
         for (int e = max(v, lo); e < min(v + VEC, hi); ++e) one(e);
       }
@@ -211,7 +280,7 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
 
 template <bool F32, int THREADS>
 void launch(const RulesArgs& a, hipStream_t s) {
-  const size_t lds = a.tokens || a.nb > 0 ? (size_t)a.tile * 4 + a.tile / 8 + (size_t)a.nb * 8 : 0;
+  const size_t lds = a.tokens || a.nb > 0 ? (size_t)a.tile * 4 + a.tile / 8 : 0;
   rules_kernel<F32, THREADS><<<dim3((unsigned)(a.B * a.W * a.tiles)), THREADS, lds, s>>>(a);
 }
 
