@@ -11,10 +11,12 @@
 // A workgroup takes one tile of a row's vocabulary with a word of LDS per token, and
 // first sends for its logits. The history and the biases mark the words of their
 // tokens in the tile (times generated, a flag, the number of biases: integer
-// atomics, so their order does not matter). Then each marked token is settled by
-// one thread: that of its bias, or the first to set the token's bit. It gathers the
-// logit and leaves the result in the word. The dense pass looks the words up: no
-// division and no branch in it.
+// atomics, so their order does not matter), and whoever marks one first puts it in
+// a list. Then each listed token, and each with a bias, is settled by one thread, which
+// gathers its logit and leaves the result in the word: by list, because the hits of
+// a history are spread thinly over its lanes (settled where they were found they
+// took half of the kernel's vector instructions). The dense pass looks the words up:
+// no division and no branch in it.
 #include <algorithm>
 
 #include "gdn_device.h"
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
   using I = Io<F32>;
   using T = typename I::T;
   constexpr int VEC = I::VEC, ES = sizeof(T);
-  extern __shared__ __attribute__((aligned(16))) uint32_t word[];   // [tile], [tile / 32] bits of settled tokens
+  extern __shared__ __attribute__((aligned(16))) uint32_t word[];   // [tile], number listed, the list
   const int row = blockIdx.x / a.tiles, tile = blockIdx.x - row * a.tiles, b = row / a.W, tid = threadIdx.x;
   const T* in = static_cast<const T*>(a.logits) + (int64_t)row * a.in_stride;
   T* out = static_cast<T*>(a.out) + (int64_t)row * a.out_stride;
@@ -121,7 +123,8 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
   };
   fetch(tid * VEC);
   if (marks) {
-    uint32_t* const owned = word + a.tile;
+    uint32_t* const listed = word + a.tile;
+    uint16_t* const list = reinterpret_cast<uint16_t*>(listed + 4);
     // the history, HELD tokens a thread at a time; the first of them stay in registers
     constexpr int HELD = 8;
     const int len = a.tokens ? min(max(a.lens ? a.lens[row] : a.L, 0), a.L) : 0;
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
         if (t[u] < 0 || at[u] < low || at[u] >= high) at[u] = ~0u;
       }
     };
-    uint32_t held[HELD], more[HELD];
+    uint32_t held[HELD];
     load(tid, held);
     // the biases
     constexpr int MINE = kRulesMaxBias / THREADS;
@@ -155,22 +158,25 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
         add[u] = a.bias_vals[(int64_t)b * a.nb + i];
       }
     }
-    for (int i = 4 * tid; i < a.tile + a.tile / 32; i += 4 * THREADS)
-      *reinterpret_cast<u32x4*>(word + i) = u32x4{0, 0, 0, 0};
+    for (int i = 4 * tid; i < a.tile + 4; i += 4 * THREADS) *reinterpret_cast<u32x4*>(word + i) = u32x4{0, 0, 0, 0};
     __syncthreads();
     auto mark = [&](int i0, const uint32_t (&at)[HELD]) {
+      uint32_t old[HELD];
 #pragma unroll
       for (int u = 0; u < HELD; ++u)
-        if (at[u] != ~0u) {
-          if (i0 + u * THREADS < prompt) atomicOr(&word[at[u]], kSaid);
-          else atomicAdd(&word[at[u]], 1u);
-        }
+        if (at[u] != ~0u)
+          old[u] = i0 + u * THREADS < prompt ? atomicOr(&word[at[u]], kSaid) : atomicAdd(&word[at[u]], 1u);
+#pragma unroll
+      for (int u = 0; u < HELD; ++u)
+        if (at[u] != ~0u && old[u] == 0) list[atomicAdd(listed, 1u)] = (uint16_t)at[u];
     };
     mark(tid, held);
     for (int i0 = tid + HELD * THREADS; i0 < len; i0 += HELD * THREADS) {
-      load(i0, more);
-      mark(i0, more);
+      load(i0, held);
+      mark(i0, held);
     }
+    // not listed: their threads are known. A token of the history that a bias marks
+    // first is not listed either, and need not be
 #pragma unroll
     for (int u = 0; u < MINE; ++u)
       if (spot[u] != ~0u) atomicAdd(&word[spot[u]], 1u << kBiasShift);
@@ -213,31 +219,10 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
       // a ban is one, whatever the logit
       if (spot[u] != ~0u) with[u] = add[u] == -__builtin_inff() ? add[u] : penal(w, I::wide(in[(int)spot[u] + v0])) + add[u];
     }
-    auto settle = [&](const uint32_t (&at)[HELD]) {
-      uint32_t w[HELD], old[HELD];
-      T y[HELD];
-#pragma unroll
-      for (int u = 0; u < HELD; ++u)
-        if (at[u] != ~0u) {
-          w[u] = word[at[u]];
-          old[u] = atomicOr(&owned[at[u] >> 5], 1u << (at[u] & 31));
-        }
-      // not one with a bias, nor one that another has taken (whose word may hold
-      // its result by now); the gathers of the rest are in flight together
-      bool mine[HELD];
-#pragma unroll
-      for (int u = 0; u < HELD; ++u) {
-        mine[u] = at[u] != ~0u && !((old[u] >> (at[u] & 31)) & 1) && !((w[u] >> kBiasShift) & kBiases);
-        if (mine[u]) y[u] = in[(int)at[u] + v0];
-      }
-#pragma unroll
-      for (int u = 0; u < HELD; ++u)
-        if (mine[u]) word[at[u]] = I::result(penal(w[u], I::wide(y[u])));
-    };
-    settle(held);
-    for (int i0 = tid + HELD * THREADS; i0 < len; i0 += HELD * THREADS) {
-      load(i0, more);
-      settle(more);
+    const int count = *listed;
+    for (int i = tid; i < count; i += THREADS) {
+      const uint32_t at = list[i], w = word[at];
+      if (!((w >> kBiasShift) & kBiases)) word[at] = I::result(penal(w, I::wide(in[(int)at + v0])));
     }
     __syncthreads();                                      // the marks of biased tokens are read
 #pragma unroll
@@ -280,7 +265,8 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(RulesArgs a) {
 
 template <bool F32, int THREADS>
 void launch(const RulesArgs& a, hipStream_t s) {
-  const size_t lds = a.tokens || a.nb > 0 ? (size_t)a.tile * 4 + a.tile / 8 : 0;
+  const size_t list = a.tokens ? (size_t)std::min(a.L, a.tile) * 2 : 0;
+  const size_t lds = a.tokens || a.nb > 0 ? (size_t)a.tile * 4 + 16 + list : 0;
   rules_kernel<F32, THREADS><<<dim3((unsigned)(a.B * a.W * a.tiles)), THREADS, lds, s>>>(a);
 }
 
