@@ -432,7 +432,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   constexpr bool REV = ROLE == kDk || ROLE == kDv || ROLE == kStateRev, STATE = W::STATE;
   constexpr bool TURNED = ROLE == kDq || ROLE == kDk;      // the state is held transposed
   // bf16 parts of the state where an output reads it, and of what it takes up
-  constexpr int NIN = ES == 2 && TURNED ? 3 : 1, NADD = ES == 2 && ROLE != kDv ? 3 : 1;
+  constexpr int NIN = ES == 2 && TURNED ? 3 : 1, NADD = ES == 2 ? (ROLE == kDv ? 2 : 3) : 1;
   constexpr int STEP = 4 * CW;
 
   Segment seg;
@@ -915,33 +915,54 @@ __global__ void __launch_bounds__(kThreads) lin_dg_kernel(LinearArgs a, int unit
     if (a.ws_dgsum && lane == 0) a.ws_dgsum[unit] = 0.0;
     return;
   }
-  // Tokens backwards, 64 at a time, lane 63 the first of them: a prefix sum over
-  // lanes is a suffix sum over tokens. Chunks need no care of their own: pairs
-  // within one add up to nothing before it.
+  // With E = <dS, S> after a chunk, x = q . dq and y = (pairs' sums) - k . dk:
+  //   dg_t = E + sum over s >= t of the chunk of (x_s + y_s)
+  //   F = e^gam_n <dS, S before> = E + sum y,  E before = F + sum x
+  // as the pairs' sums add up to nothing over a chunk. Where the chunk's decay
+  // is below 2^-30, F is nothing beside either sum, and is set so: carried on as
+  // the difference of two of them, it would be their roundings, which no decay
+  // takes away (2.4e-6 of dg after 16 chunks, instead of 1e-6).
+  // Two chunks at a time, tokens backwards over the lanes of a half: a prefix sum
+  // over lanes is a suffix sum over tokens.
+  static_assert(2 * C == WAVE, "a chunk per half");
   constexpr int AHEAD = 4;
-  const int lo = seg.first * C, hi = min(lo + seg.count * C, seg.len);
+  const int half = lane >> 5, back = C - 1 - (lane & 31);
   double end = a.ws_end[unit], sum = 0.0;
-  for (int t0 = hi - 1; t0 >= lo; t0 -= AHEAD * WAVE) {
+  for (int c0 = seg.first + seg.count - 1; c0 >= seg.first; c0 -= 2 * AHEAD) {
     float x[AHEAD], y[AHEAD], g[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      const int t = t0 - u * WAVE - lane;
-      const int64_t at = ((int64_t)(seg.cslot + t / C) * a.Hv + h) * C + t % C;
-      x[u] = t >= lo ? a.ws_qdq[at] : 0.f;
-      y[u] = t >= lo ? a.ws_kdk[at] : 0.f;
-      g[u] = t >= lo ? a.g[(int64_t)(seg.bos + t) * a.gs + h] : 0.f;
+      const int c = c0 - 2 * u - half, t = c * C + back;
+      const bool here = c >= seg.first && t < seg.len;
+      const int64_t at = ((int64_t)(seg.cslot + c) * a.Hv + h) * C + back;
+      x[u] = here ? a.ws_qdq[at] : 0.f;
+      y[u] = here ? a.ws_kdk[at] : 0.f;
+      g[u] = here ? a.g[(int64_t)(seg.bos + t) * a.gs + h] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      const int t = t0 - u * WAVE - lane;
-      const double s = wave_incl_scan64(static_cast<double>(x[u]) + static_cast<double>(y[u]));
+      const int c = c0 - 2 * u - half, t = c * C + back;
+      const bool here = c >= seg.first && t < seg.len;
+      const double sx = wave_incl_scan64(x[u]), sy = wave_incl_scan64(y[u]);
+      const double sg = wave_incl_scan64(g[u] < kResetGate ? kResetGate : g[u]);
+      double e[2];
+      double at = end, bx = 0.0, by = 0.0, bg = 0.0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const double tx = read_lane64(sx, 32 * i + 31), ty = read_lane64(sy, 32 * i + 31), tg = read_lane64(sg, 32 * i + 31);
+        e[i] = at - bx - by;                              // the scans run on over both halves
+        at = (tg - bg < -20.8 ? 0.0 : at + (ty - by)) + (tx - bx);
+        bx = tx;
+        by = ty;
+        bg = tg;
+      }
+      end = at;
       // where exp(g) is zero in FP32 nothing reaches over the token
-      const double d = g[u] < -88.f ? 0.0 : end + s;
-      if (t >= lo) {
+      const double d = g[u] < -88.f ? 0.0 : (half ? e[1] : e[0]) + (sx + sy);
+      if (here) {
         if (a.ws_dgsum) sum += d;
         else a.dg[(int64_t)(seg.bos + t) * a.Hv + h] = static_cast<float>(d);
       }
-      end += read_lane64(s, WAVE - 1);
     }
   }
   if (a.ws_dgsum) {
