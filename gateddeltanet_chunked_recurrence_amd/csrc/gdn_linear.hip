@@ -414,7 +414,7 @@ struct WalkLds {
   static constexpr int K = Z + Rows<T, DO>::BYTES, P = K + (ROLE == kDk ? Rows<T, DO>::BYTES : 0);
   static constexpr int G = P + (STATE ? 0 : C * C * (int)sizeof(T));
   static constexpr int SUMS = G + 2 * (int)((sizeof(Gates<C>) + 15) / 16 * 16);
-  static constexpr int BYTES = SUMS + (ROLE == kDk ? 3 : ROLE == kDq ? 1 : 0) * kWaves * C * 4;
+  static constexpr int BYTES = SUMS + (ROLE == kDk ? 9 : ROLE == kDq ? 4 : 0) * kWaves * C * 4;
 };
 
 // One walk of a workgroup: segment `slot`, value head h, columns 64 CW slab ...
@@ -451,7 +451,10 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   char* const sP = lds + W::P;
   // not an array of two pointers: loads through one would be flat, and wait for every load in flight
   auto gates = [&](int i) -> Gates<C>& { return *reinterpret_cast<Gates<C>*>(lds + W::G + (i & 1) * ((W::SUMS - W::G) / 2)); };
-  float* const sums = reinterpret_cast<float*>(lds + W::SUMS);
+  // dots of rows and column sums, by wave and lane group; row sums, by wave
+  float* const dots = reinterpret_cast<float*>(lds + W::SUMS);
+  float* const cols = dots + 4 * kWaves * C;
+  float* const sums = cols + (ROLE == kDk ? 4 * kWaves * C : 0);
   // this lane's places in the tiles
   const int xrow = Tile<T, DC>::at(r16, 8 * grp), ycol = L::template colbase<DC>(8, r16, grp);
   const int zrow = Tile<T, DO>::at(r16, 8 * grp);
@@ -515,6 +518,10 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     if (lane < C) gate = lane < n ? a.g[(tok + lane) * a.gs + h] : 0.f;
     if constexpr (!STATE) rx.load(x.p + tok * x.stride, (uint32_t)x.stride, n);
     ry.load(y.p + tok * y.stride, (uint32_t)y.stride, n);
+  };
+  auto fetch_late = [&](int c) {
+    const int t0 = c * C, n = min(C, seg.len - t0);
+    const int64_t tok = seg.bos + t0;
     rz.load(z.p + tok * z.stride, (uint32_t)z.stride, n);
     if constexpr (ROLE == kDk) rk.load(w.p + tok * w.stride, (uint32_t)w.stride, n);
   };
@@ -526,10 +533,25 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     if constexpr (STATE) lin_gates_far<C, REV>(gates(i), gate, a.scale, far);
     else lin_gates<C, REV>(gates(i), gate, a.scale, i ? gates(i + 1).unit : 1.f);
   };
+  // the rows that q . dq needs, from memory, a chunk ahead too
+  Four rows[NQ][CW];
+  auto fetch_rows = [&](int c) {
+    const int64_t tok = seg.bos + c * C;
+    const auto rsrc = rows_rsrc(w.p + tok * w.stride, (uint32_t)w.stride, min(C, seg.len - c * C), a.Dk * ES);
+    const int l = fresh_lane();
+#pragma unroll
+    for (int t = 0; t < NQ; ++t)
+#pragma unroll
+      for (int ct = 0; ct < CW; ++ct)
+        rows[t][ct] = L::load4(rsrc, (16 * t + (l & 15)) * (uint32_t)w.stride +
+                                         (uint32_t)(16 * CW * wave + STEP * (l >> 4) + 4 * ct) * ES);
+  };
   int count = seg.count;
   if constexpr (STATE) count = lin_reach<C, BACK>(a, seg, h, lds + W::Y, far_total);
   if (count > 0) {
     fetch(chunk_of(0));
+    fetch_late(chunk_of(0));
+    if constexpr (ROLE == kDq) fetch_rows(chunk_of(0));
     if (wave == 0) put_gates(0);
   }
   for (int i = 0; i < count; ++i) {
@@ -542,18 +564,6 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     if constexpr (ROLE == kDk) rk.store(sK);
     lds_barrier();
     const Gates<C>& G = gates(i);
-    // the rows that q . dq needs, ahead of the next chunk's
-    Four rows[NQ][CW];
-    if constexpr (ROLE == kDq) {
-      const int l = fresh_lane();
-      const auto rsrc = rows_rsrc(w.p + tok * w.stride, (uint32_t)w.stride, n, a.Dk * ES);
-#pragma unroll
-      for (int t = 0; t < NQ; ++t)
-#pragma unroll
-        for (int ct = 0; ct < CW; ++ct)
-          rows[t][ct] = L::load4(rsrc, (16 * t + (l & 15)) * (uint32_t)w.stride +
-                                           (uint32_t)(16 * CW * wave + STEP * (l >> 4) + 4 * ct) * ES);
-    }
     if (i + 1 < count) fetch(chunk_of(i + 1));
 
     f32x4 O[CW][NQ];
@@ -569,24 +579,25 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
           const int kt = kt0 + u;
-          const bool need = REV ? kt >= qt : kt <= qt;
           f32x4 p = zero4();
-          float rsum[4] = {0.f, 0.f, 0.f, 0.f};
-          if (need) {
+          {
 #pragma unroll
             for (int kb = 0; kb < DC / 32; ++kb)
               p = L::mma(L::template row<DC>(sY, xrow, kt, kb), xf[kb], p);
             const f32x4 khi = *reinterpret_cast<const f32x4*>(&G.hi[16 * kt + 4 * grp]);
             const f32x4 klo = *reinterpret_cast<const f32x4*>(&G.lo[16 * kt + 4 * grp]);
-            // the tile on the diagonal is cut: weight 0 where the exponent is -inf
+            // pairs that are not taken have weight 0, their exponent -inf (a tile of
+            // them is computed like the others: no branch, so that the chain of
+            // products is worked on beside the state's part)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float diff = (qhi - khi[r]) + (qlo - klo[r]);
-              const bool cut = kt == qt && (REV ? 4 * grp + r < r16 : 4 * grp + r > r16);
-              p[r] *= a.scale * fexp2(cut ? -__builtin_inff() : REV ? -diff : diff);
+              const int later = 16 * (kt - qt) + 4 * grp + r - r16;
+              p[r] *= a.scale * fexp2((REV ? later < 0 : later > 0) ? -__builtin_inff() : REV ? -diff : diff);
             }
             if constexpr (ROLE == kDk) {
               // the other product of the pair, q_i . k_j
+              float rsum[4];
               f32x4 m = zero4();
 #pragma unroll
               for (int kb = 0; kb < DO / 32; ++kb)
@@ -603,22 +614,16 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
                 t += dpp_f<0x140>(t);
                 rsum[r] = t;
               }
+              if (r16 == 0)
+                *reinterpret_cast<f32x4*>(sums + wave * C + 16 * kt + 4 * grp) = f32x4{rsum[0], rsum[1], rsum[2], rsum[3]};
             }
           }
-          // a block of 32 keys is read whole: its masked half holds zeros
-          if (REV ? (kt | 1) >= qt : (kt & ~1) <= qt) L::put4(reinterpret_cast<T*>(sP + 16 * qt * Tile<T, C>::RB + (pput ^ (16 * kt * ES))), p);
-          if constexpr (ROLE == kDk) {
-            if (r16 == 0)
-              *reinterpret_cast<f32x4*>(sums + wave * C + 16 * kt + 4 * grp) = f32x4{rsum[0], rsum[1], rsum[2], rsum[3]};
-          }
+          L::put4(reinterpret_cast<T*>(sP + 16 * qt * Tile<T, C>::RB + (pput ^ (16 * kt * ES))), p);
         }
         if constexpr (ROLE == kDk) {
-          csum += __shfl_xor(csum, 16, WAVE);
-          csum += __shfl_xor(csum, 32, WAVE);
-          if (grp == 0) sums[(kWaves + wave) * C + 16 * qt + r16] = csum;
+          cols[(4 * wave + grp) * C + 16 * qt + r16] = csum;
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
       // ---- the state's part: out = factor x S
 #pragma unroll
       for (int ct = 0; ct < CW; ++ct)
@@ -656,14 +661,17 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
             for (int r = 0; r < 4; ++r) dot = fmaf(O[ct][t][r], m[r], dot);
           }
-          dot += __shfl_xor(dot, 16, WAVE);
-          dot += __shfl_xor(dot, 32, WAVE);
-          if (grp == 0) sums[((ROLE == kDk ? 2 * kWaves : 0) + wave) * C + row] = dot;
+          dots[(4 * wave + grp) * C + row] = dot;
         }
+      }
+      if constexpr (ROLE == kDq) {
+        if (i + 1 < count) fetch_rows(chunk_of(i + 1));
       }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
+    // half of the loads here: all at once, the waves queue for 900 cycles to send them
+    if (i + 1 < count) fetch_late(chunk_of(i + 1));
     // ---- Z as an operand over tokens
     Frag zf[C / 32][CW];
 #pragma unroll
@@ -722,15 +730,17 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
           const int t = threadIdx.x;
           float s = 0.f;
 #pragma unroll
-          for (int u = 0; u < kWaves; ++u) s += sums[((ROLE == kDk ? 2 * kWaves : 0) + u) * C + t];
+          for (int u = 0; u < 4 * kWaves; ++u) s += dots[u * C + t];
           if constexpr (ROLE == kDk) {
             const int tile = t >> 4;
-            float rows = 0.f, cols = 0.f;
+            float r = 0.f, k = 0.f;
 #pragma unroll
-            for (int u = 0; u < NQ; ++u) rows += sums[(tile / NT * NQ + u) * C + t];
+            for (int u = 0; u < NQ; ++u) r += sums[(tile / NT * NQ + u) * C + t];
 #pragma unroll
-            for (int u = 0; u < kWaves / NQ; ++u) cols += sums[(kWaves + u * NQ + tile) * C + t];
-            s = (rows - cols) - s;
+            for (int u = 0; u < kWaves / NQ; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) k += cols[(4 * (u * NQ + tile) + e) * C + t];
+            s = (r - k) - s;
           }
           (ROLE == kDk ? a.ws_kdk : a.ws_qdq)[((int64_t)(seg.cslot + c) * a.Hv + h) * C + t] = s;
         }
@@ -814,9 +824,9 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     }
     dot = wave_sum(dot);
     lds_barrier();
-    if (lane == 0) sums[wave] = dot;
+    if (lane == 0) dots[wave] = dot;
     lds_barrier();
-    if (threadIdx.x == 0) a.ws_end[slot_head] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    if (threadIdx.x == 0) a.ws_end[slot_head] = (dots[0] + dots[1]) + (dots[2] + dots[3]);
   }
 }
 
@@ -832,34 +842,38 @@ constexpr int role_lds() {
   using R = RoleDims<DK, DV, ROLE>;
   return WalkLds<T, R::DC, R::CW, ROLE>::BYTES;
 }
-template <class T, int DK, int DV, int ROLE>
-__device__ __forceinline__ void lin_role(const LinearArgs& a, int unit, char* lds) {
-  using R = RoleDims<DK, DV, ROLE>;
-  const int per = a.Hv * R::SLABS, slot = unit / per, rest = unit - slot * per;
-  if (slot < a.slots) lin_walk<T, R::DC, R::CW, ROLE>(a, slot, rest / R::SLABS, rest % R::SLABS, lds);
-}
 // Consecutive units, which share q and k, on one XCD (workgroups go round the eight).
-__device__ __forceinline__ int lin_unit() { return (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3); }
+template <class T, int DK, int DV, int ROLE>
+__device__ __forceinline__ void lin_role(const LinearArgs& a, char* lds) {
+  using R = RoleDims<DK, DV, ROLE>;
+  const int per = a.Hv * R::SLABS, units = a.slots * per, share = (units + 7) >> 3;
+  const int at = blockIdx.x >> 3, unit = (blockIdx.x & 7) * share + at;
+  if (at >= share || unit >= units) return;
+  const int slot = unit / per, rest = unit - slot * per;
+  lin_walk<T, R::DC, R::CW, ROLE>(a, slot, rest / R::SLABS, rest % R::SLABS, lds);
+}
 
 template <class T, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 3) lin_fwd_kernel(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  lin_role<T, DK, DV, kFwd>(a, lin_unit(), lds);
+  lin_role<T, DK, DV, kFwd>(a, lds);
 }
 // blockIdx.y: what segments add to the state, or to its gradient.
 template <class T, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 3) lin_states_kernel(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  if (blockIdx.y == 0) lin_role<T, DK, DV, kStateFwd>(a, lin_unit(), lds);
-  else lin_role<T, DK, DV, kStateRev>(a, lin_unit(), lds);
+  if (blockIdx.y == 0) lin_role<T, DK, DV, kStateFwd>(a, lds);
+  else lin_role<T, DK, DV, kStateRev>(a, lds);
 }
-// blockIdx.y: the walks of dk, dq and dv, the longest first.
+// blockIdx.y: the walks of dq, dk and dv, the longest first (with dk before dq 1 to 3%
+// more; all three interleaved, so that they share what they read, a fifth more: then
+// short and long ones pair up on the CUs).
 template <class T, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, DV == 256 ? 1 : 2) lin_bwd_kernel(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  if (blockIdx.y == 0) lin_role<T, DK, DV, kDk>(a, lin_unit(), lds);
-  else if (blockIdx.y == 1) lin_role<T, DK, DV, kDq>(a, lin_unit(), lds);
-  else lin_role<T, DK, DV, kDv>(a, lin_unit(), lds);
+  if (blockIdx.y == 0) lin_role<T, DK, DV, kDq>(a, lds);
+  else if (blockIdx.y == 1) lin_role<T, DK, DV, kDk>(a, lds);
+  else lin_role<T, DK, DV, kDv>(a, lds);
 }
 
 // Folds what each segment adds into the state before it (REV: the gradient of
