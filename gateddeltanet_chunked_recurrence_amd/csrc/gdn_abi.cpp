@@ -896,8 +896,8 @@ gdn_status check_linear(const gdn_linear_args* a, const char* what) {
 }
 
 gdn::LinearPlan plan_linear(const gdn_linear_args* a, bool bwd) {
-  return gdn::linear_plan(a->num_seqs, a->T, (int64_t)a->B * a->T, a->cu_seqlens != nullptr, a->Hv, a->Dv,
-                          a->io_dtype == GDN_F32, bwd);
+  return gdn::linear_plan(a->num_seqs, a->T, (int64_t)a->B * a->T, a->cu_seqlens != nullptr, a->Hv, a->Dk,
+                          a->Dv, bwd);
 }
 
 // Offsets of the workspace's parts.

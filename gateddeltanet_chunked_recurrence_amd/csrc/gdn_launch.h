@@ -386,7 +386,7 @@ struct LinearPlan {
   bool segmented;             // some sequence may have several segments
   int64_t slots, chunk_slots;
 };
-LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dv, bool f32, bool bwd);
+LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dk, int Dv, bool bwd);
 hipError_t launch_linear_fwd(const LinearArgs& a, bool f32, hipStream_t s);
 hipError_t launch_linear_bwd(const LinearArgs& a, bool f32, hipStream_t s);
 

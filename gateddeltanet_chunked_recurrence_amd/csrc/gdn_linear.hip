@@ -112,7 +112,6 @@ struct Tile {
 
 template <class T> struct Lin;
 template <> struct Lin<bf16> {
-  static constexpr int C = 32;
   using Frag = bf16x8;
   static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) { return mfma(a, b, c); }
   // elements 32 kb + 8 g .. + 7 of row 16 t + r16; `base`: Tile::at(r16, 8 g)
@@ -176,6 +175,9 @@ template <> struct Lin<bf16> {
   static __device__ __forceinline__ void put4(bf16* p, const f32x4& x) {
     *reinterpret_cast<bf16x4*>(p) = bf16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
   }
+  static __device__ __forceinline__ f32x4 rounded4(const f32x4& x) {
+    return f32x4{from_bf16(to_bf16(x[0])), from_bf16(to_bf16(x[1])), from_bf16(to_bf16(x[2])), from_bf16(to_bf16(x[3]))};
+  }
   using Four = bf16x4;
   static __device__ __forceinline__ f32x4 wide(const Four& v) {
     return f32x4{from_bf16(v[0]), from_bf16(v[1]), from_bf16(v[2]), from_bf16(v[3])};
@@ -187,7 +189,6 @@ template <> struct Lin<bf16> {
   }
 };
 template <> struct Lin<float> {
-  static constexpr int C = 32;
   struct Frag { f32x4 a, b; };
   static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
 #pragma unroll
@@ -229,6 +230,7 @@ template <> struct Lin<float> {
     t1 = x.b * b1;
   }
   static __device__ __forceinline__ void put4(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
+  static __device__ __forceinline__ f32x4 rounded4(const f32x4& x) { return x; }
   using Four = f32x4;
   static __device__ __forceinline__ f32x4 wide(const Four& v) { return v; }
   static __device__ __forceinline__ f32x4 get4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
@@ -239,6 +241,10 @@ template <> struct Lin<float> {
 };
 
 constexpr int kThreads = 256, kWaves = 4;
+// Tokens per chunk. 64 halve the barriers but hold twice the rows on their way: two
+// waves per SIMD instead of three in the forward (78 us where 32 take 65; 4 x 4,096
+// tokens, 16 heads), spills in the gradients (399 and 327).
+constexpr int kChunk = 32;
 
 // n rows of `bytes` bytes, `stride` apart, as a buffer: loads beyond them give
 // zeros, stores beyond them do nothing. The chunk's rows span less than 2^32 bytes.
@@ -251,7 +257,7 @@ __device__ __forceinline__ auto rows_rsrc(const void* base, uint32_t stride, int
 // and pass; rows from n on are zeros.
 template <class T, int D>
 struct Rows {
-  static constexpr int C = Lin<T>::C;
+  static constexpr int C = kChunk;
   static constexpr int VPR = D * (int)sizeof(T) / 16, RPP = kThreads / VPR, NP = C / RPP;
   static_assert(RPP * NP == C, "whole passes");
   static constexpr int BYTES = C * D * (int)sizeof(T);
@@ -408,11 +414,13 @@ __device__ __forceinline__ int lin_reach(const LinearArgs& a, const Segment& seg
 template <class T, int DC, int CW, int ROLE>
 struct WalkLds {
   using L = Lin<T>;
-  static constexpr int C = L::C, DO = 64 * CW;
+  static constexpr int C = kChunk, DO = 64 * CW;
   static constexpr bool STATE = ROLE == kStateFwd || ROLE == kStateRev;
   static constexpr int X = 0, Y = X + (STATE ? 0 : Rows<T, DC>::BYTES), Z = Y + Rows<T, DC>::BYTES;
   static constexpr int K = Z + Rows<T, DO>::BYTES, P = K + (ROLE == kDk ? Rows<T, DO>::BYTES : 0);
-  static constexpr int G = P + (STATE ? 0 : C * C * (int)sizeof(T));
+  // bf16 parts of the pairs' products
+  static constexpr int NP = sizeof(T) == 2 ? 2 : 1, PLANE = C * C * (int)sizeof(T);
+  static constexpr int G = P + (STATE ? 0 : NP * PLANE);
   static constexpr int SUMS = G + 2 * (int)((sizeof(Gates<C>) + 15) / 16 * 16);
   static constexpr int BYTES = SUMS + (ROLE == kDk ? 9 : ROLE == kDq ? 4 : 0) * kWaves * C * 4;
 };
@@ -428,7 +436,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   using W = WalkLds<T, DC, CW, ROLE>;
   using Frag = typename L::Frag;
   using Four = typename L::Four;
-  constexpr int C = L::C, DO = 64 * CW, ES = sizeof(T), NQ = C / 16, NT = NQ * NQ / kWaves;
+  constexpr int C = kChunk, DO = 64 * CW, ES = sizeof(T), NQ = C / 16, NT = NQ * NQ / kWaves;
   constexpr bool REV = ROLE == kDk || ROLE == kDv || ROLE == kStateRev, STATE = W::STATE;
   constexpr bool TURNED = ROLE == kDq || ROLE == kDk;      // the state is held transposed
   // bf16 parts of the state where an output reads it, and of what it takes up
@@ -618,7 +626,12 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
                 *reinterpret_cast<f32x4*>(sums + wave * C + 16 * kt + 4 * grp) = f32x4{rsum[0], rsum[1], rsum[2], rsum[3]};
             }
           }
-          L::put4(reinterpret_cast<T*>(sP + 16 * qt * Tile<T, C>::RB + (pput ^ (16 * kt * ES))), p);
+          char* const at = sP + 16 * qt * Tile<T, C>::RB + (pput ^ (16 * kt * ES));
+#pragma unroll
+          for (int m = 0; m < W::NP; ++m) {
+            L::put4(reinterpret_cast<T*>(at + m * W::PLANE), p);
+            if (m + 1 < W::NP) p -= L::rounded4(p);
+          }
         }
         if constexpr (ROLE == kDk) {
           cols[(4 * wave + grp) * C + 16 * qt + r16] = csum;
@@ -686,9 +699,12 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
 #pragma unroll
         for (int tb = 0; tb < C / 32; ++tb) {
           if (REV ? 2 * tb + 1 < t : 2 * tb > t) continue;
-          const Frag pf = L::template row<C>(sP, prow, t, tb);
 #pragma unroll
-          for (int ct = 0; ct < CW; ++ct) O[ct][t] = L::mma(zf[tb][ct], pf, O[ct][t]);
+          for (int m = 0; m < W::NP; ++m) {
+            const Frag pf = L::template row<C>(sP + m * W::PLANE, prow, t, tb);
+#pragma unroll
+            for (int ct = 0; ct < CW; ++ct) O[ct][t] = L::mma(zf[tb][ct], pf, O[ct][t]);
+          }
         }
       // ---- the outputs
       char* dst;
@@ -1022,7 +1038,7 @@ hipError_t launch(K* kernel, const LinearArgs& a, int64_t units, int y, int lds,
 }
 template <class T, int DK, int DV>
 hipError_t launch_states(const LinearArgs& a, int y, hipStream_t s) {
-  constexpr int C = Lin<T>::C;
+  constexpr int C = kChunk;
   const hipError_t e = launch(lin_states_kernel<T, DK, DV>, a, (int64_t)a.slots * a.Hv * RoleDims<DK, DV, kStateFwd>::SLABS,
                               y, role_lds<T, DK, DV, kStateFwd>(), s);
   if (e != hipSuccess || a.N == 0) return e;
@@ -1056,7 +1072,7 @@ hipError_t launch_walks(const LinearArgs& a, hipStream_t s) {
 
 template <class T>
 hipError_t linear_bwd(const LinearArgs& a, hipStream_t s) {
-  constexpr int C = Lin<T>::C;
+  constexpr int C = kChunk;
   hipError_t e = GDN_LINEAR_DIMS(launch_walks, T);
   if (e != hipSuccess) return e;
   const int units = a.slots * a.Hv;
@@ -1078,8 +1094,8 @@ hipError_t linear_bwd(const LinearArgs& a, hipStream_t s) {
 
 }  // namespace
 
-LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dv, bool f32, bool bwd) {
-  const int C = f32 ? Lin<float>::C : Lin<bf16>::C;
+LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dk, int Dv, bool bwd) {
+  const int C = kChunk;
   const int slabs = Dv <= 128 ? 1 : 2;
   const int64_t chunks = packed ? tokens / C + N : (int64_t)N * ((T + C - 1) / C);
   const int64_t most = packed ? tokens / C + 1 : std::max(1, (T + C - 1) / C);      // of one sequence
@@ -1089,8 +1105,13 @@ LinearPlan linear_plan(int N, int T, int64_t tokens, bool packed, int Hv, int Dv
   // cost states, fewer leave CUs idle.
   const int64_t target = bwd ? 256 : 512;
   const int64_t want = std::max<int64_t>(1, (target + Hv * slabs - 1) / (Hv * slabs));
+  // Not below 256 tokens, or 128 with states of at most 64 x 128, whose states cost
+  // as much as their tokens; and short sequences stay whole: a state's two launches
+  // cost more than a few chunks in series (gradients in FP32, 2 x 515 tokens, 64 x 64:
+  // 40 and 54 us with 128 and 256; packed 128 x 128: 74 and 68).
+  const int least = (Dk * Dv <= 64 * 128 ? 128 : 256) / C;
   LinearPlan p{};
-  p.seg = (int)std::min<int64_t>(most, std::max<int64_t>(256 / C, (chunks + want - 1) / want));
+  p.seg = (int)std::min<int64_t>(most, std::max<int64_t>(most < 12 ? most : least, (chunks + want - 1) / want));
   p.segmented = p.seg < most;
   const int64_t m = (int64_t)p.seg * C;
   p.slots = packed ? N + tokens / m : N * std::max<int64_t>(1, (T + m - 1) / m);
