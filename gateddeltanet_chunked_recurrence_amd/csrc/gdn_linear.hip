@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(kThreads) lin_dg_kernel(LinearArgs a, int unit
   // Two chunks at a time, tokens backwards over the lanes of a half: a prefix sum
   // over lanes is a suffix sum over tokens.
   static_assert(2 * C == WAVE, "a chunk per half");
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = 8;
   const int half = lane >> 5, back = C - 1 - (lane & 31);
   double end = a.ws_end[unit], sum = 0.0;
   for (int c0 = seg.first + seg.count - 1; c0 >= seg.first; c0 -= 2 * AHEAD) {
@@ -974,12 +974,12 @@ __global__ void __launch_bounds__(kThreads) lin_dg_kernel(LinearArgs a, int unit
       const int c = c0 - 2 * u - half, t = c * C + back;
       const bool here = c >= seg.first && t < seg.len;
       const double sx = wave_incl_scan64(x[u]), sy = wave_incl_scan64(y[u]);
-      const double sg = wave_incl_scan64(g[u] < kResetGate ? kResetGate : g[u]);
+      const float sg = wave_incl_scan(fmaxf(g[u], kResetGate));   // for the comparison alone
       double e[2];
       double at = end, bx = 0.0, by = 0.0, bg = 0.0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const double tx = read_lane64(sx, 32 * i + 31), ty = read_lane64(sy, 32 * i + 31), tg = read_lane64(sg, 32 * i + 31);
+        const double tx = read_lane64(sx, 32 * i + 31), ty = read_lane64(sy, 32 * i + 31), tg = read_lane(sg, 32 * i + 31);
         e[i] = at - bx - by;                              // the scans run on over both halves
         at = (tg - bg < -20.8 ? 0.0 : at + (ty - by)) + (tx - bx);
         bx = tx;
