@@ -11,7 +11,9 @@
 // a = alpha d:  p = c^T k, w = c^T q;  u = beta (v - a p);
 //   o_before = scale (a w + (k . q) u);  S' = a c + k u^T
 // so both products read the codes as they are and the output needs no pass
-// over S'. Linear attention (LIN) is the same step with u = v.
+// over S'. Linear attention (LIN) is the same step with u = v. On pages of FP32
+// states it is a copy: 301 sequences of 32 heads of 128 x 256 (2.5 GB) 476 us, 5.2 TB/s;
+// on E4M3 pages, 192 sequences of 16 heads from parents' pages, 22 us (25 as delta rule).
 //
 // Bound: a token moves Dk Dv bytes in and out per head for 6 Dk Dv FLOP, so
 // at many sequences this is a copy (bound by HBM). The page is value-major

@@ -580,10 +580,11 @@ gdn_status gdn_logits_adjust(const gdn_logits_args* a, void* stream);
  * h / (Hv / Hqk). Tokens that no sequence holds (before cu_seqlens[0] or from
  * cu_seqlens[N] on) are neither read nor written; offsets outside the
  * buffer are cut to it.
- * Arithmetic: products on the matrix cores with FP32 sums. States, decays and dg
- * keep FP32 (bf16 factors of states are taken in two parts, 2^-17); the pairs'
- * weights of a chunk, and states that only o is read from, are rounded to the input
- * type. The results do not depend on what else runs, and repeat bit for bit.
+ * Arithmetic: products on the matrix cores with FP32 sums. States, decays, dh0 and
+ * dg keep FP32 (their factors enter in three bf16 parts); with bf16 inputs the
+ * states that o and dv are read from are rounded to bf16, and the weighted products
+ * of the tokens of a chunk to two parts, 2^-16. Contributions whose decay is zero in FP32
+ * are left out. The results do not depend on what else runs, and repeat bit for bit.
  * Sizes: Dk in {64, 128}, Dv in {64, 128, 256}, Hv % Hqk == 0, either io_dtype. */
 typedef struct {
   int32_t B, T, Hqk, Hv, Dk, Dv;

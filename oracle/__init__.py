@@ -13,6 +13,8 @@ Modules:
   decode     decode continuation: exact chunk prefill of a prefix, then
              token-state writes through the state quantizer, both readouts,
              and the straight-through backward (torch float64 CPU)
+  linear     linear attention with a decay per head, token by token, and its
+             gradients (torch float64 CPU)
 """
 from .qdq import FMT_OFF, FMT_E4M3, FMT_INT8, qdq32, round_e4m3, round_int8, e4m3_encode  # noqa: F401
 from .recurrent import recurrent_fwd  # noqa: F401

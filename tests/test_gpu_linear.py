@@ -1,8 +1,8 @@
 """Linear attention with a decay per head on the GPU against the float64 oracle.
 
 Bounds. U = 2^-8 is half a bf16 step. Each value of o is a sum of products; the
-kernel rounds the pair weights and the state it is read from to bf16 (once each) and
-the result once, so |error| <= U A + U |o|, with A the same sum over the
+kernel rounds the weighted products of pairs and the state it is read from to bf16 at
+most once each and the result once, so |error| <= U A + U |o|, with A the same sum over the
 absolute values of every factor (which the oracle computes from |q|, |k|, |v|,
 |h0|); FP32 sums and exponentials add less than 2^-14 A at these lengths (under
 900 sums of 2^-24 each, exponents to 2^-21). dq, dk, dv: the same form. States and
