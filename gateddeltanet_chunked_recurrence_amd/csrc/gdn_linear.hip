@@ -39,13 +39,15 @@
 // registers a chunk ahead and put in LDS without padding (Tile).
 //
 // Bound: memory, but for what the phases of a chunk leave uncovered. 65,536 tokens, 32
-// heads of 128 x 256 (3.2 GB): the forward walk alone 820 to 920 us, without its
-// products 670, without its loads and stores 540. 4 x 4,096 tokens, 16 heads of 128 x
+// heads of 128 x 256 (3.2 GB): the forward walk alone 820 to 920 us on two cards. An
+// earlier step's whole call took 995 us, without its products 887, without loads and
+// stores 755, so neither alone bounds it. 4 x 4,096 tokens, 16 heads of 128 x
 // 128 (268 MB): 69 us of walk, 22 and 12 of states. Gradients of 2 x 8,192 tokens: 280 us of
-// walks, each of which reads four operands (720 MB, of which the counters see 760 from beyond
-// L2: dk and dv do not stay close enough to share), 25, 14 and 20 of states, folds and dg. A chunk of a walk takes 6,600 cycles in
-// the forward and 9,300 to 9,500 in dk and dq: of these (dk) 1,900 to send loads and multiply
-// pairs, 3,200 for the state's part (192 of its vector instructions make parts), 1,700 for
+// walks, which read eleven operands of 67 MB between them (738 MB; the counters see 760
+// fetched with the states, so L2 shares nothing between walks), 25, 14 and 20 of
+// states, folds and dg. A chunk of a walk takes about 6,400 cycles in the forward; dk
+// alone on the device 9,000: of these 1,950 to send loads and multiply pairs, 3,200
+// for the state's part (192 of its vector instructions make parts), 1,700 for
 // the update. Dropped: tokens 64 to a chunk (see kChunk), three workgroups per CU for the
 // gradients (registers spill: 420 us where two take 325), dv in half-wide columns (351),
 // non-temporal loads and stores (no change, or 3% more).
