@@ -958,7 +958,8 @@ def gdn_linear_fwd(q, k, v, g, scale=None, h0=None, cu_seqlens=None, output_fina
     (bf16 or FP32; token strides are free), g FP32, the log-decay [B, T, Hv], or [Hv]
     for one per head; h0 [N, Hv, Dk, Dv] FP32 or None; cu_seqlens int32 [N + 1]
     (B = 1) or None. Returns (o [B, T, Hv, Dv] in q's type, ht FP32 or None).
-    Tokens that no sequence holds are not written."""
+    Tokens that no sequence holds are not written. out (given to be written to) lies
+    apart from the inputs."""
     a, state = _linear_args(q, k, v, g, scale, h0, cu_seqlens)
     dev, shape = q.device, (a.B, a.T, a.Hv, a.Dv)
     if out is None:
@@ -993,7 +994,7 @@ def gdn_linear_bwd(q, k, v, g, do, dht=None, scale=None, h0=None, cu_seqlens=Non
     q, contiguous) and dht [N, Hv, Dk, Dv] FP32 or None. Returns dict dq, dk, dv (the
     type of q), dg FP32 in g's shape, and dh0 FP32 when h0 is given. Tokens
     that no sequence holds are not written. out: optional dict of dq, dk, dv, dg to
-    write to."""
+    write to, apart from the inputs and each other."""
     a, state = _linear_args(q, k, v, g, scale, h0, cu_seqlens)
     dev, dt = q.device, q.dtype
     _need(do, 'do', dt, (a.B, a.T, a.Hv, a.Dv), dev)

@@ -857,7 +857,12 @@ gdn_status check_beam_parts(const gdn::BeamArgs& k) {
 }
 
 // ------------------------------------------------------- linear attention
-gdn_status check_linear(const gdn_linear_args* a, const char* what) {
+gdn::LinearPlan plan_linear(const gdn_linear_args* a, bool bwd) {
+  return gdn::linear_plan(a->num_seqs, a->T, (int64_t)a->B * a->T, a->cu_seqlens != nullptr, a->Hv, a->Dk,
+                          a->Dv, bwd);
+}
+
+gdn_status check_linear(const gdn_linear_args* a, const char* what, bool bwd) {
   if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
   if (a->B < 0 || a->T < 0 || a->Hqk <= 0 || a->Hv <= 0 || a->num_seqs < 0)
     return fail(GDN_E_INVALID, "%s: bad sizes B=%d T=%d Hqk=%d Hv=%d", what, a->B, a->T, a->Hqk, a->Hv);
@@ -889,15 +894,17 @@ gdn_status check_linear(const gdn_linear_args* a, const char* what) {
     if (e.stride != 0 && (e.stride < e.row || e.stride * es % 16 != 0 || e.stride >= (1 << 24)))
       return fail(GDN_E_INVALID, "%s: %s_stride %lld: at least %lld, below 2^24 and a multiple of 16 bytes", what,
                   e.name, (long long)e.stride, (long long)e.row);
-  // every grid: (segments, at most chunks + sequences) x heads x slabs, and vectors of a state per head
-  if ((tokens / 32 + a->num_seqs + 1) * a->Hv * 4 > INT32_MAX || (int64_t)a->num_seqs * a->Hv * 32 > INT32_MAX)
-    return fail(GDN_E_UNSUPPORTED, "%s: (chunks + sequences) * Hv is too large", what);
+  // Every grid has fewer than 2^32 threads in x, by the bound of the most workgroups
+  // first so that the plan's own products hold.
+  const char* large = "%s: (chunks + sequences) * Hv is too large";
+  if ((tokens / 32 + a->num_seqs + 1) * a->Hv * 4 > INT32_MAX) return fail(GDN_E_UNSUPPORTED, large, what);
+  const gdn::LinearPlan p = plan_linear(a, bwd);
+  const int64_t heads = (int64_t)a->num_seqs * a->Hv, most = UINT32_MAX / 256 - 8;
+  if (p.slots * a->Hv * (a->Dv == 256 ? 2 : 1) > most || (p.segmented && heads * (a->Dk * a->Dv / 1024) > most))
+    return fail(GDN_E_UNSUPPORTED, large, what);
+  if (bwd && a->Hv != a->Hqk && tokens * a->Hqk * a->Dk / 4 > most * 256)
+    return fail(GDN_E_UNSUPPORTED, "%s: B * T * Hqk * Dk is too large", what);
   return GDN_OK;
-}
-
-gdn::LinearPlan plan_linear(const gdn_linear_args* a, bool bwd) {
-  return gdn::linear_plan(a->num_seqs, a->T, (int64_t)a->B * a->T, a->cu_seqlens != nullptr, a->Hv, a->Dk,
-                          a->Dv, bwd);
 }
 
 // Offsets of the workspace's parts.
@@ -982,6 +989,30 @@ gdn_status check_linear_ptrs(const char* what, const LinearPtr* e, int n, const 
       return fail(GDN_E_INVALID, "%s: %s is not %d-byte aligned", what, e[i].name, (int)align);
   }
   return GDN_OK;
+}
+
+// Outputs are written while inputs are still read, so none may lie in another's
+// memory (from its first token to its last).
+struct LinearSpan { const void* p; int64_t bytes; const char* name; };
+gdn_status check_linear_apart(const char* what, const LinearSpan* out, int outs, const LinearSpan* in, int ins) {
+  auto meet = [](const LinearSpan& x, const LinearSpan& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return a && b && x.bytes > 0 && y.bytes > 0 && a < b + (uintptr_t)y.bytes && b < a + (uintptr_t)x.bytes;
+  };
+  for (int i = 0; i < outs; ++i) {
+    for (int j = 0; j < ins; ++j)
+      if (meet(out[i], in[j])) return fail(GDN_E_INVALID, "%s: %s overlaps %s", what, out[i].name, in[j].name);
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return fail(GDN_E_INVALID, "%s: %s overlaps %s", what, out[i].name, out[j].name);
+  }
+  return GDN_OK;
+}
+struct LinearBytes { int64_t q, k, v, g, row_qk, row_v, state; };   // of inputs as they lie, of contiguous tensors
+LinearBytes linear_bytes(const gdn_linear_args* a, const gdn::LinearArgs& k) {
+  const int64_t es = a->io_dtype == GDN_F32 ? 4 : 2, n = k.tokens, qk = (int64_t)a->Hqk * a->Dk, v = (int64_t)a->Hv * a->Dv;
+  auto span = [&](int64_t stride, int64_t row) { return n ? ((n - 1) * stride + row) * es : 0; };
+  return {span(k.qs, qk), span(k.ks, qk), span(k.vs, v), (a->g_per_head ? 1 : n) * a->Hv * 4, n * qk * es, n * v * es,
+          (int64_t)a->num_seqs * a->Hv * a->Dk * a->Dv * 4};
 }
 
 // gdn_pool_step, or (linear) gdn_pool_linear_step: g one per head or per token, no beta.
@@ -1396,14 +1427,14 @@ gdn_status gdn_beam_select(const gdn_beam_args* a, void* stream) {
 }
 
 size_t gdn_linear_fwd_workspace_bytes(const gdn_linear_args* a) {
-  if (check_linear(a, "gdn_linear_fwd") != GDN_OK) return 0;
+  if (check_linear(a, "gdn_linear_fwd", false) != GDN_OK) return 0;
   const gdn::LinearPlan p = plan_linear(a, false);
   return (size_t)linear_ws(a, p, false).total;
 }
 
 gdn_status gdn_linear_fwd(const gdn_linear_args* a, void* stream) {
   const char* what = "gdn_linear_fwd";
-  gdn_status s = check_linear(a, what);
+  gdn_status s = check_linear(a, what, false);
   if (s != GDN_OK) return s;
   const bool any = (int64_t)a->B * a->T > 0;
   const LinearPtr ptrs[] = {{a->q, "q", any}, {a->k, "k", any}, {a->v, "v", any}, {a->g, "g", any},
@@ -1418,12 +1449,16 @@ gdn_status gdn_linear_fwd(const gdn_linear_args* a, void* stream) {
   gdn::LinearArgs k = linear_args(a, p, w, false, a->workspace);
   k.o = a->o;
   k.ht = a->ht;
+  const LinearBytes n = linear_bytes(a, k);
+  const LinearSpan in[] = {{a->q, n.q, "q"}, {a->k, n.k, "k"}, {a->v, n.v, "v"}, {a->g, n.g, "g"}, {a->h0, n.state, "h0"}};
+  const LinearSpan out[] = {{a->o, n.row_v, "o"}, {a->ht, n.state, "ht"}};
+  if ((s = check_linear_apart(what, out, 2, in, 5)) != GDN_OK) return s;
   return hip_status(gdn::launch_linear_fwd(k, a->io_dtype == GDN_F32, static_cast<hipStream_t>(stream)),
                     "gdn_linear_fwd launch");
 }
 
 size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_bwd_args* a) {
-  if (!a || check_linear(&a->fwd, "gdn_linear_bwd") != GDN_OK) return 0;
+  if (!a || check_linear(&a->fwd, "gdn_linear_bwd", true) != GDN_OK) return 0;
   const gdn::LinearPlan p = plan_linear(&a->fwd, true);
   return (size_t)linear_ws(&a->fwd, p, true).total;
 }
@@ -1432,7 +1467,7 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* a, void* stream) {
   const char* what = "gdn_linear_bwd";
   if (!a) return fail(GDN_E_INVALID, "argument struct is NULL");
   const gdn_linear_args* f = &a->fwd;
-  gdn_status s = check_linear(f, what);
+  gdn_status s = check_linear(f, what, true);
   if (s != GDN_OK) return s;
   const bool any = (int64_t)f->B * f->T > 0;
   const LinearPtr ptrs[] = {{f->q, "q", any},  {f->k, "k", any},   {f->v, "v", any},   {f->g, "g", any},
@@ -1453,6 +1488,12 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* a, void* stream) {
   k.dv = a->dv;
   k.dg = a->dg;
   k.dh0 = a->dh0;
+  const LinearBytes n = linear_bytes(f, k);
+  const LinearSpan in[] = {{f->q, n.q, "q"},       {f->k, n.k, "k"},         {f->v, n.v, "v"},         {f->g, n.g, "g"},
+                           {f->h0, n.state, "h0"}, {a->do_, n.row_v, "do"}, {a->dht, n.state, "dht"}};
+  const LinearSpan out[] = {{a->dq, n.row_qk, "dq"}, {a->dk, n.row_qk, "dk"}, {a->dv, n.row_v, "dv"},
+                            {a->dg, n.g, "dg"},      {a->dh0, n.state, "dh0"}};
+  if ((s = check_linear_apart(what, out, 5, in, 7)) != GDN_OK) return s;
   return hip_status(gdn::launch_linear_bwd(k, f->io_dtype == GDN_F32, static_cast<hipStream_t>(stream)),
                     "gdn_linear_bwd launch");
 }
@@ -1523,7 +1564,8 @@ gdn_status gdn_logits_adjust(const gdn_logits_args* a, void* stream) {
   k.f32 = a->io_dtype == GDN_F32;
   if (!any) return GDN_OK;
   gdn::rules_plan(k);
-  if ((int64_t)k.B * k.W * k.tiles > INT32_MAX) return fail(GDN_E_UNSUPPORTED, "%s: B * W * V is too large", what);
+  if ((int64_t)k.B * k.W * k.tiles > UINT32_MAX / 512)      // 2^32 threads at most
+    return fail(GDN_E_UNSUPPORTED, "%s: B * W * V is too large", what);
   k.err = err_word();
   if (!k.err) return no_err_word();
   return hip_status(gdn::launch_rules(k, static_cast<hipStream_t>(stream)), "gdn_logits_adjust launch");

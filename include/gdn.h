@@ -585,6 +585,10 @@ gdn_status gdn_logits_adjust(const gdn_logits_args* a, void* stream);
  * states that o and dv are read from are rounded to bf16, and the weighted products
  * of the tokens of a chunk to two parts, 2^-16. Contributions whose decay is zero in FP32
  * are left out. The results do not depend on what else runs, and repeat bit for bit.
+ * Inputs other than gates must be finite: one that is not reaches its own
+ * sequence and head alone (in gradients those that share q and k), but there also
+ * outputs of earlier tokens, as its chunk's products are formed together. Outputs lie
+ * apart from the inputs, h0 and each other; a call where they do not is refused.
  * Sizes: Dk in {64, 128}, Dv in {64, 128, 256}, Hv % Hqk == 0, either io_dtype. */
 typedef struct {
   int32_t B, T, Hqk, Hv, Dk, Dv;

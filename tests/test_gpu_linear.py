@@ -283,3 +283,37 @@ def test_growing_gates_and_long_decays():
         say(f'gates of {level}')
         check_fwd(x, d, cu, 'bf16')
         check_bwd(x, d, cu, 'bf16')
+
+
+@pytest.mark.parametrize('bad', [math.nan, math.inf])
+def test_what_is_not_finite_stays_in_its_sequence_and_heads(bad):
+    _, d, cu = make('bf16', 1, 0, [37, 300, 1, 64], 2, 4, 64, 128)
+    run = lambda: (G.gdn_linear_fwd(d['q'], d['k'], d['v'], d['g'], h0=d['h0'], cu_seqlens=d['cu']),     # noqa: E731
+                   G.gdn_linear_bwd(d['q'], d['k'], d['v'], d['g'], d['do'], d['dht'], h0=d['h0'], cu_seqlens=d['cu']))
+    (o, ht), grads = run()
+    for name in ('q', 'k', 'v', 'do'):
+        d[name][:, cu[1]:cu[2], 0] = bad                                # sequence 1, first head
+    d['h0'][1, 0] = d['dht'][1, 0] = bad
+    (o1, ht1), grads1 = run()
+    here = torch.zeros(cu[-1], 4, dtype=torch.bool)
+    here[cu[1]:cu[2], :2] = True                                        # the value heads of its group
+    rest = ~here.cuda()
+    assert torch.equal(_bits(o[0][rest]), _bits(o1[0][rest])) and torch.isnan(o1[0, cu[1]:cu[2], 0]).any()
+    for n in ('dv', 'dg'):
+        assert torch.equal(_bits(grads[n][0][rest]), _bits(grads1[n][0][rest])), n
+    for n in ('dq', 'dk'):
+        assert torch.equal(_bits(grads[n][0][rest[:, ::2]]), _bits(grads1[n][0][rest[:, ::2]])), n
+    keep = torch.ones(4, 4, dtype=torch.bool, device='cuda')
+    keep[1, :2] = False
+    for a, b in ((ht, ht1), (grads['dh0'], grads1['dh0'])):
+        assert torch.equal(a[keep], b[keep])
+
+
+def test_outputs_in_the_inputs_memory_are_refused():
+    _, d, _ = make('bf16', 1, 70, None, 2, 2, 64, 64)
+    for name in ('q', 'v'):
+        with pytest.raises(G.GdnError, match='o overlaps ' + name):
+            G.gdn_linear_fwd(d['q'], d['k'], d['v'], d['g'], out=d[name])
+    out = dict(dq=torch.empty_like(d['q']), dk=torch.empty_like(d['k']), dv=d['do'], dg=torch.empty_like(d['g']))
+    with pytest.raises(G.GdnError, match='dv overlaps do'):
+        G.gdn_linear_bwd(d['q'], d['k'], d['v'], d['g'], d['do'], out=out)

@@ -96,6 +96,60 @@ def test_linear_backward_checks_its_arguments(kw, status, msg):
     assert got == status and msg in text, (got, text)
 
 
+# the last byte of one and the first of another, in a call whose tensors lie apart otherwise
+def _apart(names, at):
+    return {n: 0x100000000 + (i << 32) for i, n in enumerate(names)} | at
+
+
+QB, VB, SB = 2 * 100 * 2 * 128 * 2, 2 * 100 * 4 * 256 * 2, 2 * 4 * 128 * 256 * 4
+
+
+@pytest.mark.parametrize('out,of,off', [
+    ('o', 'v', 0), ('o', 'q', QB - 16), ('o', 'k', 16 - VB), ('o', 'g', 0), ('ht', 'h0', 0), ('ht', 'o', VB - 16),
+    ('o', 'q', 'strided')])
+def test_linear_forward_refuses_outputs_in_other_memory(out, of, off):
+    kw = _apart(('q', 'k', 'v', 'g', 'h0', 'o', 'ht'), {})
+    if off == 'strided':
+        kw['q_stride'] = 1024
+        off = 199 * 1024 * 2
+    kw[out] = kw[of] + off
+    got, text = _call('gdn_linear_fwd', _linear(**kw))
+    assert got == B.GDN_E_INVALID and f'{out} overlaps {of}' in text, (got, text)
+
+
+@pytest.mark.parametrize('out,of,off', [
+    ('dq', 'q', 0), ('dk', 'dq', QB - 16), ('dv', 'do_', 0), ('dv', 'v', 16 - VB), ('dg', 'g', 0), ('dh0', 'dht', SB - 16)])
+def test_linear_backward_refuses_outputs_in_other_memory(out, of, off):
+    kw = _apart(('q', 'k', 'v', 'g', 'h0', 'do_', 'dht', 'dq', 'dk', 'dv', 'dg', 'dh0', 'workspace'), {})
+    kw[out] = kw[of] + off
+    own = {k: kw.pop(k) for k in ('do_', 'dht', 'dq', 'dk', 'dv', 'dg', 'dh0', 'workspace')}
+    b = B.LinearBwdArgs(fwd=_linear(**kw), workspace_bytes=1 << 31, **own)
+    got, text = _call('gdn_linear_bwd', b)
+    assert got == B.GDN_E_INVALID and f'{out} overlaps {of.rstrip("_")}' in text, (got, text)
+
+
+@pytest.mark.parametrize('kw', [
+    dict(B=65535, num_seqs=65535, T=1, Hv=512, Hqk=512, Dk=64, Dv=64),          # workgroups of the walks
+    dict(B=1, num_seqs=65535, T=1 << 20, Hv=256, Hqk=128, cu_seqlens=FAKE)])
+def test_linear_refuses_grids_past_32_bits(kw):
+    got, text = _call('gdn_linear_fwd', _linear(**kw))
+    assert got == B.GDN_E_UNSUPPORTED and 'too large' in text, (got, text)
+    assert B.load_library().gdn_linear_fwd_workspace_bytes(ctypes.byref(_linear(**kw))) == 0
+
+
+def test_linear_backward_refuses_a_sum_over_heads_past_32_bits():
+    b = B.LinearBwdArgs(fwd=_linear(B=1, num_seqs=1, T=1 << 20, Hqk=128, Hv=256, Dv=64))
+    for name in ('do_', 'dq', 'dk', 'dv', 'dg'):
+        setattr(b, name, FAKE)
+    got, text = _call('gdn_linear_bwd', b)
+    assert got == B.GDN_E_UNSUPPORTED and 'Hqk * Dk is too large' in text, (got, text)
+
+
+def test_logits_adjust_refuses_grids_past_32_bits():
+    got, text = _call('gdn_logits_adjust', _logits(B=65535, W=300, V=10, out=FAKE, mask=None))
+    assert got == B.GDN_E_UNSUPPORTED and 'too large' in text, (got, text)
+
+
 def test_linear_with_nothing_to_do():
     for kw in (dict(B=0, num_seqs=0), dict(T=0)):
         assert _call('gdn_linear_fwd', _linear(**kw))[0] == B.GDN_OK
