@@ -826,14 +826,16 @@ def gdn_logits_adjust(logits, tokens=None, lens=None, prompt_lens=None, repetiti
     [B, W] picks a row for each beam (-1: none; default: row b W + w). Returns a new
     tensor, or out, which may be logits."""
     B, W, V, rs = _logit_rows(logits, 'logits')
-    dev = logits.device
+    dev, os = logits.device, 0
     if out is None:
-        out = torch.empty(B, W, V, dtype=logits.dtype, device=dev)
+        out = torch.empty((B, W, V), dtype=logits.dtype, device=dev)
     elif out.shape != logits.shape or out.dtype is not logits.dtype or out.device != dev:
         raise ValueError(f'out: {str(logits.dtype)[6:]} {list(logits.shape)} on {dev}; got '
                          f'{str(out.dtype)[6:]} {list(out.shape)} on {out.device}')
+    else:
+        os = _logit_rows(out, 'out')[3]
     a = LogitsArgs(B=B, W=W, V=V, io_dtype=GDN_BF16 if logits.dtype is torch.bfloat16 else GDN_F32,
-                   row_stride=rs, out_stride=_logit_rows(out, 'out')[3], logits=logits.data_ptr(),
+                   row_stride=rs, out_stride=os, logits=logits.data_ptr(),
                    out=out.data_ptr())
     if tokens is not None:
         L = tokens.shape[-1] if tokens.dim() else 0

@@ -963,8 +963,8 @@ __global__ void __launch_bounds__(kThreads) lin_fold_kernel(LinearArgs a, int bl
 // dg of a segment's tokens, a wave per (segment, head): suffix sums over each
 // chunk on top of <dS, S> at its end.
 template <int C>
-__global__ void __launch_bounds__(kThreads) lin_dg_kernel(LinearArgs a, int units) {
-  const int unit = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__device__ __forceinline__ void lin_dg(const LinearArgs& a, int units, int block) {
+  const int unit = block * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (unit >= units) return;
   const int slot = unit / a.Hv, h = unit - slot * a.Hv, lane = __lane_id();
   Segment seg;
@@ -1027,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads) lin_dg_kernel(LinearArgs a, int unit
     if (lane == WAVE - 1) a.ws_dgsum[unit] = sum;
   }
 }
+
 // A decay per head: dg is the sum over all tokens, segments in their order.
 __global__ void __launch_bounds__(WAVE) lin_dgsum_kernel(LinearArgs a) {
   const int h = blockIdx.x, lane = __lane_id();
@@ -1038,8 +1039,8 @@ __global__ void __launch_bounds__(WAVE) lin_dgsum_kernel(LinearArgs a) {
 
 // The sum over the value heads that share a query and key head.
 template <class T>
-__global__ void __launch_bounds__(kThreads) lin_group_kernel(LinearArgs a, int64_t vecs) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+__device__ __forceinline__ void lin_group(const LinearArgs& a, int64_t vecs, int block) {
+  const int64_t i = (int64_t)block * kThreads + threadIdx.x;
   if (i >= vecs) return;
   const int G = a.Hv / a.Hqk, per = a.Hqk * a.Dk / 4;
   const int64_t tok = i / per;
@@ -1054,6 +1055,15 @@ __global__ void __launch_bounds__(kThreads) lin_group_kernel(LinearArgs a, int64
   }
   Lin<T>::put4(static_cast<T*>(a.dq) + tok * a.Hqk * a.Dk + at, s);
   Lin<T>::put4(static_cast<T*>(a.dk) + tok * a.Hqk * a.Dk + at, t);
+}
+
+// What follows the walks, in one launch: the first dg_blocks workgroups form dg, chains of
+// loads in few waves, beside those that sum heads, memory alone (apart, 2 x 515 tokens of FP32
+// 42 us and packed 4 / 16 heads of 128 x 128 207; together 38 and 200).
+template <class T>
+__global__ void __launch_bounds__(kThreads) lin_ends_kernel(LinearArgs a, int units, int dg_blocks, int64_t vecs) {
+  if ((int)blockIdx.x < dg_blocks) lin_dg<kChunk>(a, units, blockIdx.x);
+  else lin_group<T>(a, vecs, blockIdx.x - dg_blocks);
 }
 
 // A kernel's grid: units, rounded up to eight, by y.
@@ -1099,21 +1109,16 @@ hipError_t launch_walks(const LinearArgs& a, hipStream_t s) {
 
 template <class T>
 hipError_t linear_bwd(const LinearArgs& a, hipStream_t s) {
-  constexpr int C = kChunk;
   hipError_t e = GDN_LINEAR_DIMS(launch_walks, T);
   if (e != hipSuccess) return e;
-  const int units = a.slots * a.Hv;
-  if (units > 0) {
-    lin_dg_kernel<C><<<dim3((unsigned)((units + kWaves - 1) / kWaves)), kThreads, 0, s>>>(a, units);
+  const int units = a.slots * a.Hv, dg_blocks = (units + kWaves - 1) / kWaves;
+  const int64_t vecs = a.ws_dq ? (int64_t)a.tokens * a.Hqk * a.Dk / 4 : 0, blocks = dg_blocks + (vecs + kThreads - 1) / kThreads;
+  if (blocks > 0) {
+    lin_ends_kernel<T><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a, units, dg_blocks, vecs);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.ws_dgsum) {
     lin_dgsum_kernel<<<dim3((unsigned)a.Hv), WAVE, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (a.ws_dq && a.tokens > 0) {
-    const int64_t vecs = (int64_t)a.tokens * a.Hqk * a.Dk / 4;
-    lin_group_kernel<T><<<dim3((unsigned)((vecs + kThreads - 1) / kThreads)), kThreads, 0, s>>>(a, vecs);
     return hipGetLastError();
   }
   return hipSuccess;
