@@ -902,7 +902,7 @@ gdn_status check_linear(const gdn_linear_args* a, const char* what, bool bwd) {
   const int64_t heads = (int64_t)a->num_seqs * a->Hv, most = UINT32_MAX / 256 - 8;
   if (p.slots * a->Hv * (a->Dv == 256 ? 2 : 1) > most || (p.segmented && heads * (a->Dk * a->Dv / 1024) > most))
     return fail(GDN_E_UNSUPPORTED, large, what);
-  if (bwd && a->Hv != a->Hqk && tokens * a->Hqk * a->Dk / 1024 + p.slots * a->Hv / 4 + 2 > most)
+  if (bwd && a->Hv != a->Hqk && tokens * a->Hqk * a->Dk / 1024 + p.slots * a->Hv + 2 > most)
     return fail(GDN_E_UNSUPPORTED, "%s: B * T * Hqk * Dk is too large", what);
   return GDN_OK;
 }

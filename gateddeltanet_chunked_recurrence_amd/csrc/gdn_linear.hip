@@ -44,8 +44,8 @@
 // stores 755, so neither alone bounds it. 4 x 4,096 tokens, 16 heads of 128 x
 // 128 (268 MB): 69 us of walk, 22 and 12 of states. Gradients of 2 x 8,192 tokens: 280 us of
 // walks, which read eleven operands of 67 MB between them (738 MB; the counters see 760
-// fetched with the states, so L2 shares nothing between walks), 25, 14 and 20 of
-// states, folds and dg. A chunk of a walk takes about 6,400 cycles in the forward; dk
+// fetched with the states, so L2 shares nothing between walks), 25, 14 and 11 of
+// states, folds and dg (20 with a wave per segment for dg). A chunk of a walk takes about 6,400 cycles in the forward; dk
 // alone on the device 9,000: of these 1,950 to send loads and multiply pairs, 3,200
 // for the state's part (192 of its vector instructions make parts), 1,700 for
 // the update. Dropped: tokens 64 to a chunk (see kChunk), three workgroups per CU for the
@@ -960,16 +960,19 @@ __global__ void __launch_bounds__(kThreads) lin_fold_kernel(LinearArgs a, int bl
   else lin_fold<C, true>(a, blocks);
 }
 
-// dg of a segment's tokens, a wave per (segment, head): suffix sums over each
+// dg of a segment's tokens, a workgroup per (segment, head): suffix sums over each
 // chunk on top of <dS, S> at its end.
 template <int C>
-__device__ __forceinline__ void lin_dg(const LinearArgs& a, int units, int block) {
-  const int unit = block * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (unit >= units) return;
+__device__ __forceinline__ void lin_dg(const LinearArgs& a, int unit) {
+  static_assert(2 * C == WAVE, "a chunk per half");
+  constexpr int AHEAD = 4, EACH = 2 * AHEAD;               // chunks of a wave
+  __shared__ double moved[2][kWaves], sums[kWaves];
+  __shared__ int kept[2][kWaves];
   const int slot = unit / a.Hv, h = unit - slot * a.Hv, lane = __lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Segment seg;
   if (!lin_segment<C>(a, slot, seg)) {
-    if (a.ws_dgsum && lane == 0) a.ws_dgsum[unit] = 0.0;
+    if (a.ws_dgsum && threadIdx.x == 0) a.ws_dgsum[unit] = 0.0;
     return;
   }
   // With E = <dS, S> after a chunk, x = q . dq and y = (pairs' sums) - k . dk:
@@ -979,13 +982,15 @@ __device__ __forceinline__ void lin_dg(const LinearArgs& a, int units, int block
   // is below 2^-30, F is nothing beside either sum, and is set so: carried on as
   // the difference of two of them, it would be their roundings, which no decay
   // takes away (2.4e-6 of dg after 16 chunks, instead of 1e-6).
-  // Two chunks at a time, tokens backwards over the lanes of a half: a prefix sum
-  // over lanes is a suffix sum over tokens.
-  static_assert(2 * C == WAVE, "a chunk per half");
-  constexpr int AHEAD = 8;
+  // So over some chunks E becomes (kept ? E : 0) + moved: each wave forms these of
+  // eight chunks, then takes E from the later chunks' waves. Two chunks at a time,
+  // tokens backwards over the lanes of a half: a prefix sum over the wave is a suffix sum
+  // over both.
   const int half = lane >> 5, back = C - 1 - (lane & 31);
   double end = a.ws_end[unit], sum = 0.0;
-  for (int c0 = seg.first + seg.count - 1; c0 >= seg.first; c0 -= 2 * AHEAD) {
+  int turn = 0;
+  for (int c1 = seg.first + seg.count - 1; c1 >= seg.first; c1 -= kWaves * EACH, turn ^= 1) {
+    const int c0 = c1 - wave * EACH;
     float x[AHEAD], y[AHEAD], g[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
@@ -996,27 +1001,45 @@ __device__ __forceinline__ void lin_dg(const LinearArgs& a, int units, int block
       y[u] = here ? a.ws_kdk[at] : 0.f;
       g[u] = here ? a.g[(int64_t)(seg.bos + t) * a.gs + h] : 0.f;
     }
+    double own[AHEAD], add = 0.0;                          // own: dg without E, where E is kept up to the chunk
+    bool keep = true, still[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      const int c = c0 - 2 * u - half, t = c * C + back;
-      const bool here = c >= seg.first && t < seg.len;
       const double sx = wave_incl_scan64(x[u]), sy = wave_incl_scan64(y[u]);
       const float sg = wave_incl_scan(fmaxf(g[u], kResetGate));   // for the comparison alone
-      double e[2];
-      double at = end, bx = 0.0, by = 0.0, bg = 0.0;
+      double bx = 0.0, by = 0.0, bg = 0.0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const double tx = read_lane64(sx, 32 * i + 31), ty = read_lane64(sy, 32 * i + 31), tg = read_lane(sg, 32 * i + 31);
-        e[i] = at - bx - by;                              // the scans run on over both halves
-        at = (tg - bg < -20.8 ? 0.0 : at + (ty - by)) + (tx - bx);
+        if (half == i) {
+          own[u] = (add - bx - by) + (sx + sy);           // the scans run on over both halves
+          still[u] = keep;
+        }
+        const bool gone = tg - bg < -20.8;
+        add = (gone ? 0.0 : add + (ty - by)) + (tx - bx);
+        keep = keep && !gone;
         bx = tx;
         by = ty;
         bg = tg;
       }
-      end = at;
-      // where exp(g) is zero in FP32 nothing reaches over the token
-      const double d = g[u] < -88.f ? 0.0 : (half ? e[1] : e[0]) + (sx + sy);
-      if (here) {
+    }
+    if (lane == 0) {
+      moved[turn][wave] = add;
+      kept[turn][wave] = keep;
+    }
+    __syncthreads();
+    double in = end;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w == wave) in = end;
+      end = (kept[turn][w] ? end : 0.0) + moved[turn][w];
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int c = c0 - 2 * u - half, t = c * C + back;
+      if (c >= seg.first && t < seg.len) {
+        // where exp(g) is zero in FP32 nothing reaches over the token
+        const double d = g[u] < -88.f ? 0.0 : (still[u] ? in : 0.0) + own[u];
         if (a.ws_dgsum) sum += d;
         else a.dg[(int64_t)(seg.bos + t) * a.Hv + h] = static_cast<float>(d);
       }
@@ -1024,7 +1047,13 @@ __device__ __forceinline__ void lin_dg(const LinearArgs& a, int units, int block
   }
   if (a.ws_dgsum) {
     sum = wave_incl_scan64(sum);
-    if (lane == WAVE - 1) a.ws_dgsum[unit] = sum;
+    if (lane == WAVE - 1) sums[wave] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double all = 0.0;
+      for (int w = 0; w < kWaves; ++w) all += sums[w];
+      a.ws_dgsum[unit] = all;
+    }
   }
 }
 
@@ -1057,13 +1086,13 @@ __device__ __forceinline__ void lin_group(const LinearArgs& a, int64_t vecs, int
   Lin<T>::put4(static_cast<T*>(a.dk) + tok * a.Hqk * a.Dk + at, t);
 }
 
-// What follows the walks, in one launch: the first dg_blocks workgroups form dg, chains of
+// What follows the walks, in one launch: the first workgroups form dg, chains of
 // loads in few waves, beside those that sum heads, memory alone (apart, 2 x 515 tokens of FP32
 // 42 us and packed 4 / 16 heads of 128 x 128 207; together 38 and 200).
 template <class T>
-__global__ void __launch_bounds__(kThreads) lin_ends_kernel(LinearArgs a, int units, int dg_blocks, int64_t vecs) {
-  if ((int)blockIdx.x < dg_blocks) lin_dg<kChunk>(a, units, blockIdx.x);
-  else lin_group<T>(a, vecs, blockIdx.x - dg_blocks);
+__global__ void __launch_bounds__(kThreads) lin_ends_kernel(LinearArgs a, int units, int64_t vecs) {
+  if ((int)blockIdx.x < units) lin_dg<kChunk>(a, blockIdx.x);
+  else lin_group<T>(a, vecs, blockIdx.x - units);
 }
 
 // A kernel's grid: units, rounded up to eight, by y.
@@ -1111,10 +1140,10 @@ template <class T>
 hipError_t linear_bwd(const LinearArgs& a, hipStream_t s) {
   hipError_t e = GDN_LINEAR_DIMS(launch_walks, T);
   if (e != hipSuccess) return e;
-  const int units = a.slots * a.Hv, dg_blocks = (units + kWaves - 1) / kWaves;
-  const int64_t vecs = a.ws_dq ? (int64_t)a.tokens * a.Hqk * a.Dk / 4 : 0, blocks = dg_blocks + (vecs + kThreads - 1) / kThreads;
+  const int units = a.slots * a.Hv;
+  const int64_t vecs = a.ws_dq ? (int64_t)a.tokens * a.Hqk * a.Dk / 4 : 0, blocks = units + (vecs + kThreads - 1) / kThreads;
   if (blocks > 0) {
-    lin_ends_kernel<T><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a, units, dg_blocks, vecs);
+    lin_ends_kernel<T><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a, units, vecs);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.ws_dgsum) {
