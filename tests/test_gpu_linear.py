@@ -317,3 +317,30 @@ def test_outputs_in_the_inputs_memory_are_refused():
     out = dict(dq=torch.empty_like(d['q']), dk=torch.empty_like(d['k']), dv=d['do'], dg=torch.empty_like(d['g']))
     with pytest.raises(G.GdnError, match='dv overlaps do'):
         G.gdn_linear_bwd(d['q'], d['k'], d['v'], d['g'], d['do'], out=out)
+
+
+@pytest.mark.parametrize('gate', ['slow', 'reset', 'head'])
+@pytest.mark.parametrize('T', [1024, 1025, 2208])
+def test_dg_of_long_segments(gate, T):
+    """32, 33 and 69 chunks in one segment: 256 equal heads fill the device, so sequences
+    stay whole. Bound: a product passes fewer than 2,300 sums of 2^-24 each, 2^-12.8, and
+    two split factors, 2^-15: under 2^-12 of the suffix sum of the absolute dots."""
+    H = 256
+    x, d, _ = make('bf16', 1, T, None, 1, 1, 64, 64, gate if gate != 'slow' else 'token', seed=11)
+    if gate == 'slow':
+        x['g'] = x['g'].float().mul(2.0 ** -8).double()
+    else:
+        x['g'] = x['g'].float().double()
+    g = x['g'].float().cuda()
+    wide = {n: d[n].repeat_interleave(H, 1 if n in ('h0', 'dht') else 2) for n in ('q', 'k', 'v', 'do', 'h0', 'dht')}
+    g = g.repeat_interleave(H, g.dim() - 1)
+    got = G.gdn_linear_bwd(wide['q'], wide['k'], wide['v'], g, wide['do'], wide['dht'], h0=wide['h0'])['dg']
+    scale = 64 ** -0.5
+    want = linear_bwd(x['q'], x['k'], x['v'], x['g'], scale, x['do'], x['dht'], x['h0'])['dg']
+    mag = positive(x)
+    top = linear_bwd(mag['q'], mag['k'], mag['v'], mag['g'], scale, mag['do'], mag['dht'], mag['h0'])
+    dots = sum((mag[n] * top['d' + n]).sum(-1) for n in ('q', 'k'))
+    sums = dots.flip(1).cumsum(1).flip(1)
+    bound = (sums.sum((0, 1)) if gate == 'head' else sums + top['dg'].abs()) * 2.0 ** -12 + 1e-30
+    assert torch.equal(got, got[..., :1].expand_as(got))                # equal heads, equal bits
+    within('dg', got[..., -1:], want, bound)
