@@ -909,7 +909,7 @@ gdn_status check_linear(const gdn_linear_args* a, const char* what, bool bwd) {
 
 // Offsets of the workspace's parts.
 struct LinearWs {
-  int64_t state = 0, dstate = 0, decay = 0, qdq = 0, kdk = 0, end = 0, dgsum = 0, dq = 0, dk = 0, total = 0;
+  int64_t state = 0, dstate = 0, decay = 0, qdq = 0, kdk = 0, end = 0, begin = 0, dgsum = 0, dq = 0, dk = 0, total = 0;
 };
 LinearWs linear_ws(const gdn_linear_args* a, const gdn::LinearPlan& p, bool bwd) {
   LinearWs w;
@@ -928,6 +928,7 @@ LinearWs linear_ws(const gdn_linear_args* a, const gdn::LinearPlan& p, bool bwd)
     part(w.qdq, dots);
     part(w.kdk, dots);
     part(w.end, sh * 4);
+    if (a->h0) part(w.begin, (int64_t)a->num_seqs * a->Hv * 4);
     if (a->g_per_head) part(w.dgsum, std::max<int64_t>(sh, 1) * 8);   // present without a sequence too: dg is 0
     if (a->Hv != a->Hqk) {
       const int64_t parts = (int64_t)a->B * a->T * a->Hv * a->Dk * 4;
@@ -961,6 +962,7 @@ gdn::LinearArgs linear_args(const gdn_linear_args* a, const gdn::LinearPlan& p, 
     k.ws_qdq = at(w.qdq);
     k.ws_kdk = at(w.kdk);
     k.ws_end = at(w.end);
+    if (a->h0) k.ws_begin = at(w.begin);
     if (a->g_per_head) k.ws_dgsum = reinterpret_cast<double*>(b + w.dgsum);
     if (a->Hv != a->Hqk) {
       k.ws_dq = at(w.dq);

@@ -374,6 +374,7 @@ struct LinearArgs {
   float* ws_qdq;              // [chunk slots, Hv, C] q . dq, the state's part
   float* ws_kdk;              // same, the pairs' row minus column sums minus k . dk of the state's part
   float* ws_end;              // [slots, Hv] <dS, S> at the segment's end
+  float* ws_begin;            // [N, Hv] <dS, S> at the sequence's start, with h0 only
   double* ws_dgsum;           // [slots, Hv], one gate per head only
   float* ws_dq;               // [tokens, Hv, Dk] per value head, where heads share q and k
   float* ws_dk;

@@ -17,7 +17,7 @@
 //   dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <dS, S'>,
 // where pairs (i, j) of one chunk enter as row and column sums of M = P * dP, the
 // reads and writes of states as q . dq and k . dk of the state's part alone, and
-// <dS, S'> is taken from both states at the end of each segment and carried
+// <dS, S'> is taken from both states at both ends of each segment and carried
 // from chunk to chunk by these sums. So dg has no rounded product in it.
 //
 // A walk is sequential in its chunks. Where the heads alone do not fill the
@@ -31,7 +31,9 @@
 // states that q . dq and k . dk come from, enter the matrix cores as three bf16 parts
 // (24 bits); the pairs' products as two. So bf16 outputs are off by their own rounding
 // (1.7e-3 of their norm; with one part for the pairs 2.3e-3 for 1 to 3% less time), ht and
-// dh0 by 1e-7 (two parts: 2e-6, and dg 5e-6 to 2e-5, for 5% less).
+// dh0 by 1e-7 (two parts: 2e-6, and dg 5e-6 to 2e-5, for 5% less), dg by 3e-7 to 8e-7;
+// with a decay per head, where what its tokens are off by adds up and they cancel, by
+// 1e-7 to 3e-6 (8e-6 where one head is all there is).
 //
 // Layout: four waves, each with 16 or 32 columns of the state, which stays in
 // accumulators from chunk to chunk: its tiles are operands for the outputs as they
@@ -851,9 +853,13 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
   if constexpr (STATE) {
     if (threadIdx.x == 0 && slab == 0) a.ws_decay[slot_head] = fexp2(static_cast<float>(far_total));
   }
-  if constexpr (ROLE == kDq) {
-    // <dS, S> at the segment's end
-    const float* other = a.ws_dstate ? a.ws_dstate + slot_head * elems : a.dht ? a.dht + seq_head * elems : nullptr;
+  if constexpr (ROLE == kDk) {
+    if (!a.h0 || seg.s != 0) return;
+  }
+  if constexpr (ROLE == kDq || ROLE == kDk) {
+    // <dS, S> at the segment's end; at the sequence's start
+    const float* other = ROLE == kDk ? a.h0 + seq_head * elems
+                         : a.ws_dstate ? a.ws_dstate + slot_head * elems : a.dht ? a.dht + seq_head * elems : nullptr;
     float dot = 0.f;
     if (other) {
 #pragma unroll
@@ -869,7 +875,7 @@ __device__ __forceinline__ void lin_walk(const LinearArgs& a, int slot, int h, i
     lds_barrier();
     if (lane == 0) dots[wave] = dot;
     lds_barrier();
-    if (threadIdx.x == 0) a.ws_end[slot_head] = (dots[0] + dots[1]) + (dots[2] + dots[3]);
+    if (threadIdx.x == 0) (ROLE == kDk ? a.ws_begin[seq_head] : a.ws_end[slot_head]) = (dots[0] + dots[1]) + (dots[2] + dots[3]);
   }
 }
 
@@ -987,8 +993,16 @@ __device__ __forceinline__ void lin_dg(const LinearArgs& a, int unit) {
   // tokens backwards over the lanes of a half: a prefix sum over the wave is a suffix sum
   // over both.
   const int half = lane >> 5, back = C - 1 - (lane & 31);
-  double end = a.ws_end[unit], sum = 0.0;
+  double end = a.ws_end[unit], sum = 0.0, parts = 0.0;
   int turn = 0;
+  // E is known at the segment's start too. What the walk through the chunks misses it by
+  // (their roundings, summed) is taken off along the way, in proportion to the tokens: 0.7e-6 of
+  // dg instead of 1.3e-6 with decays of 0.9 to 1 and 32 chunks. Not where a chunk lets nothing through, which takes the roundings too.
+  bool linked = true;
+  const double before = seg.s > 0 ? a.ws_end[unit - a.Hv] : a.h0 ? a.ws_begin[(int64_t)seg.n * a.Hv + h] : 0.0;
+  const int t1 = min((seg.first + seg.count) * C, seg.len);
+  const double per = 1.0 / (t1 - seg.first * C);
+  const bool once = seg.count <= kWaves * EACH;
   for (int c1 = seg.first + seg.count - 1; c1 >= seg.first; c1 -= kWaves * EACH, turn ^= 1) {
     const int c0 = c1 - wave * EACH;
     float x[AHEAD], y[AHEAD], g[AHEAD];
@@ -1033,17 +1047,31 @@ __device__ __forceinline__ void lin_dg(const LinearArgs& a, int unit) {
     for (int w = 0; w < kWaves; ++w) {
       if (w == wave) in = end;
       end = (kept[turn][w] ? end : 0.0) + moved[turn][w];
+      linked = linked && kept[turn][w];
     }
+    const double off = once && linked ? (before - end) * per : 0.0;
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const int c = c0 - 2 * u - half, t = c * C + back;
       if (c >= seg.first && t < seg.len) {
         // where exp(g) is zero in FP32 nothing reaches over the token
-        const double d = g[u] < -88.f ? 0.0 : (still[u] ? in : 0.0) + own[u];
+        const double d = g[u] < -88.f ? 0.0 : (still[u] ? in : 0.0) + own[u] + off * (t1 - t);
+        parts += t1 - t;
         if (a.ws_dgsum) sum += d;
         else a.dg[(int64_t)(seg.bos + t) * a.Hv + h] = static_cast<float>(d);
       }
     }
+  }
+  if (!once && linked) {
+    const double off = (before - end) * per;
+    if (a.ws_dgsum) sum += off * parts;
+    else
+      for (int c0 = seg.first + seg.count - 1 - wave * EACH; c0 >= seg.first; c0 -= kWaves * EACH)
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int c = c0 - 2 * u - half, t = c * C + back;
+          if (c >= seg.first && t < seg.len) a.dg[(int64_t)(seg.bos + t) * a.Hv + h] += static_cast<float>(off * (t1 - t));
+        }
   }
   if (a.ws_dgsum) {
     sum = wave_incl_scan64(sum);
